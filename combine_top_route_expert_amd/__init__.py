@@ -27,7 +27,8 @@ __all__ = [
     "MOE_SCHEDULE_PAIR_FUSED", "MOE_SCHEDULE_PER_CHUNK", "MOE_SCHEDULE_PAIR_FUSED_PREFETCH",
     "MOE_SCHEDULE_EXPERT_HALVES",
     "EXPORTED_SYMBOLS",
-    "moe_chunked_forward_noalloc",
+    "moe_chunked_forward_noalloc", "moe_layer_norm", "moe_layer_norm_quantize",
+    "moe_layer_norm_backward_workspace_size", "moe_layer_norm_backward", "moe_quantize_rows",
 ]
 
 MOE_F32, MOE_BF16 = 0, 1
@@ -44,6 +45,8 @@ EXPORTED_SYMBOLS = (
     "moe_chunked_forward", "moe_chunked_forward_schedule", "moe_chunked_forward_noalloc",
     "moe_backward_workspace_size",
     "moe_chunked_backward", "moe_unpermute_combine_backward", "moe_permute_backward",
+    "moe_layer_norm", "moe_layer_norm_quantize", "moe_layer_norm_backward_workspace_size",
+    "moe_layer_norm_backward", "moe_quantize_rows",
 )
 
 
@@ -144,6 +147,16 @@ def load_library() -> ctypes.CDLL:
         "moe_unpermute_combine_backward": (ctypes.c_int, [_SP, ctypes.c_int32, _P, _P, _P, _P,
                                                           _P, _P, _P]),
         "moe_permute_backward": (ctypes.c_int, [_SP, ctypes.c_int32, _P, _P, _P, _P]),
+        "moe_layer_norm": (ctypes.c_int, [_SP, _P, _P, _P, _P, ctypes.c_float, _P, _P, _P, _P,
+                                          _P]),
+        "moe_layer_norm_quantize": (ctypes.c_int, [_SP, _P, _P, _P, _P, ctypes.c_float, _P, _P,
+                                                   _P, _P, _P]),
+        "moe_layer_norm_backward_workspace_size": (ctypes.c_int,
+                                                   [_SP, ctypes.POINTER(ctypes.c_size_t)]),
+        "moe_layer_norm_backward": (ctypes.c_int, [_SP, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P,
+                                                   ctypes.c_size_t, _P]),
+        "moe_quantize_rows": (ctypes.c_int, [ctypes.c_int64, ctypes.c_int64, ctypes.c_int32, _P,
+                                             _P, _P, _P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -450,3 +463,92 @@ def moe_permute_backward(shape: moe_shape, chunk: int, grad_x_perm, dst_row, gra
         ctypes.byref(shape), chunk, _ptr(grad_x_perm, dt, rows * shape.H, "grad_x_perm"),
         _ptr(dst_row, torch.int32, shape.T * shape.k, "dst_row"),
         _ptr(grad_hidden, dt, shape.T * shape.H, "grad_hidden"), _stream(stream)))
+
+
+# ---------------------------------------------------------------- layer norm, row quantisation
+class _OnDevice:
+    """Pointers of one call's tensors, which must all live on one device; the call is made with
+    that device current, on the given stream or the device's current one."""
+
+    def __init__(self):
+        self.device = None
+
+    def __call__(self, t, dtype, min_numel: int, name: str) -> Optional[int]:
+        p = _ptr(t, dtype, min_numel, name)
+        if t is not None:
+            if self.device is None:
+                self.device = t.device
+            elif t.device != self.device:
+                raise ValueError(f"{name} is on {t.device}, the tensors before it on {self.device}")
+        return p
+
+    def optional(self, t, dtype, min_numel: int, name: str) -> Optional[int]:
+        return None if t is None else self(t, dtype, min_numel, name)
+
+    def call(self, fn: str, stream, *args) -> None:
+        dev = self.device
+        if isinstance(stream, torch.cuda.Stream) and dev is not None and stream.device != dev:
+            raise ValueError(f"stream is on {stream.device}, the tensors on {dev}")
+        f = getattr(load_library(), fn)
+        if dev is None or dev.index == torch.cuda.current_device():
+            _check(fn, f(*args, _stream(stream)))
+        else:
+            with torch.cuda.device(dev):
+                _check(fn, f(*args, _stream(stream)))
+
+
+def moe_layer_norm(shape: moe_shape, x, residual, weight, bias, eps: float, sum_out, y, mean=None,
+                   rstd=None, stream=None) -> None:
+    """y = layer norm of x (or of x + residual, which goes to sum_out); weight, bias, mean and rstd
+    are float32 and may be None."""
+    on, dt, f32, n = _OnDevice(), shape.torch_dtype, torch.float32, shape.T * shape.H
+    on.call("moe_layer_norm", stream, ctypes.byref(shape), on(x, dt, n, "x"),
+            on.optional(residual, dt, n, "residual"), on.optional(weight, f32, shape.H, "weight"),
+            on.optional(bias, f32, shape.H, "bias"), eps, on.optional(sum_out, dt, n, "sum"),
+            on(y, dt, n, "y"), on.optional(mean, f32, shape.T, "mean"),
+            on.optional(rstd, f32, shape.T, "rstd"))
+
+
+def moe_layer_norm_quantize(shape: moe_shape, x, residual, weight, bias, eps: float, sum_out, y, q,
+                            scale, stream=None) -> None:
+    """moe_layer_norm whose rows are also quantised into q (int8) and scale; y may be None."""
+    on, dt, f32, n = _OnDevice(), shape.torch_dtype, torch.float32, shape.T * shape.H
+    on.call("moe_layer_norm_quantize", stream, ctypes.byref(shape), on(x, dt, n, "x"),
+            on.optional(residual, dt, n, "residual"), on.optional(weight, f32, shape.H, "weight"),
+            on.optional(bias, f32, shape.H, "bias"), eps, on.optional(sum_out, dt, n, "sum"),
+            on.optional(y, dt, n, "y"), on(q, torch.int8, n, "q"), on(scale, f32, shape.T, "scale"))
+
+
+def moe_layer_norm_backward_workspace_size(shape: moe_shape) -> int:
+    b = ctypes.c_size_t()
+    _check("moe_layer_norm_backward_workspace_size",
+           load_library().moe_layer_norm_backward_workspace_size(ctypes.byref(shape),
+                                                                 ctypes.byref(b)))
+    return b.value
+
+
+def moe_layer_norm_backward(shape: moe_shape, grad_y, x, weight, mean, rstd, grad_sum, grad_x,
+                            grad_weight=None, grad_bias=None, ws=None, stream=None) -> None:
+    """Gradient of moe_layer_norm: x holds the normalised rows (sum_out where there was a
+    residual); grad_sum, grad_weight and grad_bias may be None."""
+    on, dt, f32, n = _OnDevice(), shape.torch_dtype, torch.float32, shape.T * shape.H
+    args = (on(grad_y, dt, n, "grad_y"), on(x, dt, n, "x"),
+            on.optional(weight, f32, shape.H, "weight"), on(mean, f32, shape.T, "mean"),
+            on(rstd, f32, shape.T, "rstd"), on.optional(grad_sum, dt, n, "grad_sum"),
+            on(grad_x, dt, n, "grad_x"), on.optional(grad_weight, f32, shape.H, "grad_weight"),
+            on.optional(grad_bias, f32, shape.H, "grad_bias"))
+    params = grad_weight is not None or grad_bias is not None
+    need = moe_layer_norm_backward_workspace_size(shape) if params else 0
+    wp = on(ws, torch.uint8, need, "ws")
+    on.call("moe_layer_norm_backward", stream, ctypes.byref(shape), *args, wp,
+            0 if ws is None else ws.numel())
+
+
+def moe_quantize_rows(rows: int, cols: int, dtype: str, x, q, scale, stream=None) -> None:
+    """Rows of x ("bf16" or "f32") as int8 q with one float32 scale each."""
+    if dtype not in ("bf16", "f32"):
+        raise ValueError(f"dtype must be 'bf16' or 'f32', got {dtype!r}")
+    on, bf16 = _OnDevice(), dtype == "bf16"
+    on.call("moe_quantize_rows", stream, rows, cols, MOE_BF16 if bf16 else MOE_F32,
+            on(x, torch.bfloat16 if bf16 else torch.float32, rows * cols, "x"),
+            on(q, torch.int8, rows * cols, "q"), on(scale, torch.float32, rows, "scale"))

@@ -904,4 +904,98 @@ moe_status moe_chunked_forward(const moe_shape* shape, const void* hidden_states
                                       MOE_SCHEDULE_PAIR_FUSED);
 }
 
+namespace moe {
+namespace {
+
+// Checks shared by the layer-norm entry points: the shape, its width, and that
+// [T][H] arrays and parameters are usable.
+moe_status norm_shape(const moe_shape* shape, Shape* s) {
+  const moe_status st = resolve_shape(shape, s);
+  if (st != MOE_OK) return st;
+  return s->H > kNormMaxHidden ? MOE_ERR_UNSUPPORTED : MOE_OK;
+}
+
+moe_status norm_args(const Shape& s, const NormIO& io) {
+  if (!(io.eps > 0.0f) || io.eps > 3.0e38f) return MOE_ERR_INVALID_ARG;
+  if ((io.residual == nullptr) != (io.sum == nullptr)) return MOE_ERR_INVALID_ARG;
+  if (s.T > 0 && !io.x) return MOE_ERR_INVALID_ARG;
+  if (!aligned(io.x, 16) || !aligned(io.residual, 16) || !aligned(io.sum, 16) ||
+      !aligned(io.y, 16) || !aligned(io.weight, 4) || !aligned(io.bias, 4) ||
+      !aligned(io.mean, 4) || !aligned(io.rstd, 4) || !aligned(io.scale, 4) || !aligned(io.q, 16))
+    return MOE_ERR_INVALID_ARG;
+  return MOE_OK;
+}
+
+}  // namespace
+}  // namespace moe
+
+moe_status moe_quantize_rows(int64_t rows, int64_t cols, int32_t dtype, const void* x, int8_t* q,
+                             float* scale, hipStream_t stream) {
+  if (rows < 0 || cols < 1 || (dtype != MOE_F32 && dtype != MOE_BF16)) return MOE_ERR_INVALID_ARG;
+  if (cols % (dtype == MOE_BF16 ? 8 : 4)) return MOE_ERR_UNSUPPORTED;
+  if (rows == 0) return MOE_OK;
+  if (!x || !q || !scale) return MOE_ERR_INVALID_ARG;
+  if (!aligned(x, 16) || !aligned(q, 16) || !aligned(scale, 4)) return MOE_ERR_INVALID_ARG;
+  return hip_status(launch_quantize_rows(rows, cols, dtype == MOE_BF16, x, q, scale, nullptr,
+                                         nullptr, stream));
+}
+
+moe_status moe_layer_norm(const moe_shape* shape, const void* x, const void* residual,
+                          const float* weight, const float* bias, float eps, void* sum, void* y,
+                          float* mean, float* rstd, hipStream_t stream) {
+  Shape s;
+  moe_status st = norm_shape(shape, &s);
+  if (st != MOE_OK) return st;
+  const NormIO io{x, residual, weight, bias, eps, sum, y, mean, rstd, nullptr, nullptr};
+  st = norm_args(s, io);
+  if (st != MOE_OK || s.T == 0) return st;
+  if (!y) return MOE_ERR_INVALID_ARG;
+  return hip_status(launch_layer_norm(s, io, stream));
+}
+
+moe_status moe_layer_norm_quantize(const moe_shape* shape, const void* x, const void* residual,
+                                   const float* weight, const float* bias, float eps, void* sum,
+                                   void* y, int8_t* q, float* scale, hipStream_t stream) {
+  Shape s;
+  moe_status st = norm_shape(shape, &s);
+  if (st != MOE_OK) return st;
+  const NormIO io{x, residual, weight, bias, eps, sum, y, nullptr, nullptr, q, scale};
+  st = norm_args(s, io);
+  if (st != MOE_OK || s.T == 0) return st;
+  if (!q || !scale) return MOE_ERR_INVALID_ARG;
+  return hip_status(launch_layer_norm(s, io, stream));
+}
+
+moe_status moe_layer_norm_backward_workspace_size(const moe_shape* shape, size_t* bytes) {
+  Shape s;
+  const moe_status st = norm_shape(shape, &s);
+  if (st != MOE_OK) return st;
+  if (!bytes) return MOE_ERR_INVALID_ARG;
+  *bytes = align256(norm_grad_partial_bytes(s));
+  return MOE_OK;
+}
+
+moe_status moe_layer_norm_backward(const moe_shape* shape, const void* grad_y, const void* x,
+                                   const float* weight, const float* mean, const float* rstd,
+                                   const void* grad_sum, void* grad_x, float* grad_weight,
+                                   float* grad_bias, void* ws, size_t ws_bytes,
+                                   hipStream_t stream) {
+  Shape s;
+  const moe_status st = norm_shape(shape, &s);
+  if (st != MOE_OK) return st;
+  if (s.T > 0 && (!grad_y || !x || !mean || !rstd || !grad_x)) return MOE_ERR_INVALID_ARG;
+  if (!aligned(grad_y, 16) || !aligned(x, 16) || !aligned(weight, 4) || !aligned(mean, 4) ||
+      !aligned(rstd, 4) || !aligned(grad_sum, 16) || !aligned(grad_x, 16) ||
+      !aligned(grad_weight, 16) || !aligned(grad_bias, 16) || !aligned(ws, 256))
+    return MOE_ERR_INVALID_ARG;
+  const bool params = grad_weight || grad_bias;
+  if (params && s.T > 0) {
+    if (!ws) return MOE_ERR_INVALID_ARG;
+    if (ws_bytes < norm_grad_partial_bytes(s)) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  }
+  const NormGradIO io{grad_y, x,      weight,      mean,      rstd,
+                      grad_sum, grad_x, grad_weight, grad_bias, params ? (float*)ws : nullptr};
+  return hip_status(launch_layer_norm_backward(s, io, stream));
+}
+
 }  // extern "C"

@@ -92,6 +92,37 @@ hipError_t launch_combine_pair(const Shape& s, int t0, int t_mid, int t1, const 
                                const void* y1, const int32_t* dst_row, const float* w,
                                void* out, hipStream_t st);
 
+// ---- layer norm and row quantisation (norm_quantize.hip) ----------------------
+constexpr int kNormMaxHidden = 16384;  // widest row the layer-norm kernels hold in registers
+struct NormIO {
+  const void* x;
+  const void* residual;   // optional: rows are rd(x + residual), written to sum
+  const float *weight, *bias;  // [H], each optional (1 and 0)
+  float eps;
+  void* sum;              // [T][H] (with residual; may alias x or residual)
+  void* y;                // [T][H], optional in the quantising form
+  float *mean, *rstd;     // [T], each optional (plain form)
+  int8_t* q;              // [T][H] and [T] (quantising form), or null
+  float* scale;
+};
+hipError_t launch_layer_norm(const Shape& s, const NormIO& io, hipStream_t st);
+struct NormGradIO {
+  const void *grad_y, *x;      // [T][H]; x: the rows the statistics belong to
+  const float* weight;         // [H], optional
+  const float *mean, *rstd;    // [T]
+  const void* grad_sum;        // [T][H], optional: added to grad_x
+  void* grad_x;                // [T][H]
+  float *grad_weight, *grad_bias;  // [H], each optional
+  float* partials;             // norm_grad_partial_bytes(s), when either is wanted
+};
+size_t norm_grad_partial_bytes(const Shape& s);
+hipError_t launch_layer_norm_backward(const Shape& s, const NormGradIO& io, hipStream_t st);
+// Rows [0, rows) of x, or only the first *valid0 + *valid1 of them (device
+// counts, each optional); the others are left as they are.
+hipError_t launch_quantize_rows(int64_t rows, int64_t cols, bool bf16, const void* x, int8_t* q,
+                                float* scale, const int32_t* valid0, const int32_t* valid1,
+                                hipStream_t st);
+
 // ---- weight warm-up (prefetch.hip) -------------------------------------------
 // Reads the first head_bytes (a multiple of 16) of each of `rows` rows of
 // row_bytes so they sit in the caches; writes nothing but, at most, *sink.
@@ -168,6 +199,28 @@ hipError_t launch_down_f32(const Shape& s, const GroupedIO& io, const void* w_do
                            hipStream_t st);
 
 // ---- small device helpers ----------------------------------------------------
+// A 16-byte vector of a row: eight bf16 or four fp32 elements.
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+__device__ __forceinline__ void unpack_bf16x8(const u32x4& q, float* f) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = __uint_as_float(q[i] << 16);
+    f[2 * i + 1] = __uint_as_float(q[i] & 0xffff0000u);
+  }
+}
+
+__device__ __forceinline__ u32x4 pack_bf16x8(const float* f) {
+  u32x4 q;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    __bf16 lo = (__bf16)f[2 * i], hi = (__bf16)f[2 * i + 1];
+    q[i] = (uint32_t)__builtin_bit_cast(uint16_t, lo) |
+           ((uint32_t)__builtin_bit_cast(uint16_t, hi) << 16);
+  }
+  return q;
+}
+
 __device__ __forceinline__ uint64_t lanemask_lt() {
   return (1ull << __lane_id()) - 1ull;
 }

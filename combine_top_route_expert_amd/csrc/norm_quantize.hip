@@ -1,0 +1,596 @@
+// Layer norm of the layer's input rows (forward, backward, and a form that also
+// quantises its rows to 8-bit integers) and the row quantiser by itself.
+//
+//   s = rd(x + residual)           (or x), rd: rounding to the layer's dtype
+//   y = (s - mean) * rstd * weight + bias,  mean and rstd over the row's H values
+//   backward, with xh = (s - mean) rstd and h = grad_y weight:
+//     grad_x = rstd (h - mean_H(h) - xh mean_H(h xh)) [+ grad_sum]
+//     grad_weight = sum_t grad_y xh,  grad_bias = sum_t grad_y
+//   quantise: a = max |row|, scale = a / 127, q = rne(127 row / a)
+//
+// All of it is bound by memory: a row is read once, held in registers as fp32
+// while its statistics are reduced, and written once.  The variance is the
+// mean of the squared distances from the mean (a second pass over registers),
+// so a large common offset costs no precision.
+//
+// A row is a wave's (up to 2048 values: four rows to a workgroup, no barrier)
+// or a workgroup's.  Threads take 16-byte vectors round robin, so every load and
+// store of a wave is one contiguous kilobyte.
+#include <algorithm>
+#include <type_traits>
+
+#include "moe_internal.h"
+
+namespace moe {
+
+namespace {
+
+template <bool kBf16>
+constexpr int kVecEl = kBf16 ? 8 : 4;  // elements of a 16-byte vector
+
+template <bool kBf16>
+__device__ __forceinline__ void unpack(const u32x4& q, float* f) {
+  if constexpr (kBf16) {
+    unpack_bf16x8(q, f);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = __uint_as_float(q[i]);
+  }
+}
+
+template <bool kBf16>
+__device__ __forceinline__ u32x4 pack(const float* f) {
+  if constexpr (kBf16) {
+    return pack_bf16x8(f);
+  } else {
+    return u32x4{__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
+                 __float_as_uint(f[3])};
+  }
+}
+
+__device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+  for (int d = 32; d > 0; d >>= 1) v += __shfl_xor(v, d);
+  return v;
+}
+
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
+#pragma unroll
+  for (int d = 32; d > 0; d >>= 1) {
+    const uint32_t o = __shfl_xor(v, d);
+    v = o > v ? o : v;
+  }
+  return v;
+}
+
+// Reductions over the THREADS threads of a row; `red` is a slot of THREADS / 64
+// words used by no other reduction that a barrier does not separate.  Every
+// thread gets the same bits.
+template <int THREADS>
+__device__ __forceinline__ float row_sum(float v, float* red) {
+  v = wave_sum(v);
+  if constexpr (THREADS > 64) {
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+    __syncthreads();
+    v = red[0];
+#pragma unroll
+    for (int w = 1; w < THREADS / 64; ++w) v += red[w];
+  }
+  return v;
+}
+
+template <int THREADS>
+__device__ __forceinline__ uint32_t row_max(uint32_t v, uint32_t* red) {
+  v = wave_max(v);
+  if constexpr (THREADS > 64) {
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+    __syncthreads();
+    v = red[0];
+#pragma unroll
+    for (int w = 1; w < THREADS / 64; ++w) v = red[w] > v ? red[w] : v;
+  }
+  return v;
+}
+
+// One row's quantiser, from the bits of its largest magnitude (as an unsigned
+// number these order finite < infinity < NaN, so one maximum finds all three).
+//
+// q must be rne of the exact quotient 127 x / a: a rounded quotient can land on
+// the other side of a tie.  bf16 rows: 127 x is exact in fp32, the residual of
+// the approximate quotient is exact too (24 + 8 bits, of which all but the last
+// few cancel), and one correction step gives the quotient to within far less
+// than half a unit of any representable tie.  fp32 rows take the same steps in
+// fp64.  Rows whose largest magnitude is beyond 2^+-64 are scaled by a power of
+// two first, so neither 127 x nor 1 / a leaves the range.  A row that holds an
+// infinity or a NaN has no quotient: q = 0 and a NaN scale, so every product
+// with it is NaN.
+template <bool kBf16>
+struct RowQuantizer {
+  typedef std::conditional_t<kBf16, float, double> real;
+  float scale;
+  real a, r, lift;  // lift: 127 times the power of two
+  bool finite;
+
+  __device__ __forceinline__ explicit RowQuantizer(uint32_t max_bits) {
+    finite = max_bits < 0x7f800000u;
+    const float m = __uint_as_float(max_bits);
+    scale = finite ? m / 127.0f : __uint_as_float(0x7fc00000u);
+    real p = 1;
+    if constexpr (kBf16) p = m > 0x1p64f ? 0x1p-64f : m < 0x1p-64f ? 0x1p64f : 1.0f;
+    a = (real)m * p;
+    r = finite && max_bits != 0 ? (real)1 / a : (real)0;
+    lift = (real)127 * p;
+  }
+  __device__ __forceinline__ uint32_t operator()(float x) const {
+    const real n = (real)x * lift;
+    real q = n * r;
+    if constexpr (kBf16)
+      q = rintf(__builtin_fmaf(__builtin_fmaf(-q, a, n), r, q));
+    else
+      q = rint(__builtin_fma(__builtin_fma(-q, a, n), r, q));
+    return finite ? (uint32_t)(int)q & 0xffu : 0u;
+  }
+  // kVecEl quantised elements of a vector as one 8- or 4-byte store
+  __device__ __forceinline__ void store(const float* f, int8_t* q, int64_t v) const {
+    constexpr int W = kVecEl<kBf16> / 4;
+    uint32_t o[W];
+#pragma unroll
+    for (int i = 0; i < W; ++i)
+      o[i] = (*this)(f[4 * i]) | (*this)(f[4 * i + 1]) << 8 | (*this)(f[4 * i + 2]) << 16 |
+             (*this)(f[4 * i + 3]) << 24;
+    typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+    if constexpr (W == 2)
+      *(u32x2*)(q + v * 8) = u32x2{o[0], o[1]};
+    else
+      *(uint32_t*)(q + v * 4) = o[0];
+  }
+};
+
+template <int N>
+__device__ __forceinline__ uint32_t max_magnitude(const float* f, uint32_t m) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const uint32_t b = __float_as_uint(f[i]) & 0x7fffffffu;
+    m = b > m ? b : m;
+  }
+  return m;
+}
+
+// kEl consecutive floats of a [H] parameter, or `none` where there is none.
+template <int kEl>
+__device__ __forceinline__ void load_param(const float* p, int64_t v, float none, float* f) {
+#pragma unroll
+  for (int i = 0; i < kEl; ++i) f[i] = p ? p[v * kEl + i] : none;
+}
+
+// A row: THREADS threads of EPT values each.
+template <int THREADS>
+struct RowOf {
+  static constexpr int kPerGroup = THREADS == 64 ? 4 : 1;
+  static constexpr int kGroup = THREADS == 64 ? 256 : THREADS;  // workgroup size
+  static __device__ __forceinline__ int tid() {
+    return THREADS == 64 ? (int)threadIdx.x & 63 : (int)threadIdx.x;
+  }
+  static __device__ __forceinline__ int64_t row() {
+    return THREADS == 64 ? (int64_t)blockIdx.x * kPerGroup + (threadIdx.x >> 6)
+                         : (int64_t)blockIdx.x;
+  }
+  static dim3 grid(int64_t rows) { return dim3((unsigned)((rows + kPerGroup - 1) / kPerGroup)); }
+};
+
+// Rows of one launch: a launch holds fewer than 2^32 threads, and a row takes
+// at most 1024 of them.  More rows go in several launches.
+constexpr int64_t kRowsPerLaunch = 1 << 21;
+
+template <bool kBf16, int THREADS, int EPT, bool kQuant>
+__global__ void __launch_bounds__(RowOf<THREADS>::kGroup) norm_rows(NormIO io, int64_t row0, int64_t rows,
+                                                                     int nvec) {
+  constexpr int kEl = kVecEl<kBf16>, VPT = EPT / kEl, NW = THREADS / 64;
+  const int64_t row = row0 + RowOf<THREADS>::row();
+  if (row >= rows) return;
+  __shared__ float red[3][NW];
+  const int tid = RowOf<THREADS>::tid();
+  const u32x4* x = (const u32x4*)io.x + row * nvec;
+  u32x4 xv[VPT], rv[VPT];
+#pragma unroll
+  for (int i = 0; i < VPT; ++i)
+    if (i * THREADS + tid < nvec) xv[i] = x[i * THREADS + tid];
+  if (io.residual) {
+    const u32x4* r = (const u32x4*)io.residual + row * nvec;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i)
+      if (i * THREADS + tid < nvec) rv[i] = r[i * THREADS + tid];
+  }
+  float f[VPT][kEl];
+  float total = 0.0f;
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int v = i * THREADS + tid;
+    if (v >= nvec) continue;
+    unpack<kBf16>(xv[i], f[i]);
+    if (io.residual) {
+      float g[kEl];
+      unpack<kBf16>(rv[i], g);
+#pragma unroll
+      for (int e = 0; e < kEl; ++e) f[i][e] += g[e];
+      // the sum is what later layers read: its statistics are those of the
+      // rounded values
+      const u32x4 p = pack<kBf16>(f[i]);
+      ((u32x4*)io.sum)[row * nvec + v] = p;
+      unpack<kBf16>(p, f[i]);
+    }
+#pragma unroll
+    for (int e = 0; e < kEl; ++e) total += f[i][e];
+  }
+  const float h = (float)(nvec * kEl);
+  const float mean = row_sum<THREADS>(total, red[0]) / h;
+  float sq = 0.0f;
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    if (i * THREADS + tid >= nvec) continue;
+#pragma unroll
+    for (int e = 0; e < kEl; ++e) {
+      f[i][e] -= mean;
+      sq = __builtin_fmaf(f[i][e], f[i][e], sq);
+    }
+  }
+  const float rstd = 1.0f / sqrtf(row_sum<THREADS>(sq, red[1]) / h + io.eps);
+  if (tid == 0) {
+    if (io.mean) io.mean[row] = mean;
+    if (io.rstd) io.rstd[row] = rstd;
+  }
+  uint32_t big = 0;
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int v = i * THREADS + tid;
+    if (v >= nvec) continue;
+    float w[kEl], b[kEl];
+    load_param<kEl>(io.weight, v, 1.0f, w);
+    load_param<kEl>(io.bias, v, 0.0f, b);
+#pragma unroll
+    for (int e = 0; e < kEl; ++e) f[i][e] = __builtin_fmaf(f[i][e] * rstd, w[e], b[e]);
+    const u32x4 p = pack<kBf16>(f[i]);
+    if (!kQuant || io.y) ((u32x4*)io.y)[row * nvec + v] = p;
+    if constexpr (kQuant) {
+      // quantised from the rounded y: the same bits as the two calls one after
+      // the other
+      unpack<kBf16>(p, f[i]);
+      big = max_magnitude<kEl>(f[i], big);
+    }
+  }
+  if constexpr (kQuant) {
+    const RowQuantizer<kBf16> quant(row_max<THREADS>(big, (uint32_t*)red[2]));
+    if (tid == 0) io.scale[row] = quant.scale;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int v = i * THREADS + tid;
+      if (v < nvec) quant.store(f[i], io.q, row * nvec + v);
+    }
+  }
+}
+
+// EPT = 0: rows wider than the registers hold; read twice (the second time
+// mostly from the caches).
+template <bool kBf16, int THREADS, int EPT>
+__global__ void __launch_bounds__(RowOf<THREADS>::kGroup)
+quantize_rows(const u32x4* __restrict__ x, int8_t* __restrict__ q, float* __restrict__ scale,
+              int64_t row0, int64_t rows, int64_t nvec, const int32_t* __restrict__ valid0,
+              const int32_t* __restrict__ valid1) {
+  constexpr int kEl = kVecEl<kBf16>, VPT = EPT / kEl, NW = THREADS / 64;
+  const int64_t row = row0 + RowOf<THREADS>::row();
+  if (row >= rows) return;
+  if (valid0 && row >= (int64_t)*valid0 + (valid1 ? *valid1 : 0)) return;
+  __shared__ uint32_t red[NW];
+  const int tid = RowOf<THREADS>::tid();
+  x += row * nvec;
+  uint32_t big = 0;
+  if constexpr (EPT > 0) {
+    u32x4 xv[VPT];
+#pragma unroll
+    for (int i = 0; i < VPT; ++i)
+      if (i * THREADS + tid < nvec) xv[i] = x[i * THREADS + tid];
+    float f[VPT][kEl];
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      if (i * THREADS + tid >= nvec) continue;
+      unpack<kBf16>(xv[i], f[i]);
+      big = max_magnitude<kEl>(f[i], big);
+    }
+    const RowQuantizer<kBf16> quant(row_max<THREADS>(big, red));
+    if (tid == 0) scale[row] = quant.scale;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int v = i * THREADS + tid;
+      if (v < nvec) quant.store(f[i], q, row * nvec + v);
+    }
+  } else {
+    float f[kEl];
+    for (int64_t v = tid; v < nvec; v += THREADS) {
+      unpack<kBf16>(x[v], f);
+      big = max_magnitude<kEl>(f, big);
+    }
+    const RowQuantizer<kBf16> quant(row_max<THREADS>(big, red));
+    if (tid == 0) scale[row] = quant.scale;
+    for (int64_t v = tid; v < nvec; v += THREADS) {
+      unpack<kBf16>(x[v], f);
+      quant.store(f, q, row * nvec + v);
+    }
+  }
+}
+
+// Backward.  A workgroup takes rows b, b + gridDim, ...; its threads keep their
+// columns' sums of grad_y xh and grad_y in registers over all its rows and write
+// them once, as row b of the partials ([workgroups][2][H]).  norm_grad_reduce
+// adds those rows in a fixed order: no atomics, the same bits every time.
+// THREADS = 64: a wave's row; the four waves' sums are joined in LDS.
+template <bool kBf16, int THREADS, int EPT>
+__global__ void __launch_bounds__(RowOf<THREADS>::kGroup)
+norm_grad_rows(NormGradIO io, int T, int nvec) {
+  constexpr int kEl = kVecEl<kBf16>, VPT = EPT / kEl, NW = THREADS / 64;
+  constexpr int kPar = RowOf<THREADS>::kPerGroup;
+  __shared__ float red[2][2][NW];
+  const int tid = RowOf<THREADS>::tid();
+  const float inv_h = 1.0f / (float)(nvec * kEl);
+  float w[VPT][kEl], dw[VPT][kEl], db[VPT][kEl];
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int v = i * THREADS + tid;
+#pragma unroll
+    for (int e = 0; e < kEl; ++e) w[i][e] = dw[i][e] = db[i][e] = 0.0f;
+    if (v < nvec) load_param<kEl>(io.weight, v, 1.0f, w[i]);
+  }
+  const int64_t stride = (int64_t)gridDim.x * kPar;
+  int par = 0;
+  for (int64_t row = RowOf<THREADS>::row(); row < T; row += stride, par ^= 1) {
+    const u32x4* gy = (const u32x4*)io.grad_y + row * nvec;
+    const u32x4* x = (const u32x4*)io.x + row * nvec;
+    u32x4 gv[VPT], xv[VPT];
+#pragma unroll
+    for (int i = 0; i < VPT; ++i)
+      if (i * THREADS + tid < nvec) {
+        gv[i] = gy[i * THREADS + tid];
+        xv[i] = x[i * THREADS + tid];
+      }
+    const float mean = io.mean[row], rstd = io.rstd[row];
+    float s1 = 0.0f, s2 = 0.0f;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      if (i * THREADS + tid >= nvec) continue;
+      float g[kEl], s[kEl];
+      unpack<kBf16>(gv[i], g);
+      unpack<kBf16>(xv[i], s);
+#pragma unroll
+      for (int e = 0; e < kEl; ++e) {
+        const float xh = (s[e] - mean) * rstd, h = g[e] * w[i][e];
+        s1 += h;
+        s2 = __builtin_fmaf(h, xh, s2);
+        dw[i][e] = __builtin_fmaf(g[e], xh, dw[i][e]);
+        db[i][e] += g[e];
+      }
+    }
+    // two slots in turn: a wave can be one row ahead of the slowest, not two
+    s1 = wave_sum(s1);
+    s2 = wave_sum(s2);
+    if constexpr (THREADS > 64) {
+      if ((threadIdx.x & 63) == 0) {
+        red[par][0][threadIdx.x >> 6] = s1;
+        red[par][1][threadIdx.x >> 6] = s2;
+      }
+      __syncthreads();
+      s1 = s2 = 0.0f;
+#pragma unroll
+      for (int k = 0; k < NW; ++k) {
+        s1 += red[par][0][k];
+        s2 += red[par][1][k];
+      }
+    }
+    const float m1 = s1 * inv_h, m2 = s2 * inv_h;
+    const u32x4* gs = io.grad_sum ? (const u32x4*)io.grad_sum + row * nvec : nullptr;
+    u32x4* gx = (u32x4*)io.grad_x + row * nvec;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int v = i * THREADS + tid;
+      if (v >= nvec) continue;
+      float g[kEl], s[kEl], o[kEl];
+      unpack<kBf16>(gv[i], g);
+      unpack<kBf16>(xv[i], s);
+      if (gs)
+        unpack<kBf16>(gs[v], o);
+      else
+#pragma unroll
+        for (int e = 0; e < kEl; ++e) o[e] = 0.0f;
+#pragma unroll
+      for (int e = 0; e < kEl; ++e) {
+        const float xh = (s[e] - mean) * rstd, h = g[e] * w[i][e];
+        o[e] = __builtin_fmaf(rstd, __builtin_fmaf(-xh, m2, h - m1), o[e]);
+      }
+      gx[v] = pack<kBf16>(o);
+    }
+  }
+  if (!io.partials) return;
+  const int H = nvec * kEl;
+  float* part = io.partials + (int64_t)blockIdx.x * 2 * H;
+  if constexpr (THREADS == 64) {
+    // wave w adds its sums to those of the waves before it, in turn
+    extern __shared__ float cols[];  // [2][H]
+    const int wave = threadIdx.x >> 6;
+    for (int k = 0; k < kPar; ++k) {
+      if (wave == k) {
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+          const int v = i * 64 + tid;
+          if (v >= nvec) continue;
+#pragma unroll
+          for (int e = 0; e < kEl; ++e) {
+            const int c = v * kEl + e;
+            cols[c] = k ? cols[c] + dw[i][e] : dw[i][e];
+            cols[H + c] = k ? cols[H + c] + db[i][e] : db[i][e];
+          }
+        }
+      }
+      __syncthreads();
+    }
+    for (int c = threadIdx.x; c < 2 * H; c += 256) part[c] = cols[c];
+  } else {
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int v = i * THREADS + tid;
+      if (v >= nvec) continue;
+#pragma unroll
+      for (int e = 0; e < kEl; ++e) {
+        part[v * kEl + e] = dw[i][e];
+        part[H + v * kEl + e] = db[i][e];
+      }
+    }
+  }
+}
+
+// grad_weight / grad_bias: the column sums of the partials' n rows.  A
+// workgroup takes 64 columns (16 threads of four) with its rows dealt to 16
+// groups of threads, whose sums are joined in order.
+__global__ void __launch_bounds__(256)
+norm_grad_reduce(const float* __restrict__ part, int n, int H, float* __restrict__ grad_weight,
+                 float* __restrict__ grad_bias) {
+  __shared__ float4 sums[16][16];
+  float* out = blockIdx.y ? grad_bias : grad_weight;
+  if (!out) return;
+  const int cx = threadIdx.x & 15, g = threadIdx.x >> 4;
+  const int c = blockIdx.x * 64 + cx * 4;
+  float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  if (c < H)
+    for (int r = g; r < n; r += 16) {
+      const float4 p = *(const float4*)(part + ((int64_t)r * 2 + blockIdx.y) * H + c);
+      a.x += p.x;
+      a.y += p.y;
+      a.z += p.z;
+      a.w += p.w;
+    }
+  sums[g][cx] = a;
+  __syncthreads();
+  if (g != 0 || c >= H) return;
+  for (int k = 1; k < 16; ++k) {
+    const float4 p = sums[k][cx];
+    a.x += p.x;
+    a.y += p.y;
+    a.z += p.z;
+    a.w += p.w;
+  }
+  *(float4*)(out + c) = a;
+}
+
+// Workgroups of norm_grad_rows.
+int norm_grad_groups(const Shape& s) {
+  const int par = s.H <= 2048 ? 4 : 1;
+  return (int)std::min<int64_t>(((int64_t)s.T + par - 1) / par, 512);
+}
+
+template <bool kBf16, bool kQuant>
+hipError_t norm_launch(const Shape& s, const NormIO& io, hipStream_t st) {
+  const int nvec = s.H / kVecEl<kBf16>;
+  for (int64_t r0 = 0; r0 < s.T; r0 += kRowsPerLaunch) {
+    const int64_t end = std::min<int64_t>(s.T, r0 + kRowsPerLaunch);
+#define MOE_NORM(THREADS, EPT)                                                             \
+  hipLaunchKernelGGL((norm_rows<kBf16, THREADS, EPT, kQuant>), RowOf<THREADS>::grid(end - r0), \
+                     dim3(RowOf<THREADS>::kGroup), 0, st, io, r0, end, nvec)
+    if (s.H <= 1024)
+      MOE_NORM(64, 16);
+    else if (s.H <= 2048)
+      MOE_NORM(64, 32);
+    else if (s.H <= 4096)
+      MOE_NORM(256, 16);
+    else if (s.H <= 8192)
+      MOE_NORM(256, 32);
+    else
+      MOE_NORM(1024, 16);
+#undef MOE_NORM
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+template <bool kBf16>
+hipError_t norm_grad_launch(const Shape& s, const NormGradIO& io, hipStream_t st) {
+  const int nvec = s.H / kVecEl<kBf16>, groups = norm_grad_groups(s);
+#define MOE_NORM_GRAD(THREADS, EPT)                                                              \
+  hipLaunchKernelGGL((norm_grad_rows<kBf16, THREADS, EPT>), dim3((unsigned)groups),              \
+                     dim3(RowOf<THREADS>::kGroup),                                               \
+                     (THREADS == 64 && io.partials ? 2 * (size_t)s.H * 4 : 0), st, io, s.T, nvec)
+  if (s.H <= 1024)
+    MOE_NORM_GRAD(64, 16);
+  else if (s.H <= 2048)
+    MOE_NORM_GRAD(64, 32);
+  else if (s.H <= 4096)
+    MOE_NORM_GRAD(256, 16);
+  else if (s.H <= 8192)
+    MOE_NORM_GRAD(512, 16);
+  else
+    MOE_NORM_GRAD(1024, 16);
+#undef MOE_NORM_GRAD
+  return hipGetLastError();
+}
+
+template <bool kBf16>
+hipError_t quantize_launch(int64_t rows, int64_t cols, const void* x, int8_t* q, float* scale,
+                           const int32_t* valid0, const int32_t* valid1, hipStream_t st) {
+  const int64_t nvec = cols / kVecEl<kBf16>;
+  for (int64_t r0 = 0; r0 < rows; r0 += kRowsPerLaunch) {
+    const int64_t end = std::min(rows, r0 + kRowsPerLaunch);
+#define MOE_QUANTIZE(THREADS, EPT)                                                         \
+  hipLaunchKernelGGL((quantize_rows<kBf16, THREADS, EPT>), RowOf<THREADS>::grid(end - r0), \
+                     dim3(RowOf<THREADS>::kGroup), 0, st, (const u32x4*)x, q, scale, r0, end, \
+                     nvec, valid0, valid1)
+    if (cols <= 1024)
+      MOE_QUANTIZE(64, 16);
+    else if (cols <= 2048)
+      MOE_QUANTIZE(64, 32);
+    else if (cols <= 4096)
+      MOE_QUANTIZE(256, 16);
+    else if (cols <= 8192)
+      MOE_QUANTIZE(256, 32);
+    else if (cols <= 16384)
+      MOE_QUANTIZE(1024, 16);
+    else
+      MOE_QUANTIZE(1024, 0);
+#undef MOE_QUANTIZE
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+}  // namespace
+
+hipError_t launch_layer_norm(const Shape& s, const NormIO& io, hipStream_t st) {
+  if (s.T <= 0) return hipSuccess;
+  if (s.dtype == MOE_BF16)
+    return io.q ? norm_launch<true, true>(s, io, st) : norm_launch<true, false>(s, io, st);
+  return io.q ? norm_launch<false, true>(s, io, st) : norm_launch<false, false>(s, io, st);
+}
+
+size_t norm_grad_partial_bytes(const Shape& s) {
+  return (size_t)norm_grad_groups(s) * 2 * s.H * 4;
+}
+
+hipError_t launch_layer_norm_backward(const Shape& s, const NormGradIO& io, hipStream_t st) {
+  if (s.T > 0) {
+    const hipError_t e = s.dtype == MOE_BF16 ? norm_grad_launch<true>(s, io, st)
+                                             : norm_grad_launch<false>(s, io, st);
+    if (e != hipSuccess) return e;
+  }
+  if (!io.grad_weight && !io.grad_bias) return hipSuccess;
+  hipLaunchKernelGGL(norm_grad_reduce, dim3((unsigned)((s.H + 63) / 64), 2), dim3(256), 0, st,
+                     io.partials, s.T > 0 ? norm_grad_groups(s) : 0, s.H, io.grad_weight,
+                     io.grad_bias);
+  return hipGetLastError();
+}
+
+hipError_t launch_quantize_rows(int64_t rows, int64_t cols, bool bf16, const void* x, int8_t* q,
+                                float* scale, const int32_t* valid0, const int32_t* valid1,
+                                hipStream_t st) {
+  if (rows <= 0) return hipSuccess;
+  return bf16 ? quantize_launch<true>(rows, cols, x, q, scale, valid0, valid1, st)
+              : quantize_launch<false>(rows, cols, x, q, scale, valid0, valid1, st);
+}
+
+}  // namespace moe

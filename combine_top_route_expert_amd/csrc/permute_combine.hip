@@ -29,8 +29,6 @@ namespace {
 constexpr int kWavesPerBlock = 4;
 constexpr int kVecPerLane = 4;  // 16-byte vectors each lane keeps in flight per pass
 
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-
 __global__ void __launch_bounds__(64 * kWavesPerBlock)
 permute_rows(const u32x4* __restrict__ hidden, const int32_t* __restrict__ dst_row,
              u32x4* __restrict__ x_perm, int t0, int t1, int k, int nvec) {
@@ -58,25 +56,6 @@ permute_rows(const u32x4* __restrict__ hidden, const int32_t* __restrict__ dst_r
       }
     }
   }
-}
-
-__device__ __forceinline__ void unpack_bf16x8(const u32x4& q, float* f) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[2 * i] = __uint_as_float(q[i] << 16);
-    f[2 * i + 1] = __uint_as_float(q[i] & 0xffff0000u);
-  }
-}
-
-__device__ __forceinline__ u32x4 pack_bf16x8(const float* f) {
-  u32x4 q;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    __bf16 lo = (__bf16)f[2 * i], hi = (__bf16)f[2 * i + 1];
-    q[i] = (uint32_t)__builtin_bit_cast(uint16_t, lo) |
-           ((uint32_t)__builtin_bit_cast(uint16_t, hi) << 16);
-  }
-  return q;
 }
 
 // One wave per token; each lane holds kVecPerLane 16-byte vectors of the row.

@@ -406,6 +406,86 @@ moe_status moe_unpermute_combine_backward(const moe_shape* shape, int32_t chunk,
 moe_status moe_permute_backward(const moe_shape* shape, int32_t chunk, const void* grad_x_perm,
                                 const int32_t* dst_row, void* grad_hidden, hipStream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * Layer norm of the rows that enter the layer, and their 8-bit integer form.
+ *
+ * The norm's weight and bias and its statistics are float32 for every dtype (as
+ * top_k_weights are); statistics and gradient sums are held in fp32, every
+ * [T][H] output is rounded to the layer's dtype once.  Limit: H <= 16384
+ * (MOE_ERR_UNSUPPORTED beyond).  Only T, H and dtype of the shape matter here.
+ * --------------------------------------------------------------------------- */
+
+/*
+ * y[t] = (s[t] - mean[t]) * rstd[t] * weight + bias over the H values of a row,
+ * mean and variance of the row, rstd = 1 / sqrt(variance + eps), with s = x, or
+ * with a residual s = x + residual rounded to the layer's dtype once and
+ * written to sum (the statistics are those of the rounded values, which the
+ * backward reads again).
+ *  residual, sum  [T][H], both or neither
+ *  weight, bias   [H], each nullable (1 and 0)
+ *  eps            > 0 and finite
+ *  mean, rstd     [T] (out, each nullable): what moe_layer_norm_backward reads
+ * sum and y may each be x or residual (not each other).  A row that holds an
+ * infinity or a NaN gives NaN in that row only.
+ */
+moe_status moe_layer_norm(const moe_shape* shape, const void* x, const void* residual,
+                          const float* weight, const float* bias, float eps, void* sum, void* y,
+                          float* mean, float* rstd, hipStream_t stream);
+
+/*
+ * moe_layer_norm with each row of y also quantised as by moe_quantize_rows, in
+ * the same pass (same bits as the two calls): q and scale are what
+ * moe_quant_forward reads; y is nullable (a router reads it).
+ */
+moe_status moe_layer_norm_quantize(const moe_shape* shape, const void* x, const void* residual,
+                                   const float* weight, const float* bias, float eps, void* sum,
+                                   void* y, int8_t* q, float* scale, hipStream_t stream);
+
+/* Bytes of workspace moe_layer_norm_backward needs when it gives grad_weight or
+ * grad_bias: column sums of up to 512 groups of rows.  Host-only. */
+moe_status moe_layer_norm_backward_workspace_size(const moe_shape* shape, size_t* bytes);
+
+/*
+ * Gradient of moe_layer_norm.  With xh = (x - mean) * rstd and
+ * h = grad_y * weight, row by row:
+ *   grad_x = rstd * (h - mean_H(h) - xh * mean_H(h * xh)) [+ grad_sum]
+ *   grad_weight = sum_t grad_y[t] * xh[t],  grad_bias = sum_t grad_y[t]
+ *  grad_y     [T][H]: the gradient of y (from moe_chunked_backward's
+ *             grad_hidden_states, for the layer behind the norm)
+ *  x          [T][H]: the rows that were normalised (sum, where there was a
+ *             residual); mean, rstd [T]: as moe_layer_norm left them
+ *  grad_sum   [T][H], nullable: gradient that reaches the rows past the norm
+ *             (the residual stream), added to grad_x before the one rounding;
+ *             grad_x is then the gradient of both x and residual
+ *  grad_weight, grad_bias [H] float32, 16-byte aligned, each nullable;
+ *             overwritten (zeros when T is 0); sums in a fixed order, the same
+ *             bits every time
+ *  ws         moe_layer_norm_backward_workspace_size bytes; may be null when
+ *             neither parameter gradient is wanted
+ * grad_x may be grad_y, x or grad_sum.
+ */
+moe_status moe_layer_norm_backward(const moe_shape* shape, const void* grad_y, const void* x,
+                                   const float* weight, const float* mean, const float* rstd,
+                                   const void* grad_sum, void* grad_x, float* grad_weight,
+                                   float* grad_bias, void* ws, size_t ws_bytes,
+                                   hipStream_t stream);
+
+/*
+ * Rows of x as 8-bit integers with one scale each: scale[r] = max|x[r]| / 127,
+ * q[r][c] = 127 x[r][c] / max|x[r]| rounded to the nearest integer (the exact
+ * quotient, ties to even; -127..127), so x ~ scale * q.  A row of zeros has scale
+ * 0 and q 0; a row that holds an infinity or a NaN has scale NaN and q 0, so
+ * that every product with it is NaN.  For activations a row is a token, for
+ * expert weights an output channel: w_gate_up is E*2I rows of H, w_down E*H
+ * rows of I.
+ *  x  [rows][cols] of dtype (a moe_dtype); q [rows][cols] (16-byte aligned);
+ *     scale [rows] float32
+ * cols must be a multiple of 8 (MOE_BF16) or 4 (MOE_F32), else
+ * MOE_ERR_UNSUPPORTED.  q must not overlap x.
+ */
+moe_status moe_quantize_rows(int64_t rows, int64_t cols, int32_t dtype, const void* x, int8_t* q,
+                             float* scale, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
