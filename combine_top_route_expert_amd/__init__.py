@@ -29,6 +29,8 @@ __all__ = [
     "EXPORTED_SYMBOLS",
     "moe_chunked_forward_noalloc", "moe_layer_norm", "moe_layer_norm_quantize",
     "moe_layer_norm_backward_workspace_size", "moe_layer_norm_backward", "moe_quantize_rows",
+    "moe_quant_gate_up_gather_pair", "moe_quant_act_pair", "moe_quant_down_pair",
+    "moe_quant_workspace_size", "moe_quant_forward",
 ]
 
 MOE_F32, MOE_BF16 = 0, 1
@@ -46,7 +48,8 @@ EXPORTED_SYMBOLS = (
     "moe_backward_workspace_size",
     "moe_chunked_backward", "moe_unpermute_combine_backward", "moe_permute_backward",
     "moe_layer_norm", "moe_layer_norm_quantize", "moe_layer_norm_backward_workspace_size",
-    "moe_layer_norm_backward", "moe_quantize_rows",
+    "moe_layer_norm_backward", "moe_quantize_rows", "moe_quant_gate_up_gather_pair",
+    "moe_quant_act_pair", "moe_quant_down_pair", "moe_quant_workspace_size", "moe_quant_forward",
 )
 
 
@@ -157,6 +160,14 @@ def load_library() -> ctypes.CDLL:
                                                    ctypes.c_size_t, _P]),
         "moe_quantize_rows": (ctypes.c_int, [ctypes.c_int64, ctypes.c_int64, ctypes.c_int32, _P,
                                              _P, _P, _P]),
+        "moe_quant_gate_up_gather_pair": (ctypes.c_int, [_SP, ctypes.c_int32, _P, _P, _P, _P, _P,
+                                                         _P, _P, _P]),
+        "moe_quant_act_pair": (ctypes.c_int, [_SP, ctypes.c_int32, _P, _P, _P, _P, _P]),
+        "moe_quant_down_pair": (ctypes.c_int, [_SP, ctypes.c_int32, _P, _P, _P, _P, _P, _P, _P,
+                                               _P]),
+        "moe_quant_workspace_size": (ctypes.c_int, [_SP, ctypes.POINTER(ctypes.c_size_t)]),
+        "moe_quant_forward": (ctypes.c_int, [_SP, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P,
+                                             ctypes.c_size_t, _P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -552,3 +563,67 @@ def moe_quantize_rows(rows: int, cols: int, dtype: str, x, q, scale, stream=None
     on.call("moe_quantize_rows", stream, rows, cols, MOE_BF16 if bf16 else MOE_F32,
             on(x, torch.bfloat16 if bf16 else torch.float32, rows * cols, "x"),
             on(q, torch.int8, rows * cols, "q"), on(scale, torch.float32, rows, "scale"))
+
+
+# ---------------------------------------------------------------- 8-bit integer experts
+def moe_quant_gate_up_gather_pair(shape: moe_shape, chunk: int, hidden_q, hidden_scale, src_row,
+                                  offsets, w_gate_up_q, w_gate_up_scale, act, stream=None) -> None:
+    rows = sum(_pair_rows(shape, chunk))
+    on, i8, i32, f32 = _OnDevice(), torch.int8, torch.int32, torch.float32
+    T, H, E, I = shape.T, shape.H, shape.E, shape.I  # noqa: E741
+    on.call("moe_quant_gate_up_gather_pair", stream, ctypes.byref(shape), chunk,
+            on(hidden_q, i8, T * H, "hidden_q"), on(hidden_scale, f32, T, "hidden_scale"),
+            on(src_row, i32, T * shape.k, "src_row"),
+            on(offsets, i32, shape.N * (E + 1), "offsets"),
+            on(w_gate_up_q, i8, E * 2 * I * H, "w_gate_up_q"),
+            on(w_gate_up_scale, f32, E * 2 * I, "w_gate_up_scale"),
+            on(act, shape.torch_dtype, rows * I, "act"))
+
+
+def moe_quant_act_pair(shape: moe_shape, chunk: int, act, offsets, act_q, act_scale,
+                       stream=None) -> None:
+    rows = sum(_pair_rows(shape, chunk))
+    on = _OnDevice()
+    on.call("moe_quant_act_pair", stream, ctypes.byref(shape), chunk,
+            on(act, shape.torch_dtype, rows * shape.I, "act"),
+            on(offsets, torch.int32, shape.N * (shape.E + 1), "offsets"),
+            on(act_q, torch.int8, rows * shape.I, "act_q"),
+            on(act_scale, torch.float32, rows, "act_scale"))
+
+
+def moe_quant_down_pair(shape: moe_shape, chunk: int, act_q, act_scale, offsets, w_down_q,
+                        w_down_scale, y0, y1, stream=None) -> None:
+    rows0, rows1 = _pair_rows(shape, chunk)
+    on, i8, f32, dt = _OnDevice(), torch.int8, torch.float32, shape.torch_dtype
+    H, E, I = shape.H, shape.E, shape.I  # noqa: E741
+    on.call("moe_quant_down_pair", stream, ctypes.byref(shape), chunk,
+            on(act_q, i8, (rows0 + rows1) * I, "act_q"),
+            on(act_scale, f32, rows0 + rows1, "act_scale"),
+            on(offsets, torch.int32, shape.N * (E + 1), "offsets"),
+            on(w_down_q, i8, E * H * I, "w_down_q"), on(w_down_scale, f32, E * H, "w_down_scale"),
+            on(y0, dt, rows0 * H, "y0"), on(y1, dt, rows1 * H, "y1"))
+
+
+def moe_quant_workspace_size(shape: moe_shape) -> int:
+    b = ctypes.c_size_t()
+    _check("moe_quant_workspace_size",
+           load_library().moe_quant_workspace_size(ctypes.byref(shape), ctypes.byref(b)))
+    return b.value
+
+
+def moe_quant_forward(shape: moe_shape, hidden_q, hidden_scale, top_k_index, top_k_weights,
+                      w_gate_up_q, w_gate_up_scale, w_down_q, w_down_scale, out, ws,
+                      dev_error=None, stream=None) -> None:
+    """The layer on quantised hidden rows and weights; out in the shape's dtype."""
+    on, i8, i32, f32 = _OnDevice(), torch.int8, torch.int32, torch.float32
+    T, H, E, k, I = shape.T, shape.H, shape.E, shape.k, shape.I  # noqa: E741
+    args = (on(hidden_q, i8, T * H, "hidden_q"), on(hidden_scale, f32, T, "hidden_scale"),
+            on(top_k_index, i32, T * k, "top_k_index"),
+            on(top_k_weights, f32, T * k, "top_k_weights"),
+            on(w_gate_up_q, i8, E * 2 * I * H, "w_gate_up_q"),
+            on(w_gate_up_scale, f32, E * 2 * I, "w_gate_up_scale"),
+            on(w_down_q, i8, E * H * I, "w_down_q"), on(w_down_scale, f32, E * H, "w_down_scale"),
+            on(out, shape.torch_dtype, T * H, "out"),
+            on.optional(dev_error, i32, 1, "dev_error"))
+    wp = on(ws, torch.uint8, moe_quant_workspace_size(shape), "ws")
+    on.call("moe_quant_forward", stream, ctypes.byref(shape), *args, wp, ws.numel())

@@ -998,4 +998,213 @@ moe_status moe_layer_norm_backward(const moe_shape* shape, const void* grad_y, c
   return hip_status(launch_layer_norm_backward(s, io, stream));
 }
 
+namespace moe {
+namespace {
+
+// Layout of the moe_quant_forward workspace: the forward's metadata, a [rows][H]
+// y buffer per slot, and the pair's joint act rows in the layer's dtype and
+// quantised.
+struct QuantPlan {
+  size_t counts, offsets, splits, src_row, dst_row, dev_err, meta_ws;
+  size_t y[2], act, act_q, act_scale;
+  size_t bytes;
+};
+
+QuantPlan quant_plan(const Shape& s) {
+  QuantPlan p{};
+  size_t o = 0;
+  auto take = [&](size_t n) {
+    size_t at = o;
+    o += align256(n);
+    return at;
+  };
+  p.counts = take((size_t)s.N * s.E * 4);
+  p.offsets = take((size_t)s.N * (s.E + 1) * 4);
+  p.splits = take((size_t)s.N * s.G * 4);
+  p.src_row = take((size_t)s.A * 4);
+  p.dst_row = take((size_t)s.A * 4);
+  p.dev_err = take(4);
+  p.meta_ws = take(meta_plan(s).bytes);
+  const size_t rows = (size_t)s.Tc * s.k;
+  const int nslots = s.N >= 2 ? 2 : 1;
+  for (int i = 0; i < nslots; ++i) p.y[i] = take(rows * s.H * s.elem);
+  p.act = take(nslots * rows * s.I * s.elem);
+  p.act_q = take(nslots * rows * s.I);
+  p.act_scale = take(nslots * rows * 4);
+  p.bytes = o;
+  return p;
+}
+
+// The 8-bit products' limits: 64-byte rows whatever the output's dtype, int32 sums.
+bool quant_limits(const Shape& s) {
+  return s.H % 64 == 0 && s.I % 64 == 0 && s.H <= kQuantMaxK && s.I <= kQuantMaxK;
+}
+
+// Checks shared by the 8-bit pair entry points.
+moe_status quant_pair_args(const moe_shape* shape, int32_t chunk, Shape* s,
+                           const int32_t* offsets, const int32_t** off0, const int32_t** off1,
+                           int64_t* rows0, int64_t* rows1) {
+  moe_status st = resolve_shape(shape, s);
+  if (st != MOE_OK) return st;
+  if (!quant_limits(*s)) return MOE_ERR_UNSUPPORTED;
+  return pair_args(shape, chunk, s, offsets, off0, off1, rows0, rows1);
+}
+
+bool scale_ok(const float* p) { return p && aligned(p, 4); }
+
+// Valid rows of a pair: the last offset of each chunk.
+hipError_t quantize_act(const Shape& s, const int32_t* off0, const int32_t* off1, int64_t rows,
+                        const void* act, int8_t* act_q, float* act_scale, hipStream_t st) {
+  return launch_quantize_rows(rows, s.I, s.dtype == MOE_BF16, act, act_q, act_scale, off0 + s.E,
+                              off1 ? off1 + s.E : nullptr, st);
+}
+
+// gate_up of a pair: hidden rows gathered through the two chunks' slices of src_row.
+GroupedIO quant_gate_up_io(const Shape& s, int chunk, const int8_t* hidden_q,
+                           const int32_t* src_row, const int32_t* off0, const int32_t* off1,
+                           int64_t rows, void* act) {
+  int t0, t1, u0 = 0, u1 = 0;
+  chunk_tokens(s, chunk, &t0, &t1);
+  if (chunk + 1 < s.N) chunk_tokens(s, chunk + 1, &u0, &u1);
+  GroupedIO io{};
+  io.off[0] = off0;
+  io.off[1] = off1;
+  io.rows_bound = rows;
+  io.a[0] = hidden_q;
+  io.gather[0] = src_row + (size_t)t0 * s.k;
+  io.gather[1] = src_row + (size_t)u0 * s.k;
+  io.gather_k = s.k;
+  io.c[0] = act;
+  return io;
+}
+
+GroupedIO quant_down_io(const int8_t* act_q, const int32_t* off0, const int32_t* off1,
+                        int64_t rows, void* y0, void* y1) {
+  GroupedIO io{};
+  io.off[0] = off0;
+  io.off[1] = off1;
+  io.rows_bound = rows;
+  io.a[0] = act_q;
+  io.c[0] = y0;
+  io.c[1] = y1;
+  io.c_split = true;
+  return io;
+}
+
+}  // namespace
+}  // namespace moe
+
+moe_status moe_quant_gate_up_gather_pair(const moe_shape* shape, int32_t chunk,
+                                         const int8_t* hidden_q, const float* hidden_scale,
+                                         const int32_t* src_row, const int32_t* offsets,
+                                         const int8_t* w_gate_up_q, const float* w_gate_up_scale,
+                                         void* act, hipStream_t stream) {
+  Shape s;
+  const int32_t *off0 = nullptr, *off1 = nullptr;
+  int64_t rows0 = 0, rows1 = 0;
+  moe_status st = quant_pair_args(shape, chunk, &s, offsets, &off0, &off1, &rows0, &rows1);
+  if (st != MOE_OK || rows0 + rows1 == 0) return st;
+  if (!buf_ok(hidden_q, 1) || !scale_ok(hidden_scale) || !src_row || !aligned(src_row, 4) ||
+      !buf_ok(w_gate_up_q, 1) || !scale_ok(w_gate_up_scale) || !buf_ok(act, 1))
+    return MOE_ERR_INVALID_ARG;
+  return hip_status(launch_gate_up_i8(
+      s, quant_gate_up_io(s, chunk, hidden_q, src_row, off0, off1, rows0 + rows1, act),
+      hidden_scale, w_gate_up_q, w_gate_up_scale, stream));
+}
+
+moe_status moe_quant_act_pair(const moe_shape* shape, int32_t chunk, const void* act,
+                              const int32_t* offsets, int8_t* act_q, float* act_scale,
+                              hipStream_t stream) {
+  Shape s;
+  const int32_t *off0 = nullptr, *off1 = nullptr;
+  int64_t rows0 = 0, rows1 = 0;
+  moe_status st = quant_pair_args(shape, chunk, &s, offsets, &off0, &off1, &rows0, &rows1);
+  if (st != MOE_OK || rows0 + rows1 == 0) return st;
+  if (!buf_ok(act, 1) || !buf_ok(act_q, 1) || !scale_ok(act_scale)) return MOE_ERR_INVALID_ARG;
+  return hip_status(
+      quantize_act(s, off0, off1, rows0 + rows1, act, act_q, act_scale, stream));
+}
+
+moe_status moe_quant_down_pair(const moe_shape* shape, int32_t chunk, const int8_t* act_q,
+                               const float* act_scale, const int32_t* offsets,
+                               const int8_t* w_down_q, const float* w_down_scale, void* y0,
+                               void* y1, hipStream_t stream) {
+  Shape s;
+  const int32_t *off0 = nullptr, *off1 = nullptr;
+  int64_t rows0 = 0, rows1 = 0;
+  moe_status st = quant_pair_args(shape, chunk, &s, offsets, &off0, &off1, &rows0, &rows1);
+  if (st != MOE_OK || rows0 + rows1 == 0) return st;
+  if (!buf_ok(act_q, 1) || !scale_ok(act_scale) || !buf_ok(w_down_q, 1) ||
+      !scale_ok(w_down_scale) || !buf_ok(y0, rows0) || !buf_ok(y1, rows1))
+    return MOE_ERR_INVALID_ARG;
+  return hip_status(launch_down_i8(s, quant_down_io(act_q, off0, off1, rows0 + rows1, y0, y1),
+                                   act_scale, w_down_q, w_down_scale, stream));
+}
+
+moe_status moe_quant_workspace_size(const moe_shape* shape, size_t* bytes) {
+  Shape s;
+  const moe_status st = resolve_shape(shape, &s);
+  if (st != MOE_OK) return st;
+  if (!quant_limits(s)) return MOE_ERR_UNSUPPORTED;
+  if (!bytes) return MOE_ERR_INVALID_ARG;
+  *bytes = quant_plan(s).bytes;
+  return MOE_OK;
+}
+
+moe_status moe_quant_forward(const moe_shape* shape, const int8_t* hidden_q,
+                             const float* hidden_scale, const int32_t* top_k_index,
+                             const float* top_k_weights, const int8_t* w_gate_up_q,
+                             const float* w_gate_up_scale, const int8_t* w_down_q,
+                             const float* w_down_scale, void* out, int32_t* dev_error, void* ws,
+                             size_t ws_bytes, hipStream_t stream) {
+  Shape s;
+  const moe_status st = resolve_shape(shape, &s);
+  if (st != MOE_OK) return st;
+  if (!quant_limits(s)) return MOE_ERR_UNSUPPORTED;
+  if (!ws || !aligned(ws, 256) || !aligned(dev_error, 4)) return MOE_ERR_INVALID_ARG;
+  const QuantPlan p = quant_plan(s);
+  if (ws_bytes < p.bytes) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  if (s.T > 0) {
+    if (!buf_ok(hidden_q, 1) || !scale_ok(hidden_scale) || !top_k_index || !top_k_weights ||
+        !buf_ok(w_gate_up_q, 1) || !scale_ok(w_gate_up_scale) || !buf_ok(w_down_q, 1) ||
+        !scale_ok(w_down_scale) || !buf_ok(out, 1) || !aligned(top_k_index, 4) ||
+        !aligned(top_k_weights, 4))
+      return MOE_ERR_INVALID_ARG;
+  }
+  char* w = (char*)ws;
+  int32_t* offsets = (int32_t*)(w + p.offsets);
+  int32_t* src_row = (int32_t*)(w + p.src_row);
+  int32_t* dst_row = (int32_t*)(w + p.dst_row);
+  hipError_t he = launch_route_meta(
+      s, top_k_index, (int32_t*)(w + p.counts), offsets, (int32_t*)(w + p.splits), src_row,
+      dst_row, dev_error ? dev_error : (int32_t*)(w + p.dev_err), w + p.meta_ws, stream);
+  void* act = w + p.act;
+  int8_t* act_q = (int8_t*)(w + p.act_q);
+  float* act_scale = (float*)(w + p.act_scale);
+  // pairs of chunks as in the pair-fused forward: each expert's weights are
+  // streamed once per pair
+  for (int c = 0; he == hipSuccess && c < s.N; c += 2) {
+    int t0, t1, u0 = 0, u1 = 0;
+    chunk_tokens(s, c, &t0, &t1);
+    if (c + 1 < s.N) chunk_tokens(s, c + 1, &u0, &u1);
+    const int64_t rows0 = (int64_t)(t1 - t0) * s.k, rows1 = (int64_t)(u1 - u0) * s.k;
+    const int64_t rows = rows0 + rows1;
+    if (rows == 0) continue;  // empty tail pair
+    const int32_t* off0 = offsets + (size_t)c * (s.E + 1);
+    const int32_t* off1 = rows1 > 0 ? off0 + (s.E + 1) : nullptr;
+    void *y0 = w + p.y[0], *y1 = rows1 > 0 ? w + p.y[1] : nullptr;
+    he = launch_gate_up_i8(s, quant_gate_up_io(s, c, hidden_q, src_row, off0, off1, rows, act),
+                           hidden_scale, w_gate_up_q, w_gate_up_scale, stream);
+    if (he == hipSuccess) he = quantize_act(s, off0, off1, rows, act, act_q, act_scale, stream);
+    if (he == hipSuccess)
+      he = launch_down_i8(s, quant_down_io(act_q, off0, off1, rows, y0, y1), act_scale, w_down_q,
+                          w_down_scale, stream);
+    if (he == hipSuccess)
+      he = rows1 > 0 ? launch_combine_pair(s, t0, u0, u1, y0, y1, dst_row, top_k_weights, out,
+                                           stream)
+                     : launch_combine(s, t0, t1, y0, dst_row, top_k_weights, out, stream);
+  }
+  return hip_status(he);
+}
+
 }  // extern "C"

@@ -12,7 +12,7 @@
 // rows straight from hidden_states through src_row (GroupedIO::gather): the
 // permute fused into the A loader's addresses.
 //
-// Pipeline: K advances BK (64) at a time.  Each stage of the A (rows) and B
+// Pipeline: K advances 64 at a time.  Each stage of the A (rows) and B
 // (weight) tiles is copied HBM -> LDS by the direct-to-LDS load (64 lanes x 16
 // bytes land as one contiguous 1 KB block), so loads need no VGPRs and
 // STAGES-1 stages are in flight while the matrix cores work on the oldest one
@@ -93,48 +93,16 @@
 #include <algorithm>
 #include <type_traits>
 
-#include "moe_internal.h"
+#include "gemm_tile.h"
 
 namespace moe {
 
 namespace {
 
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-typedef float f32x16 __attribute__((ext_vector_type(16)));
-typedef __attribute__((address_space(3))) void lds_void;
-
-// s_waitcnt immediates (gfx9 encoding: vmcnt[3:0] | expcnt[6:4] | lgkmcnt[11:8] | vmcnt[15:14])
-constexpr int wait_vm(int v) { return (v & 0xF) | ((v >> 4) << 14) | (0x7 << 4) | (0xF << 8); }
-constexpr int kWaitLgkm0 = 0xF | (0x3 << 14) | (0x7 << 4);
-
-struct GemmArgs {
-  const uint16_t* A[2];       // [rows][K] bf16 (A[1]: chunk-1 rows when a_split)
-  const uint16_t* B;          // [E][b_rows][K] bf16
+struct GemmArgs : TileArgs {
   uint16_t* C[2];             // [rows][ncols] bf16 (C[1]: chunk-1 rows when c_split)
-  const int32_t* off0;        // E + 1 offsets of the (first) chunk
-  const int32_t* off1;        // E + 1 offsets of the pair's second chunk, or null
-  int a_split, c_split;
-  int E, K, I, ncols, n_tiles;
-  int64_t b_expert_stride;    // elements per expert in B
   uint16_t* gu;               // gate_up, optional: g and u of each row, joint [rows][2I]
-  const int32_t* gather[2];   // optional: A rows gathered from hidden_states (src_row slices)
-  int gather_k;
-  const char* a_base;         // descriptor loads: every A row lies within 4 GiB above it
 };
-
-
-// Address of virtual row v of the tile's expert on one side of the product.
-__device__ __forceinline__ const uint16_t* row_ptr(const uint16_t* const (&base)[2], int split,
-                                                   const TileRows& tr, int v, int64_t ld) {
-  if (split) {
-    int part;
-    const int r = tr.split_row(v, &part);
-    return (part ? base[1] : base[0]) + (int64_t)r * ld;
-  }
-  return base[0] + (int64_t)tr.joint_row(v) * ld;
-}
-
-constexpr int cmax(int x, int y) { return x > y ? x : y; }
 
 __device__ __forceinline__ uint16_t to_bf16_bits(float f) {
   return __builtin_bit_cast(uint16_t, (__bf16)f);
@@ -146,207 +114,6 @@ __device__ __forceinline__ uint16_t to_bf16_bits(float f) {
 // e^-g overflowing to infinity gives g * 0 = 0, the limit.
 __device__ __forceinline__ float swiglu(float g, float u) {
   return g * __builtin_amdgcn_rcpf(1.0f + __expf(-g)) * u;
-}
-
-// LDS layout of one stage: BM rows of A then BN rows of B, each row BK bf16
-// (ROW_BYTES) holding CH 16-byte chunks; chunk c of row r sits at slot
-// c ^ swz(r).  A 16-lane phase of a 16-byte fragment read covers 16
-// consecutive rows at one chunk; rows r and r + RB share a position in a
-// 256-byte bank line, so swz(r) = (r / RB) mod CH spreads the 16 rows over 16
-// distinct 16-byte bank groups (measured: no bank conflicts).
-template <int BK>
-struct StageGeom {
-  static constexpr int ROW_BYTES = BK * 2;
-  static constexpr int CH = BK / 8;               // 16-byte chunks per row
-  static constexpr int RPB = 1024 / ROW_BYTES;     // rows per 1 KB direct-to-LDS block
-  static constexpr int RB = 256 / ROW_BYTES;       // rows per 256-byte bank line
-  static_assert(BK == 32 || BK == 64, "stage depth");
-  static __device__ __forceinline__ int swz(int r) { return (r / RB) & (CH - 1); }
-  // 32x32x16 fragment of a 32-row block: lane l holds row l % 32 and the eight
-  // K elements of 16-byte chunk 2*kk + l/32 of the stage.
-  static __device__ __forceinline__ int frag_offset(int lane, int kk) {
-    const int r = lane & 31;
-    const int chunk = 2 * kk + (lane >> 5);
-    return r * ROW_BYTES + ((chunk ^ swz(r)) << 4);
-  }
-};
-
-// Everything a workgroup needs to stream its tile's A and B stages into LDS.
-//
-// kBuf: the stages are copied with the buffer form of the direct-to-LDS load
-// (a descriptor per operand, 32-bit byte offsets per lane) instead of the
-// global form.  Same bytes, same LDS layout; but the global form is a FLAT
-// instruction, and while one is outstanding the compiler cannot count LDS
-// reads in order, so every wait for a fragment read drains all of them.  With
-// descriptor loads the K loop waits only for the fragments it is about to use,
-// and the next sub-step's reads overlap the current MFMAs.  The host picks the
-// global form when the A rows do not fit one 4 GiB window.
-template <bool kGateUp, int BM, int BN, int NW, int WN, int BK, bool kBuf>
-struct TileLoader {
-  using G = StageGeom<BK>;
-  static constexpr int LA = BM / G::RPB / NW, LB = BN / G::RPB / NW;  // 1 KB loads per wave
-  static constexpr int STAGE_BYTES = (BM + BN) * G::ROW_BYTES;
-  static_assert(LA * G::RPB * NW == BM && LB * G::RPB * NW == BN, "tile rows per wave");
-  const char* a_src[LA];
-  const char* b_src[LB];
-  uint32_t a_off[LA], b_off[LB];  // kBuf: byte offsets from the descriptors' bases
-  rsrc_t ra, rb;
-  int wave, mrows;
-  int live_a;  // A blocks of this wave that hold rows of the tile (the rest are skipped)
-
-  __device__ __forceinline__ void init(const GemmArgs& a, const TileRows& tr, int nt, int lane,
-                                       int wave_) {
-    wave = wave_;
-    mrows = tr.rows;
-    const int row_in_blk = lane / G::CH, slot = lane % G::CH;
-    live_a = 0;
-    int rr[LA], ch[LA];
-#pragma unroll
-    for (int t = 0; t < LA; ++t) {
-      const int row = (wave * LA + t) * G::RPB + row_in_blk;
-      ch[t] = slot ^ G::swz(row);
-      rr[t] = row < mrows ? row : mrows - 1;
-      live_a += (wave * LA + t) * G::RPB < mrows ? 1 : 0;
-    }
-    if (a.gather[0]) {
-      // permute fused into the row addressing: chunk row -> token (the LA
-      // lookups are issued together and waited for once)
-      int src[LA];
-#pragma unroll
-      for (int t = 0; t < LA; ++t) {
-        int part;
-        const int cr = tr.split_row(tr.v0 + rr[t], &part);
-        src[t] = (part ? a.gather[1] : a.gather[0])[cr];
-      }
-#pragma unroll
-      for (int t = 0; t < LA; ++t)
-        a_src[t] = (const char*)(a.A[0] + (int64_t)(src[t] / a.gather_k) * a.K + ch[t] * 8);
-    } else {
-#pragma unroll
-      for (int t = 0; t < LA; ++t)
-        a_src[t] = (const char*)(row_ptr(a.A, a.a_split, tr, tr.v0 + rr[t], a.K) + ch[t] * 8);
-    }
-    // the expert is the same for the whole workgroup: keep its base scalar
-    const int e = __builtin_amdgcn_readfirstlane(tr.e);
-    const uint16_t* Be = a.B + (int64_t)e * a.b_expert_stride;
-#pragma unroll
-    for (int t = 0; t < LB; ++t) {
-      const int col = (wave * LB + t) * G::RPB + row_in_blk;  // tile column = B row
-      const int chunk = slot ^ G::swz(col);
-      int brow;
-      if constexpr (kGateUp) {
-        // each wave's WN columns: gate for the first half, the matching up rows after
-        const int cw = col / WN, w = col % WN;
-        const int q = w / (WN / 2), c = w % (WN / 2);
-        brow = q * a.I + nt * (BN / 2) + cw * (WN / 2) + c;
-      } else {
-        brow = nt * BN + col;
-        if (brow > a.ncols - 1) brow = a.ncols - 1;
-      }
-      b_src[t] = (const char*)(Be + (int64_t)brow * a.K + chunk * 8);
-    }
-    if constexpr (kBuf) {
-      ra = raw_rsrc(a.a_base);
-      rb = raw_rsrc(Be);
-#pragma unroll
-      for (int t = 0; t < LA; ++t) a_off[t] = (uint32_t)(a_src[t] - a.a_base);
-#pragma unroll
-      for (int t = 0; t < LB; ++t) b_off[t] = (uint32_t)(b_src[t] - (const char*)Be);
-    }
-  }
-
-  // One 1 KB block: 64 lanes x 16 bytes at byte koff of their rows into dst.
-  __device__ __forceinline__ void load_a(int t, int koff, char* dst) const {
-    if constexpr (kBuf)
-      buffer_load_lds16(ra, dst, a_off[t], koff);
-    else
-      __builtin_amdgcn_global_load_lds((const void*)(a_src[t] + koff), (lds_void*)dst, 16, 0, 0);
-  }
-  // kNt: the weight panel is read by this tile only (its expert has one m-tile),
-  // so its bytes are streamed with the non-temporal cache policy.
-  template <bool kNt>
-  __device__ __forceinline__ void load_b(int t, int koff, char* dst) const {
-    if constexpr (kBuf) {
-      if constexpr (kNt)
-        buffer_load_lds16_nt(rb, dst, b_off[t], koff);
-      else
-        buffer_load_lds16(rb, dst, b_off[t], koff);
-    } else {
-      __builtin_amdgcn_global_load_lds((const void*)(b_src[t] + koff), (lds_void*)dst, 16, 0,
-                                       kNt ? 2 : 0);
-    }
-  }
-
-  // Compact stage of a tile with at most SROWS rows: those rows of A (the
-  // first blocks, which only the first waves hold) then the BN rows of B.
-  template <int SROWS>
-  static constexpr int small_a() { return SROWS * G::ROW_BYTES; }
-  template <int SROWS>
-  static constexpr int small_stage() { return small_a<SROWS>() + BN * G::ROW_BYTES; }
-  template <int SROWS, bool kNt>
-  __device__ __forceinline__ void issue_small(char* smem, int kt, int buf) const {
-    char* base = smem + buf * small_stage<SROWS>();
-    const int koff = kt * G::ROW_BYTES;
-#pragma unroll
-    for (int t = 0; t < LA; ++t)
-      if (t < live_a)  // blocks past the tile's (at most SROWS) rows are not live
-        load_a(t, koff, base + (wave * LA + t) * 1024);
-#pragma unroll
-    for (int t = 0; t < LB; ++t)
-      load_b<kNt>(t, koff, base + small_a<SROWS>() + (wave * LB + t) * 1024);
-  }
-
-  // Rings of the wide 256 x 256 kernel: two A stages, then three B stages.
-  static constexpr int A_BYTES = BM * G::ROW_BYTES, B_BYTES = BN * G::ROW_BYTES;
-  __device__ __forceinline__ void issue_a(char* smem, int kt, int abuf) const {
-    char* base = smem + abuf * A_BYTES;
-    const int koff = kt * G::ROW_BYTES;
-#pragma unroll
-    for (int t = 0; t < LA; ++t)
-      if (t < live_a) load_a(t, koff, base + (wave * LA + t) * 1024);
-  }
-  template <bool kNt>
-  __device__ __forceinline__ void issue_b(char* smem, int kt, int bbuf) const {
-    char* base = smem + 2 * A_BYTES + bbuf * B_BYTES;
-    const int koff = kt * G::ROW_BYTES;
-#pragma unroll
-    for (int t = 0; t < LB; ++t) load_b<kNt>(t, koff, base + (wave * LB + t) * 1024);
-  }
-
-  // Loads one stage.  A blocks of 1 KB that lie wholly past the tile's rows are
-  // not loaded (their LDS rows feed only outputs that are never stored), so a
-  // wave issues live_a + LB loads per stage.
-  template <bool kNt>
-  __device__ __forceinline__ void issue(char* smem, int kt, int buf) const {
-    char* base = smem + buf * STAGE_BYTES;
-    const int koff = kt * G::ROW_BYTES;
-#pragma unroll
-    for (int t = 0; t < LA; ++t)
-      if (t < live_a) load_a(t, koff, base + (wave * LA + t) * 1024);
-#pragma unroll
-    for (int t = 0; t < LB; ++t)
-      load_b<kNt>(t, koff, base + BM * G::ROW_BYTES + (wave * LB + t) * 1024);
-  }
-};
-
-// Waits until at most n of this wave's vector memory operations are pending
-// (s_waitcnt takes an immediate, so n is dispatched over its possible values).
-__device__ __forceinline__ void wait_loads(int n) {
-#define MOE_WAIT_CASE(v)                    \
-  case v:                                   \
-    __builtin_amdgcn_s_waitcnt(wait_vm(v)); \
-    return;
-  switch (n) {
-    MOE_WAIT_CASE(1) MOE_WAIT_CASE(2) MOE_WAIT_CASE(3) MOE_WAIT_CASE(4) MOE_WAIT_CASE(5)
-    MOE_WAIT_CASE(6) MOE_WAIT_CASE(7) MOE_WAIT_CASE(8) MOE_WAIT_CASE(9) MOE_WAIT_CASE(10)
-    MOE_WAIT_CASE(11) MOE_WAIT_CASE(12) MOE_WAIT_CASE(13) MOE_WAIT_CASE(14) MOE_WAIT_CASE(15)
-    MOE_WAIT_CASE(16) MOE_WAIT_CASE(17) MOE_WAIT_CASE(18) MOE_WAIT_CASE(19) MOE_WAIT_CASE(20)
-    MOE_WAIT_CASE(21) MOE_WAIT_CASE(22) MOE_WAIT_CASE(23) MOE_WAIT_CASE(24)
-    default:  // n <= 0, or beyond the table: wait for every load
-      __builtin_amdgcn_s_waitcnt(wait_vm(0));
-      return;
-  }
-#undef MOE_WAIT_CASE
 }
 
 // Epilogue through LDS.  The K loops pass the weight fragment as the MFMA's
@@ -437,240 +204,19 @@ __device__ __forceinline__ void store_tile_lds(const GemmArgs& a, const f32x16 (
   }
 }
 
-// The K loop of one wave.  F (<= FM) 32-row blocks of the wave's band take
-// part in the MFMAs (F = 0: none); the wave still issues its share of every
-// stage's loads and joins every barrier.  The loop body holds no branch, so
-// the compiler schedules the fragment reads, MFMAs and the next stage's loads
-// as one block.
-template <int F, int FM, int FN, int WM, int WN, int BM, int BK, int STAGES, bool kNt, class Loader>
-__device__ __forceinline__ void k_loop(f32x16 (&acc)[FM][FN], const Loader& ld, char* smem,
-                                       int KT, int per_stage, int lane, int wm, int wn) {
-  using G = StageGeom<BK>;
-  constexpr int KS = BK / 16;  // MFMA sub-steps per stage
-  // nothing of the lgkm class (scalar loads included) is pending on entry, so
-  // the waits before each sub-step's MFMAs can count the LDS reads in order
-  __builtin_amdgcn_s_waitcnt(kWaitLgkm0);
-  for (int kt = 0; kt < KT; ++kt) {
-    // stage kt has landed once only the newer stages issued so far are pending
-    const int newer = KT - 1 - kt < STAGES - 2 ? KT - 1 - kt : STAGES - 2;
-    wait_loads(newer * per_stage);
-    __builtin_amdgcn_s_barrier();
-    const char* sa = smem + (kt % STAGES) * Loader::STAGE_BYTES;
-    const char* sb = sa + BM * G::ROW_BYTES;
-    if constexpr (F > 0) {
-      // fragments in two register sets: sub-step kk + 1 is read while the
-      // MFMAs of sub-step kk run
-      bf16x8 af[2][F], bfr[2][FN];
-      auto frag = [&](int kk, int b) __attribute__((always_inline)) {
-        const int fo = G::frag_offset(lane, kk);
-#pragma unroll
-        for (int i = 0; i < F; ++i)
-          af[b][i] = *(const bf16x8*)(sa + (wm * WM + i * 32) * G::ROW_BYTES + fo);
-#pragma unroll
-        for (int j = 0; j < FN; ++j)
-          bfr[b][j] = *(const bf16x8*)(sb + (wn * WN + j * 32) * G::ROW_BYTES + fo);
-      };
-      frag(0, 0);  // ahead of the next stage's loads, so the first MFMAs start sooner
-      if (kt + STAGES - 1 < KT)
-        ld.template issue<kNt>(smem, kt + STAGES - 1, (kt + STAGES - 1) % STAGES);
-#pragma unroll
-      for (int kk = 0; kk < KS; ++kk) {
-        if (kk + 1 < KS) frag(kk + 1, (kk + 1) & 1);
-        // keeps the compiler from sinking those reads below this sub-step's MFMAs
-        __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-        for (int i = 0; i < F; ++i)
-#pragma unroll
-          for (int j = 0; j < FN; ++j)
-            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(bfr[kk & 1][j], af[kk & 1][i],
-                                                                acc[i][j], 0, 0, 0);
-        __builtin_amdgcn_sched_barrier(0);
-      }
-    } else {
-      if (kt + STAGES - 1 < KT)
-        ld.template issue<kNt>(smem, kt + STAGES - 1, (kt + STAGES - 1) % STAGES);
-    }
-    // this stage's LDS reads are complete before any wave refills its buffer
-    __builtin_amdgcn_s_waitcnt(kWaitLgkm0);
-  }
-}
-
-// The K loop of the wide 256 x 256 kernel (two waves per SIMD).
-// Each load instruction holds its wave in issue until the CU's texture unit
-// takes it, at 16-20 cycles per 1 KB; with all eight waves issuing a 64 KB
-// stage at the start of a K step, no wave reached its MFMAs for the first
-// 800-1150 of about 3300 cycles.  So the two waves of a SIMD take different
-// roles.  The second (wave row 1) issues the next step's rows of A at the
-// start of the step; the first (wave row 0), which gets the matrix pipe first
-// and used to wait about 1000 cycles at the barrier, starts its MFMAs at once
-// and issues the weight rows of B two steps ahead once its MFMAs are issued.
-// A stays double-buffered and B triple-buffered (2 x 32 + 3 x 32 KB).  Loader
-// slot q = wave % 4 of a four-wave loader layout covers the same rows in
-// either role.
-template <int F, int FM, int FN, int WM, int WN, int BM, int BK, bool kNt, class Loader>
-__device__ __forceinline__ void k_loop_roles(f32x16 (&acc)[FM][FN], const Loader& ld, char* smem,
-                                             int KT, int lane, int wm, int wn) {
-  using G = StageGeom<BK>;
-  constexpr int KS = BK / 16;
-  const bool a_role = wm != 0;
-  __builtin_amdgcn_s_waitcnt(kWaitLgkm0);
-  for (int kt = 0; kt < KT; ++kt) {
-    // an A wave's newest load is A(kt); a B wave may still have B(kt + 1)
-    // pending behind B(kt)
-    wait_loads(!a_role && kt + 1 < KT ? Loader::LB : 0);
-    __builtin_amdgcn_s_barrier();
-    const char* sa = smem + (kt & 1) * Loader::A_BYTES;
-    const char* sb = smem + 2 * Loader::A_BYTES + (kt % 3) * Loader::B_BYTES;
-    if constexpr (F > 0) {
-      bf16x8 af[2][F], bfr[2][FN];
-      auto frag = [&](int kk, int b) __attribute__((always_inline)) {
-        const int fo = G::frag_offset(lane, kk);
-#pragma unroll
-        for (int i = 0; i < F; ++i)
-          af[b][i] = *(const bf16x8*)(sa + (wm * WM + i * 32) * G::ROW_BYTES + fo);
-#pragma unroll
-        for (int j = 0; j < FN; ++j)
-          bfr[b][j] = *(const bf16x8*)(sb + (wn * WN + j * 32) * G::ROW_BYTES + fo);
-      };
-      frag(0, 0);
-      if (a_role && kt + 1 < KT) ld.issue_a(smem, kt + 1, (kt + 1) & 1);
-#pragma unroll
-      for (int kk = 0; kk < KS; ++kk) {
-        if (kk + 1 < KS) frag(kk + 1, (kk + 1) & 1);
-        __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-        for (int i = 0; i < F; ++i)
-#pragma unroll
-          for (int j = 0; j < FN; ++j)
-            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(bfr[kk & 1][j], af[kk & 1][i],
-                                                                acc[i][j], 0, 0, 0);
-        __builtin_amdgcn_sched_barrier(0);
-      }
-      if (!a_role && kt + 2 < KT) ld.template issue_b<kNt>(smem, kt + 2, (kt + 2) % 3);
-    } else {
-      if (a_role && kt + 1 < KT) ld.issue_a(smem, kt + 1, (kt + 1) & 1);
-      if (!a_role && kt + 2 < KT) ld.template issue_b<kNt>(smem, kt + 2, (kt + 2) % 3);
-    }
-    __builtin_amdgcn_s_waitcnt(kWaitLgkm0);
-  }
-}
-
-// K loop of a tile on the wide path: the first STAGES - 1 stages, then
-// k_loop over the 32-row blocks of this wave's band that hold rows of the
-// tile.  Blocks past them feed only outputs that are never stored, so a wide
-// tile skips their MFMAs (a band of 1 or 2 live blocks runs the 1- or 2-block
-// loop, 3 runs the full one).  A one-block band always runs its MFMAs: a
-// wave-uniform branch there measured slower than the wasted work.
-// (kRoles: the wide kernel's role split, k_loop_roles.)
-template <int FM, int FN, int WM, int WN, int BM, int BK, int STAGES, bool kNt, bool kRoles,
-          class Loader>
-__device__ __forceinline__ void wide_k(f32x16 (&acc)[FM][FN], const Loader& ld, char* smem, int KT,
-                                       int per_stage, int lane, int wm, int wn, int rows) {
-  if constexpr (kRoles) {
-    // KT >= 1: H and I are positive multiples of 64 (checked at the boundary)
-    if (wm != 0) {
-      ld.issue_a(smem, 0, 0);
-    } else {
-      ld.template issue_b<kNt>(smem, 0, 0);
-      if (1 < KT) ld.template issue_b<kNt>(smem, 1, 1);
-    }
-  } else {
-#pragma unroll
-    for (int s = 0; s < STAGES - 1; ++s)
-      if (s < KT) ld.template issue<kNt>(smem, s, s);
-  }
-  const int band_rows = rows - wm * WM;
-  const int fm_live = band_rows <= 0 ? 0 : (band_rows + 31) / 32;
-#define MOE_K_LOOP(F)                                                                              \
-  do {                                                                                             \
-    if constexpr (kRoles)                                                                          \
-      k_loop_roles<F, FM, FN, WM, WN, BM, BK, kNt, Loader>(acc, ld, smem, KT, lane, wm, wn);       \
-    else                                                                                           \
-      k_loop<F, FM, FN, WM, WN, BM, BK, STAGES, kNt, Loader>(acc, ld, smem, KT, per_stage, lane,   \
-                                                             wm, wn);                              \
-  } while (0)
-  if constexpr (FM == 1) {
-    MOE_K_LOOP(1);
-  } else {
-    if (fm_live > 2)
-      MOE_K_LOOP(FM);
-    else if (fm_live == 2)
-      MOE_K_LOOP(2);
-    else if (fm_live == 1)
-      MOE_K_LOOP(1);
-    else
-      MOE_K_LOOP(0);
-  }
-#undef MOE_K_LOOP
-}
-
-// MFMAs of one compact stage at sa (rows of A, then B): the wave's F 32-row
-// blocks from row0 against its FN 32-column blocks, the fragments of each
-// 16-deep sub-step read right before its MFMAs.
-template <int F, int SROWS, int FM, int FN, int WN, int BK, class Loader>
-__device__ __forceinline__ void compact_mfma(f32x16 (&acc)[FM][FN], const char* sa, int lane,
-                                             int wn, int row0) {
-  using G = StageGeom<BK>;
-  static_assert(F <= FM, "band blocks");
-  if constexpr (F > 0) {
-    const char* sb = sa + Loader::template small_a<SROWS>();
-#pragma unroll
-    for (int kk = 0; kk < BK / 16; ++kk) {
-      const int fo = G::frag_offset(lane, kk);
-      bf16x8 af[F], bfr[FN];
-#pragma unroll
-      for (int i = 0; i < F; ++i)
-        af[i] = *(const bf16x8*)(sa + (row0 + i * 32) * G::ROW_BYTES + fo);
-#pragma unroll
-      for (int j = 0; j < FN; ++j)
-        bfr[j] = *(const bf16x8*)(sb + (wn * WN + j * 32) * G::ROW_BYTES + fo);
-#pragma unroll
-      for (int i = 0; i < F; ++i)
-#pragma unroll
-        for (int j = 0; j < FN; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(bfr[j], af[i], acc[i][j], 0, 0, 0);
-    }
-  }
-}
-
-// The K loop of a tile with at most SROWS (32, 64, 128 or 160) rows: such a
-// tile (a small expert's only m-tile) is bound by streaming its B panel rather
-// than by MFMAs, so it uses the compact stage layout and SSTAGES stages
-// (SSTAGES - 1 in flight) to keep more weight bytes in flight.  The wave holds
-// F 32-row blocks of the tile's rows starting at row0 (its band); a wave with
-// F = 0 only loads and joins the barriers.  (Reading the next sub-step's
-// fragments during the current MFMAs, as k_loop does, measured no faster here.)
-template <int F, int SROWS, int SSTAGES, int FM, int FN, int WN, int BK, bool kNt, class Loader>
-__device__ __forceinline__ void k_loop_small(f32x16 (&acc)[FM][FN], const Loader& ld, char* smem,
-                                             int KT, int per_stage, int lane, int wn, int row0) {
-  constexpr int STAGE = Loader::template small_stage<SROWS>();
-#pragma unroll
-  for (int s = 0; s < SSTAGES - 1; ++s)
-    if (s < KT) ld.template issue_small<SROWS, kNt>(smem, s, s);
-  for (int kt = 0; kt < KT; ++kt) {
-    const int newer = KT - 1 - kt < SSTAGES - 2 ? KT - 1 - kt : SSTAGES - 2;
-    wait_loads(newer * per_stage);
-    __builtin_amdgcn_s_barrier();
-    if (kt + SSTAGES - 1 < KT)
-      ld.template issue_small<SROWS, kNt>(smem, kt + SSTAGES - 1, (kt + SSTAGES - 1) % SSTAGES);
-    compact_mfma<F, SROWS, FM, FN, WN, BK, Loader>(acc, smem + (kt % SSTAGES) * STAGE, lane, wn,
-                                                   row0);
-    __builtin_amdgcn_s_waitcnt(kWaitLgkm0);
-  }
-}
-
 // kLoop: the workgroup takes tile after tile of its XCD's sequence (launched
 // when the grid is capped below the tile bound); otherwise exactly one.
-template <bool kGateUp, bool kSaveGU, int BM, int BN, int WAVES_M, int WAVES_N, int BK,
+template <bool kGateUp, bool kSaveGU, int BM, int BN, int WAVES_M, int WAVES_N, int SB,
           int STAGES, bool kBuf, bool kLoop>
 __global__ void __launch_bounds__(64 * WAVES_M * WAVES_N) grouped_gemm_bf16(GemmArgs a) {
   constexpr int NW = WAVES_M * WAVES_N;
   constexpr int WM = BM / WAVES_M, WN = BN / WAVES_N;
   constexpr int FM = WM / 32, FN = WN / 32;
-  using Loader = TileLoader<kGateUp, BM, BN, NW, WN, BK, kBuf>;
+  using Loader = TileLoader<MmaBf16, kGateUp, BM, BN, NW, WN, SB, kBuf>;
   // the wide kernel splits the loads by wave role (k_loop_roles)
   constexpr bool kRoles = NW == 8;
-  using RoleLoader = TileLoader<kGateUp, BM, BN, kRoles ? NW / 2 : NW, WN, BK, kBuf>;
+  using RoleLoader =
+      TileLoader<MmaBf16, kGateUp, BM, BN, kRoles ? NW / 2 : NW, WN, SB, kBuf>;
   static_assert(WM % 32 == 0 && WN % 32 == 0, "wave tile");
   static_assert(!kGateUp || WN % 64 == 0, "gate/up halves");
   static_assert(STAGES >= 2, "pipeline depth");
@@ -714,7 +260,7 @@ __global__ void __launch_bounds__(64 * WAVES_M * WAVES_N) grouped_gemm_bf16(Gemm
 #pragma unroll
       for (int j = 0; j < FN; ++j) acc[i][j] = f32x16{};
 
-    const int KT = a.K / BK;
+    const int KT = (int)(a.row_bytes / SB);
     // tiles of at most 32, 64, 128 or 160 rows: three compact stages (a fourth
     // stage for the 32-row tiles, in 16 KB more LDS, measured no faster; the
     // 128-row case, 144 KB, took the DeepSeek-V3-shaped layer's gate/up from 3.18
@@ -731,10 +277,10 @@ __global__ void __launch_bounds__(64 * WAVES_M * WAVES_N) grouped_gemm_bf16(Gemm
   do {                                                                                           \
     constexpr int F0 = compact_f0(SR, kNt), F1 = compact_f1(SR, kNt);                            \
     if (wm == 0)                                                                                 \
-      k_loop_small<F0, SR, 3, FM, FN, WN, BK, kNt, Loader>(acc, ld, smem, KT, per_stage, lane,   \
+      k_loop_small<F0, SR, 3, FM, FN, WN, SB, kNt, Loader>(acc, ld, smem, KT, per_stage, lane,   \
                                                            wn, 0);                               \
     else                                                                                         \
-      k_loop_small<F1, SR, 3, FM, FN, WN, BK, kNt, Loader>(acc, ld, smem, KT, per_stage, lane,   \
+      k_loop_small<F1, SR, 3, FM, FN, WN, SB, kNt, Loader>(acc, ld, smem, KT, per_stage, lane,   \
                                                            wn, F0 * 32);                         \
   } while (0)
     if (kSmallPath && tr.rows <= 160) {
@@ -754,13 +300,13 @@ __global__ void __launch_bounds__(64 * WAVES_M * WAVES_N) grouped_gemm_bf16(Gemm
     } else if constexpr (kRoles) {
       RoleLoader ld;
       ld.init(a, tr, nt, lane, wave % (NW / 2));
-      wide_k<FM, FN, WM, WN, BM, BK, STAGES, kNt, true, RoleLoader>(acc, ld, smem, KT, 0, lane, wm,
+      wide_k<FM, FN, WM, WN, BM, SB, STAGES, kNt, true, RoleLoader>(acc, ld, smem, KT, 0, lane, wm,
                                                                     wn, tr.rows);
     } else {
       Loader ld;
       ld.init(a, tr, nt, lane, wave);
       const int per_stage = ld.live_a + Loader::LB;
-      wide_k<FM, FN, WM, WN, BM, BK, STAGES, kNt, false, Loader>(acc, ld, smem, KT, per_stage, lane,
+      wide_k<FM, FN, WM, WN, BM, SB, STAGES, kNt, false, Loader>(acc, ld, smem, KT, per_stage, lane,
                                                                  wm, wn, tr.rows);
     }
 #undef MOE_K_SMALL
@@ -807,7 +353,7 @@ enum Instance { kAuto = 0, kWide = 1, kNarrow = 2 };
 // weight streaming.
 bool prefer_wide(int64_t rows_bound) { return rows_bound >= 4096; }
 
-template <bool kGateUp, bool kSaveGU, int BM, int BN, int WM_, int WN_, int BK, int ST,
+template <bool kGateUp, bool kSaveGU, int BM, int BN, int WM_, int WN_, int SB, int ST,
           bool kBuf>
 hipError_t launch_instance(GemmArgs a, const Shape& s, int64_t rows_bound, hipStream_t st) {
   constexpr int threads = 64 * WM_ * WN_;
@@ -828,12 +374,12 @@ hipError_t launch_instance(GemmArgs a, const Shape& s, int64_t rows_bound, hipSt
   if constexpr (BM == 256 && kBuf) {
     const int64_t cap = 8 * std::max<int64_t>(128, 2 * ((rows_bound / BM + 7) / 8) * a.n_tiles);
     if (2 * cap < grid) {
-      hipLaunchKernelGGL((grouped_gemm_bf16<kGateUp, kSaveGU, BM, BN, WM_, WN_, BK, ST, kBuf, true>),
+      hipLaunchKernelGGL((grouped_gemm_bf16<kGateUp, kSaveGU, BM, BN, WM_, WN_, SB, ST, kBuf, true>),
                          dim3((unsigned)cap), dim3(threads), 0, st, a);
       return hipGetLastError();
     }
   }
-  hipLaunchKernelGGL((grouped_gemm_bf16<kGateUp, kSaveGU, BM, BN, WM_, WN_, BK, ST, kBuf, false>),
+  hipLaunchKernelGGL((grouped_gemm_bf16<kGateUp, kSaveGU, BM, BN, WM_, WN_, SB, ST, kBuf, false>),
                      dim3((unsigned)grid), dim3(threads), 0, st, a);
   return hipGetLastError();
 }
@@ -846,8 +392,8 @@ hipError_t launch_kind(int inst, GemmArgs a, const Shape& s, int64_t rows_bound,
     inst = prefer_wide(rows_bound) ? kWide : kNarrow;
   }
   if (inst == kWide && wide_ok)
-    return launch_instance<kGateUp, kSaveGU, 256, 256, 2, 4, 64, 2, kBuf>(a, s, rows_bound, st);
-  return launch_instance<kGateUp, kSaveGU, 64, 128, 2, 2, 64, 2, kBuf>(a, s, rows_bound, st);
+    return launch_instance<kGateUp, kSaveGU, 256, 256, 2, 4, 128, 2, kBuf>(a, s, rows_bound, st);
+  return launch_instance<kGateUp, kSaveGU, 64, 128, 2, 2, 128, 2, kBuf>(a, s, rows_bound, st);
 }
 
 template <bool kGateUp, bool kSaveGU>
@@ -862,10 +408,10 @@ hipError_t launch_kind(bool buf, int inst, GemmArgs a, const Shape& s, int64_t r
 // by the launch's rows) must lie within 4 GiB above the lower base, and each
 // expert's weight block within 4 GiB of its start.  Sets a.a_base.
 bool descriptor_loads_fit(GemmArgs& a, const Shape& s, int64_t rows_bound) {
-  const uint16_t* a1 = a.a_split ? a.A[1] : a.A[0];
-  a.a_base = (const char*)std::min(a.A[0], a1);
-  return rows_fit_4g(a.A[0], a1, a.gather[0] ? s.T : rows_bound, a.K) &&
-         (uint64_t)a.b_expert_stride * 2 < ((uint64_t)1 << 32);
+  const char* a1 = a.a_split ? a.A[1] : a.A[0];
+  a.a_base = std::min(a.A[0], a1);
+  return rows_fit_4g(a.A[0], a1, a.gather[0] ? s.T : rows_bound, a.row_bytes / 2) &&
+         (uint64_t)a.b_expert_bytes < ((uint64_t)1 << 32);
 }
 
 hipError_t launch(bool gate_up, const Shape& s, const GroupedIO& io, const void* B,
@@ -873,8 +419,8 @@ hipError_t launch(bool gate_up, const Shape& s, const GroupedIO& io, const void*
   const int64_t rows_bound = io.rows_bound;
   if (rows_bound <= 0) return hipSuccess;
   GemmArgs a{};
-  a.A[0] = (const uint16_t*)io.a[0];
-  a.A[1] = (const uint16_t*)(io.a_split ? io.a[1] : io.a[0]);
+  a.A[0] = (const char*)io.a[0];
+  a.A[1] = (const char*)(io.a_split ? io.a[1] : io.a[0]);
   a.C[0] = (uint16_t*)io.c[0];
   a.C[1] = (uint16_t*)(io.c_split ? io.c[1] : io.c[0]);
   a.off0 = io.off[0];
@@ -885,23 +431,23 @@ hipError_t launch(bool gate_up, const Shape& s, const GroupedIO& io, const void*
   a.gather[0] = gate_up ? io.gather[0] : nullptr;
   a.gather[1] = gate_up && io.off[1] ? io.gather[1] : a.gather[0];
   a.gather_k = io.gather_k;
-  a.B = (const uint16_t*)B;
+  a.B = (const char*)B;
   a.E = s.E;
   a.I = s.I;
   const int inst = MOE_GEMM_FORCE;
   if (gate_up) {
-    a.K = s.H;
+    a.row_bytes = (int64_t)s.H * 2;
     a.ncols = s.I;
-    a.b_expert_stride = (int64_t)2 * s.I * s.H;
+    a.b_expert_bytes = (int64_t)2 * s.I * s.H * 2;
     // the backward's recompute also saves g and u (its own instance, so the
     // forward kernel keeps its registers)
     const bool buf = descriptor_loads_fit(a, s, rows_bound);
     if (a.gu) return launch_kind<true, true>(buf, inst, a, s, rows_bound, st);
     return launch_kind<true, false>(buf, inst, a, s, rows_bound, st);
   }
-  a.K = s.I;
+  a.row_bytes = (int64_t)s.I * 2;
   a.ncols = s.H;
-  a.b_expert_stride = (int64_t)s.H * s.I;
+  a.b_expert_bytes = (int64_t)s.H * s.I * 2;
   const bool buf = descriptor_loads_fit(a, s, rows_bound);
   return launch_kind<false, false>(buf, inst, a, s, rows_bound, st);
 }

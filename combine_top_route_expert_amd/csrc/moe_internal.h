@@ -197,6 +197,15 @@ hipError_t launch_gate_up_f32(const Shape& s, const GroupedIO& io, const void* w
                               hipStream_t st);
 hipError_t launch_down_f32(const Shape& s, const GroupedIO& io, const void* w_down,
                            hipStream_t st);
+// 8-bit integer products (gemm_i8.hip): A and B hold int8 values, gate_up always
+// gathers its rows (a_scale: one per token), down reads joint rows (a_scale: one
+// per joint row); b_scale has one per row of each expert's B.  C in the shape's
+// dtype.
+constexpr int kQuantMaxK = 131008;  // 128 * 128 * K products fit an int32 sum
+hipError_t launch_gate_up_i8(const Shape& s, const GroupedIO& io, const float* a_scale,
+                             const void* w_gate_up, const float* w_scale, hipStream_t st);
+hipError_t launch_down_i8(const Shape& s, const GroupedIO& io, const float* a_scale,
+                          const void* w_down, const float* w_scale, hipStream_t st);
 
 // ---- small device helpers ----------------------------------------------------
 // A 16-byte vector of a row: eight bf16 or four fp32 elements.

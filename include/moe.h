@@ -486,6 +486,78 @@ moe_status moe_layer_norm_backward(const moe_shape* shape, const void* grad_y, c
 moe_status moe_quantize_rows(int64_t rows, int64_t cols, int32_t dtype, const void* x, int8_t* q,
                              float* scale, hipStream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * The layer with 8-bit integer experts (inference; there is no backward).
+ *
+ * Activations and weights are int8 with one float32 scale per row
+ * (moe_quantize_rows): hidden rows per token, act rows per assignment, weights
+ * per output channel.
+ *   hidden_q [T][H], hidden_scale [T]
+ *   w_gate_up_q [E][2I][H], w_gate_up_scale [E][2I]
+ *   w_down_q    [E][H][I],  w_down_scale    [E][H]
+ * Products are summed exactly in int32, scaled in fp32 (token, then channel).
+ * dtype is that of act, y and out: act is rounded to it once before it is
+ * quantised, y and out once each, as in the bf16 layer.  Rows, offsets, src_row,
+ * pairs and dropped ids are those of the calls above, and results depend neither on N
+ * nor on the entry point used.  A token whose scale is NaN (moe_quantize_rows of
+ * a row with an infinity or a NaN) gives NaN in its own output row only.
+ * Limits: H % 64 == 0 and I % 64 == 0 for every dtype, H and I <= 131008
+ * (MOE_ERR_UNSUPPORTED otherwise).  MOE_BF16 is the tuned form; MOE_F32 keeps
+ * act, y and out in float32 and always runs the small tile.
+ * --------------------------------------------------------------------------- */
+
+/*
+ * First expert product of chunks chunk and chunk + 1 with the SwiGLU epilogue
+ * (moe_expert_gate_up_gather_pair in 8 bits): row r of chunk c is
+ * hidden_q[src_row[t0_c*k + r] / k]; act as there: the pair's joint
+ * [rows0 + rows1][I] buffer in the shape's dtype.  A lone or last chunk is the
+ * pair whose second chunk is empty.
+ */
+moe_status moe_quant_gate_up_gather_pair(const moe_shape* shape, int32_t chunk,
+                                         const int8_t* hidden_q, const float* hidden_scale,
+                                         const int32_t* src_row, const int32_t* offsets,
+                                         const int8_t* w_gate_up_q, const float* w_gate_up_scale,
+                                         void* act, hipStream_t stream);
+
+/*
+ * moe_quantize_rows over the pair's valid act rows (their number is read on the
+ * device): act joint [rows0 + rows1][I] of the shape's dtype, act_q the same in
+ * int8, act_scale [rows0 + rows1].  Rows past the valid ones are not written.
+ */
+moe_status moe_quant_act_pair(const moe_shape* shape, int32_t chunk, const void* act,
+                              const int32_t* offsets, int8_t* act_q, float* act_scale,
+                              hipStream_t stream);
+
+/*
+ * Second expert product (moe_expert_down_pair in 8 bits): act_q and act_scale
+ * are the pair's joint rows; y0 / y1 receive the two chunks' rows at their
+ * chunk-local positions (y1 ignored, may be null, when the second chunk does
+ * not exist or is empty).  Rows past each chunk's valid rows are not written.
+ */
+moe_status moe_quant_down_pair(const moe_shape* shape, int32_t chunk, const int8_t* act_q,
+                               const float* act_scale, const int32_t* offsets,
+                               const int8_t* w_down_q, const float* w_down_scale, void* y0,
+                               void* y1, hipStream_t stream);
+
+/* Bytes of workspace moe_quant_forward needs: the metadata plus min(N,2) slots
+ * of ceil(T/N)*k rows of (H + I) elements, I bytes and a scale.  Host-only. */
+moe_status moe_quant_workspace_size(const moe_shape* shape, size_t* bytes);
+
+/*
+ * The whole layer on quantised hidden rows (from moe_quantize_rows or
+ * moe_layer_norm_quantize): metadata once, then per chunk pair gate_up, the act
+ * quantiser, down and the weighted combine, all on `stream`; capturable in a HIP
+ * graph.  out [T][H] in the shape's dtype; dev_error as for
+ * moe_chunked_forward (nullable); ws must hold moe_quant_workspace_size bytes and
+ * not be shared by calls, or by graphs that hold them, that may overlap.
+ */
+moe_status moe_quant_forward(const moe_shape* shape, const int8_t* hidden_q,
+                             const float* hidden_scale, const int32_t* top_k_index,
+                             const float* top_k_weights, const int8_t* w_gate_up_q,
+                             const float* w_gate_up_scale, const int8_t* w_down_q,
+                             const float* w_down_scale, void* out, int32_t* dev_error, void* ws,
+                             size_t ws_bytes, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
