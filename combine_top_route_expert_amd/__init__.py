@@ -481,53 +481,73 @@ class _OnDevice:
     """Pointers of one call's tensors, which must all live on one device; the call is made with
     that device current, on the given stream or the device's current one."""
 
+    __slots__ = ("index",)
+
     def __init__(self):
-        self.device = None
+        self.index = -1
 
     def __call__(self, t, dtype, min_numel: int, name: str) -> Optional[int]:
-        p = _ptr(t, dtype, min_numel, name)
-        if t is not None:
-            if self.device is None:
-                self.device = t.device
-            elif t.device != self.device:
-                raise ValueError(f"{name} is on {t.device}, the tensors before it on {self.device}")
-        return p
+        # one test of everything for a good tensor; _ptr words what is wrong with another
+        if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype
+                and t.is_contiguous() and t.numel() >= min_numel):
+            p = _ptr(t, dtype, min_numel, name)
+            if t is None:
+                return p
+        index = t.get_device()
+        if index != self.index:
+            if self.index >= 0:
+                raise ValueError(f"{name} is on {t.device}, the tensors before it on "
+                                 f"cuda:{self.index}")
+            self.index = index
+        return t.data_ptr()
 
     def optional(self, t, dtype, min_numel: int, name: str) -> Optional[int]:
         return None if t is None else self(t, dtype, min_numel, name)
 
     def call(self, fn: str, stream, *args) -> None:
-        dev = self.device
-        if isinstance(stream, torch.cuda.Stream) and dev is not None and stream.device != dev:
-            raise ValueError(f"stream is on {stream.device}, the tensors on {dev}")
-        f = getattr(load_library(), fn)
-        if dev is None or dev.index == torch.cuda.current_device():
-            _check(fn, f(*args, _stream(stream)))
+        f = getattr(_lib or load_library(), fn)
+        if self.index < 0 or self.index == torch.cuda.current_device():
+            code = f(*args, self._stream(stream))
         else:
-            with torch.cuda.device(dev):
-                _check(fn, f(*args, _stream(stream)))
+            with torch.cuda.device(self.index):
+                code = f(*args, self._stream(stream))
+        if code != 0:
+            raise MoeError(fn, code)
+
+    def _stream(self, stream) -> int:
+        if stream is None:
+            if self.index < 0:
+                return torch.cuda.current_stream().cuda_stream
+            return torch._C._cuda_getCurrentRawStream(self.index)
+        if isinstance(stream, int):
+            return stream
+        if self.index >= 0 and stream.device.index != self.index:
+            raise ValueError(f"stream is on {stream.device}, the tensors on cuda:{self.index}")
+        return stream.cuda_stream
 
 
 def moe_layer_norm(shape: moe_shape, x, residual, weight, bias, eps: float, sum_out, y, mean=None,
                    rstd=None, stream=None) -> None:
     """y = layer norm of x (or of x + residual, which goes to sum_out); weight, bias, mean and rstd
     are float32 and may be None."""
-    on, dt, f32, n = _OnDevice(), shape.torch_dtype, torch.float32, shape.T * shape.H
+    on, dt, f32, T, H = _OnDevice(), shape.torch_dtype, torch.float32, shape.T, shape.H
+    n = T * H
     on.call("moe_layer_norm", stream, ctypes.byref(shape), on(x, dt, n, "x"),
-            on.optional(residual, dt, n, "residual"), on.optional(weight, f32, shape.H, "weight"),
-            on.optional(bias, f32, shape.H, "bias"), eps, on.optional(sum_out, dt, n, "sum"),
-            on(y, dt, n, "y"), on.optional(mean, f32, shape.T, "mean"),
-            on.optional(rstd, f32, shape.T, "rstd"))
+            on.optional(residual, dt, n, "residual"), on.optional(weight, f32, H, "weight"),
+            on.optional(bias, f32, H, "bias"), eps, on.optional(sum_out, dt, n, "sum"),
+            on(y, dt, n, "y"), on.optional(mean, f32, T, "mean"),
+            on.optional(rstd, f32, T, "rstd"))
 
 
 def moe_layer_norm_quantize(shape: moe_shape, x, residual, weight, bias, eps: float, sum_out, y, q,
                             scale, stream=None) -> None:
     """moe_layer_norm whose rows are also quantised into q (int8) and scale; y may be None."""
-    on, dt, f32, n = _OnDevice(), shape.torch_dtype, torch.float32, shape.T * shape.H
+    on, dt, f32, T, H = _OnDevice(), shape.torch_dtype, torch.float32, shape.T, shape.H
+    n = T * H
     on.call("moe_layer_norm_quantize", stream, ctypes.byref(shape), on(x, dt, n, "x"),
-            on.optional(residual, dt, n, "residual"), on.optional(weight, f32, shape.H, "weight"),
-            on.optional(bias, f32, shape.H, "bias"), eps, on.optional(sum_out, dt, n, "sum"),
-            on.optional(y, dt, n, "y"), on(q, torch.int8, n, "q"), on(scale, f32, shape.T, "scale"))
+            on.optional(residual, dt, n, "residual"), on.optional(weight, f32, H, "weight"),
+            on.optional(bias, f32, H, "bias"), eps, on.optional(sum_out, dt, n, "sum"),
+            on.optional(y, dt, n, "y"), on(q, torch.int8, n, "q"), on(scale, f32, T, "scale"))
 
 
 def moe_layer_norm_backward_workspace_size(shape: moe_shape) -> int:
@@ -542,12 +562,13 @@ def moe_layer_norm_backward(shape: moe_shape, grad_y, x, weight, mean, rstd, gra
                             grad_weight=None, grad_bias=None, ws=None, stream=None) -> None:
     """Gradient of moe_layer_norm: x holds the normalised rows (sum_out where there was a
     residual); grad_sum, grad_weight and grad_bias may be None."""
-    on, dt, f32, n = _OnDevice(), shape.torch_dtype, torch.float32, shape.T * shape.H
+    on, dt, f32, T, H = _OnDevice(), shape.torch_dtype, torch.float32, shape.T, shape.H
+    n = T * H
     args = (on(grad_y, dt, n, "grad_y"), on(x, dt, n, "x"),
-            on.optional(weight, f32, shape.H, "weight"), on(mean, f32, shape.T, "mean"),
-            on(rstd, f32, shape.T, "rstd"), on.optional(grad_sum, dt, n, "grad_sum"),
-            on(grad_x, dt, n, "grad_x"), on.optional(grad_weight, f32, shape.H, "grad_weight"),
-            on.optional(grad_bias, f32, shape.H, "grad_bias"))
+            on.optional(weight, f32, H, "weight"), on(mean, f32, T, "mean"),
+            on(rstd, f32, T, "rstd"), on.optional(grad_sum, dt, n, "grad_sum"),
+            on(grad_x, dt, n, "grad_x"), on.optional(grad_weight, f32, H, "grad_weight"),
+            on.optional(grad_bias, f32, H, "grad_bias"))
     params = grad_weight is not None or grad_bias is not None
     need = moe_layer_norm_backward_workspace_size(shape) if params else 0
     wp = on(ws, torch.uint8, need, "ws")

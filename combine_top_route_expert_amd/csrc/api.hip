@@ -1060,9 +1060,10 @@ hipError_t quantize_act(const Shape& s, const int32_t* off0, const int32_t* off1
 }
 
 // gate_up of a pair: hidden rows gathered through the two chunks' slices of src_row.
-GroupedIO quant_gate_up_io(const Shape& s, int chunk, const int8_t* hidden_q,
-                           const int32_t* src_row, const int32_t* off0, const int32_t* off1,
-                           int64_t rows, void* act) {
+hipError_t quant_gate_up(const Shape& s, int chunk, const int8_t* hidden_q, const float* scale,
+                         const int32_t* src_row, const int32_t* off0, const int32_t* off1,
+                         int64_t rows, const int8_t* w, const float* w_scale, void* act,
+                         hipStream_t st) {
   int t0, t1, u0 = 0, u1 = 0;
   chunk_tokens(s, chunk, &t0, &t1);
   if (chunk + 1 < s.N) chunk_tokens(s, chunk + 1, &u0, &u1);
@@ -1075,11 +1076,12 @@ GroupedIO quant_gate_up_io(const Shape& s, int chunk, const int8_t* hidden_q,
   io.gather[1] = src_row + (size_t)u0 * s.k;
   io.gather_k = s.k;
   io.c[0] = act;
-  return io;
+  return launch_gate_up_i8(s, io, scale, w, w_scale, st);
 }
 
-GroupedIO quant_down_io(const int8_t* act_q, const int32_t* off0, const int32_t* off1,
-                        int64_t rows, void* y0, void* y1) {
+hipError_t quant_down(const Shape& s, const int8_t* act_q, const float* scale,
+                      const int32_t* off0, const int32_t* off1, int64_t rows, const int8_t* w,
+                      const float* w_scale, void* y0, void* y1, hipStream_t st) {
   GroupedIO io{};
   io.off[0] = off0;
   io.off[1] = off1;
@@ -1088,7 +1090,7 @@ GroupedIO quant_down_io(const int8_t* act_q, const int32_t* off0, const int32_t*
   io.c[0] = y0;
   io.c[1] = y1;
   io.c_split = true;
-  return io;
+  return launch_down_i8(s, io, scale, w, w_scale, st);
 }
 
 }  // namespace
@@ -1107,9 +1109,8 @@ moe_status moe_quant_gate_up_gather_pair(const moe_shape* shape, int32_t chunk,
   if (!buf_ok(hidden_q, 1) || !scale_ok(hidden_scale) || !src_row || !aligned(src_row, 4) ||
       !buf_ok(w_gate_up_q, 1) || !scale_ok(w_gate_up_scale) || !buf_ok(act, 1))
     return MOE_ERR_INVALID_ARG;
-  return hip_status(launch_gate_up_i8(
-      s, quant_gate_up_io(s, chunk, hidden_q, src_row, off0, off1, rows0 + rows1, act),
-      hidden_scale, w_gate_up_q, w_gate_up_scale, stream));
+  return hip_status(quant_gate_up(s, chunk, hidden_q, hidden_scale, src_row, off0, off1,
+                                  rows0 + rows1, w_gate_up_q, w_gate_up_scale, act, stream));
 }
 
 moe_status moe_quant_act_pair(const moe_shape* shape, int32_t chunk, const void* act,
@@ -1137,8 +1138,8 @@ moe_status moe_quant_down_pair(const moe_shape* shape, int32_t chunk, const int8
   if (!buf_ok(act_q, 1) || !scale_ok(act_scale) || !buf_ok(w_down_q, 1) ||
       !scale_ok(w_down_scale) || !buf_ok(y0, rows0) || !buf_ok(y1, rows1))
     return MOE_ERR_INVALID_ARG;
-  return hip_status(launch_down_i8(s, quant_down_io(act_q, off0, off1, rows0 + rows1, y0, y1),
-                                   act_scale, w_down_q, w_down_scale, stream));
+  return hip_status(quant_down(s, act_q, act_scale, off0, off1, rows0 + rows1, w_down_q,
+                               w_down_scale, y0, y1, stream));
 }
 
 moe_status moe_quant_workspace_size(const moe_shape* shape, size_t* bytes) {
@@ -1193,12 +1194,12 @@ moe_status moe_quant_forward(const moe_shape* shape, const int8_t* hidden_q,
     const int32_t* off0 = offsets + (size_t)c * (s.E + 1);
     const int32_t* off1 = rows1 > 0 ? off0 + (s.E + 1) : nullptr;
     void *y0 = w + p.y[0], *y1 = rows1 > 0 ? w + p.y[1] : nullptr;
-    he = launch_gate_up_i8(s, quant_gate_up_io(s, c, hidden_q, src_row, off0, off1, rows, act),
-                           hidden_scale, w_gate_up_q, w_gate_up_scale, stream);
+    he = quant_gate_up(s, c, hidden_q, hidden_scale, src_row, off0, off1, rows, w_gate_up_q,
+                       w_gate_up_scale, act, stream);
     if (he == hipSuccess) he = quantize_act(s, off0, off1, rows, act, act_q, act_scale, stream);
     if (he == hipSuccess)
-      he = launch_down_i8(s, quant_down_io(act_q, off0, off1, rows, y0, y1), act_scale, w_down_q,
-                          w_down_scale, stream);
+      he = quant_down(s, act_q, act_scale, off0, off1, rows, w_down_q, w_down_scale, y0, y1,
+                      stream);
     if (he == hipSuccess)
       he = rows1 > 0 ? launch_combine_pair(s, t0, u0, u1, y0, y1, dst_row, top_k_weights, out,
                                            stream)

@@ -13,9 +13,14 @@
 // mean of the squared distances from the mean (a second pass over registers),
 // so a large common offset costs no precision.
 //
-// A row is a wave's (up to 2048 values: four rows to a workgroup, no barrier)
-// or a workgroup's.  Threads take 16-byte vectors round robin, so every load and
-// store of a wave is one contiguous kilobyte.
+// A row takes 64 to 1024 threads of at most 16 values each (up to 1024 values: a
+// wave's row, four to a workgroup, no barrier).  Threads take 16-byte vectors round
+// robin, so every load and store of a wave is one contiguous kilobyte.  32 values
+// per thread: 16384 x 2048 with residual 57.7 against 54.3 us, 4096 x 7168
+// quantising 59.9 against 55.5 us, one token 5.5 against 4.4 us; eight: the same
+// within 1% but 65.6 us quantising.  What one pass reads or writes once is
+// streamed non-temporally (54.3 -> 52 us and 52.8 -> 48.2 us: 5.2 and 4.9 TB/s, against
+// 4.75 of a large device copy).
 #include <algorithm>
 #include <type_traits>
 
@@ -163,7 +168,9 @@ __device__ __forceinline__ void load_param(const float* p, int64_t v, float none
   for (int i = 0; i < kEl; ++i) f[i] = p ? p[v * kEl + i] : none;
 }
 
-// A row: THREADS threads of EPT values each.
+constexpr int kRowValues = 16;  // values of a row per thread
+
+// A row: THREADS threads of kRowValues values each.
 template <int THREADS>
 struct RowOf {
   static constexpr int kPerGroup = THREADS == 64 ? 4 : 1;
@@ -182,10 +189,10 @@ struct RowOf {
 // at most 1024 of them.  More rows go in several launches.
 constexpr int64_t kRowsPerLaunch = 1 << 21;
 
-template <bool kBf16, int THREADS, int EPT, bool kQuant>
+template <bool kBf16, int THREADS, bool kQuant>
 __global__ void __launch_bounds__(RowOf<THREADS>::kGroup) norm_rows(NormIO io, int64_t row0, int64_t rows,
                                                                      int nvec) {
-  constexpr int kEl = kVecEl<kBf16>, VPT = EPT / kEl, NW = THREADS / 64;
+  constexpr int kEl = kVecEl<kBf16>, VPT = kRowValues / kEl, NW = THREADS / 64;
   const int64_t row = row0 + RowOf<THREADS>::row();
   if (row >= rows) return;
   __shared__ float red[3][NW];
@@ -194,12 +201,12 @@ __global__ void __launch_bounds__(RowOf<THREADS>::kGroup) norm_rows(NormIO io, i
   u32x4 xv[VPT], rv[VPT];
 #pragma unroll
   for (int i = 0; i < VPT; ++i)
-    if (i * THREADS + tid < nvec) xv[i] = x[i * THREADS + tid];
+    if (i * THREADS + tid < nvec) xv[i] = __builtin_nontemporal_load(&x[i * THREADS + tid]);
   if (io.residual) {
     const u32x4* r = (const u32x4*)io.residual + row * nvec;
 #pragma unroll
     for (int i = 0; i < VPT; ++i)
-      if (i * THREADS + tid < nvec) rv[i] = r[i * THREADS + tid];
+      if (i * THREADS + tid < nvec) rv[i] = __builtin_nontemporal_load(&r[i * THREADS + tid]);
   }
   float f[VPT][kEl];
   float total = 0.0f;
@@ -216,7 +223,7 @@ __global__ void __launch_bounds__(RowOf<THREADS>::kGroup) norm_rows(NormIO io, i
       // the sum is what later layers read: its statistics are those of the
       // rounded values
       const u32x4 p = pack<kBf16>(f[i]);
-      ((u32x4*)io.sum)[row * nvec + v] = p;
+      __builtin_nontemporal_store(p, &((u32x4*)io.sum)[row * nvec + v]);
       unpack<kBf16>(p, f[i]);
     }
 #pragma unroll
@@ -250,7 +257,7 @@ __global__ void __launch_bounds__(RowOf<THREADS>::kGroup) norm_rows(NormIO io, i
 #pragma unroll
     for (int e = 0; e < kEl; ++e) f[i][e] = __builtin_fmaf(f[i][e] * rstd, w[e], b[e]);
     const u32x4 p = pack<kBf16>(f[i]);
-    if (!kQuant || io.y) ((u32x4*)io.y)[row * nvec + v] = p;
+    if (!kQuant || io.y) __builtin_nontemporal_store(p, &((u32x4*)io.y)[row * nvec + v]);
     if constexpr (kQuant) {
       // quantised from the rounded y: the same bits as the two calls one after
       // the other
@@ -318,18 +325,26 @@ quantize_rows(const u32x4* __restrict__ x, int8_t* __restrict__ q, float* __rest
   }
 }
 
-// Backward.  A workgroup takes rows b, b + gridDim, ...; its threads keep their
-// columns' sums of grad_y xh and grad_y in registers over all its rows and write
-// them once, as row b of the partials ([workgroups][2][H]).  norm_grad_reduce
-// adds those rows in a fixed order: no atomics, the same bits every time.
-// THREADS = 64: a wave's row; the four waves' sums are joined in LDS.
-template <bool kBf16, int THREADS, int EPT>
-__global__ void __launch_bounds__(RowOf<THREADS>::kGroup)
-norm_grad_rows(NormGradIO io, int T, int nvec) {
-  constexpr int kEl = kVecEl<kBf16>, VPT = EPT / kEl, NW = THREADS / 64;
-  constexpr int kPar = RowOf<THREADS>::kPerGroup;
-  __shared__ float red[2][2][NW];
-  const int tid = RowOf<THREADS>::tid();
+// Backward.  A workgroup of 1024 threads holds kPar = 1024 / THREADS rows at a
+// time, rows b kPar + p, p < kPar, then those gridDim kPar further; bf16 rows of up
+// to 8192 values are loaded while those before them are reduced (where the next
+// row fits the 128 registers of a thread).  A thread keeps its columns' sums of
+// grad_y xh and grad_y in registers over all its rows; the kPar groups' sums are
+// joined in LDS in order and written once, as row b of the partials
+// ([workgroups][2][H]).  norm_grad_reduce adds those rows in a fixed order: no
+// atomics, the same bits every time.  4096 x 7168 with grad_sum: 46 + 5 us, 4.7 TB/s;
+// with 512 workgroups of one row each, no loads ahead and partials to match 63 + 12.
+constexpr int kGradThreads = 1024;
+constexpr int kGradGroups = 256;  // one workgroup per CU: the fewest partials
+
+template <bool kBf16, int THREADS>
+__global__ void __launch_bounds__(kGradThreads) norm_grad_rows(NormGradIO io, int T, int nvec) {
+  constexpr int kEl = kVecEl<kBf16>, VPT = kRowValues / kEl, NW = THREADS / 64;
+  constexpr int kPar = kGradThreads / THREADS;
+  constexpr bool kAhead = kBf16 && THREADS < 1024;
+  __shared__ float red[2][kPar][2][NW];
+  const int tid = threadIdx.x % THREADS;
+  const int grp = __builtin_amdgcn_readfirstlane(threadIdx.x / THREADS);
   const float inv_h = 1.0f / (float)(nvec * kEl);
   float w[VPT][kEl], dw[VPT][kEl], db[VPT][kEl];
 #pragma unroll
@@ -340,51 +355,74 @@ norm_grad_rows(NormGradIO io, int T, int nvec) {
     if (v < nvec) load_param<kEl>(io.weight, v, 1.0f, w[i]);
   }
   const int64_t stride = (int64_t)gridDim.x * kPar;
-  int par = 0;
-  for (int64_t row = RowOf<THREADS>::row(); row < T; row += stride, par ^= 1) {
+  u32x4 gv[VPT] = {}, xv[VPT] = {};
+  float mean = 0.0f, rstd = 0.0f;
+  auto fetch = [&](int64_t row) __attribute__((always_inline)) {
+    if (row >= T) return;
     const u32x4* gy = (const u32x4*)io.grad_y + row * nvec;
     const u32x4* x = (const u32x4*)io.x + row * nvec;
-    u32x4 gv[VPT], xv[VPT];
 #pragma unroll
     for (int i = 0; i < VPT; ++i)
       if (i * THREADS + tid < nvec) {
-        gv[i] = gy[i * THREADS + tid];
-        xv[i] = x[i * THREADS + tid];
+        gv[i] = __builtin_nontemporal_load(&gy[i * THREADS + tid]);
+        xv[i] = __builtin_nontemporal_load(&x[i * THREADS + tid]);
       }
-    const float mean = io.mean[row], rstd = io.rstd[row];
-    float s1 = 0.0f, s2 = 0.0f;
+    mean = io.mean[row];
+    rstd = io.rstd[row];
+  };
+  int64_t row = (int64_t)blockIdx.x * kPar + grp;
+  if constexpr (kAhead) fetch(row);
+  // every group takes part in every barrier: the first group's rows end last
+  int par = 0;
+  for (int64_t first = (int64_t)blockIdx.x * kPar; first < T; first += stride, row += stride) {
+    if constexpr (!kAhead) fetch(row);
+    u32x4 g0[VPT], x0[VPT];
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-      if (i * THREADS + tid >= nvec) continue;
-      float g[kEl], s[kEl];
-      unpack<kBf16>(gv[i], g);
-      unpack<kBf16>(xv[i], s);
+      g0[i] = gv[i];
+      x0[i] = xv[i];
+    }
+    const float m = mean, rs = rstd;
+    const bool live = row < T;
+    if constexpr (kAhead) fetch(row + stride);
+    float s1 = 0.0f, s2 = 0.0f;
+    if (live) {
 #pragma unroll
-      for (int e = 0; e < kEl; ++e) {
-        const float xh = (s[e] - mean) * rstd, h = g[e] * w[i][e];
-        s1 += h;
-        s2 = __builtin_fmaf(h, xh, s2);
-        dw[i][e] = __builtin_fmaf(g[e], xh, dw[i][e]);
-        db[i][e] += g[e];
+      for (int i = 0; i < VPT; ++i) {
+        if (i * THREADS + tid >= nvec) continue;
+        float g[kEl], s[kEl];
+        unpack<kBf16>(g0[i], g);
+        unpack<kBf16>(x0[i], s);
+#pragma unroll
+        for (int e = 0; e < kEl; ++e) {
+          const float xh = (s[e] - m) * rs, h = g[e] * w[i][e];
+          s1 += h;
+          s2 = __builtin_fmaf(h, xh, s2);
+          dw[i][e] = __builtin_fmaf(g[e], xh, dw[i][e]);
+          db[i][e] += g[e];
+        }
       }
     }
-    // two slots in turn: a wave can be one row ahead of the slowest, not two
     s1 = wave_sum(s1);
     s2 = wave_sum(s2);
     if constexpr (THREADS > 64) {
-      if ((threadIdx.x & 63) == 0) {
-        red[par][0][threadIdx.x >> 6] = s1;
-        red[par][1][threadIdx.x >> 6] = s2;
+      // two slots in turn: a wave can be one row ahead of the slowest, not two
+      if ((tid & 63) == 0) {
+        red[par][grp][0][tid >> 6] = s1;
+        red[par][grp][1][tid >> 6] = s2;
       }
       __syncthreads();
       s1 = s2 = 0.0f;
 #pragma unroll
       for (int k = 0; k < NW; ++k) {
-        s1 += red[par][0][k];
-        s2 += red[par][1][k];
+        s1 += red[par][grp][0][k];
+        s2 += red[par][grp][1][k];
       }
+      par ^= 1;
     }
+    if (!live) continue;
     const float m1 = s1 * inv_h, m2 = s2 * inv_h;
+    // (loaded here: any earlier it cost the registers of the next row, 46 -> 53 us)
     const u32x4* gs = io.grad_sum ? (const u32x4*)io.grad_sum + row * nvec : nullptr;
     u32x4* gx = (u32x4*)io.grad_x + row * nvec;
 #pragma unroll
@@ -392,46 +430,25 @@ norm_grad_rows(NormGradIO io, int T, int nvec) {
       const int v = i * THREADS + tid;
       if (v >= nvec) continue;
       float g[kEl], s[kEl], o[kEl];
-      unpack<kBf16>(gv[i], g);
-      unpack<kBf16>(xv[i], s);
+      unpack<kBf16>(g0[i], g);
+      unpack<kBf16>(x0[i], s);
       if (gs)
-        unpack<kBf16>(gs[v], o);
+        unpack<kBf16>(__builtin_nontemporal_load(&gs[v]), o);
       else
 #pragma unroll
         for (int e = 0; e < kEl; ++e) o[e] = 0.0f;
 #pragma unroll
       for (int e = 0; e < kEl; ++e) {
-        const float xh = (s[e] - mean) * rstd, h = g[e] * w[i][e];
-        o[e] = __builtin_fmaf(rstd, __builtin_fmaf(-xh, m2, h - m1), o[e]);
+        const float xh = (s[e] - m) * rs, h = g[e] * w[i][e];
+        o[e] = __builtin_fmaf(rs, __builtin_fmaf(-xh, m2, h - m1), o[e]);
       }
-      gx[v] = pack<kBf16>(o);
+      __builtin_nontemporal_store(pack<kBf16>(o), &gx[v]);
     }
   }
   if (!io.partials) return;
   const int H = nvec * kEl;
   float* part = io.partials + (int64_t)blockIdx.x * 2 * H;
-  if constexpr (THREADS == 64) {
-    // wave w adds its sums to those of the waves before it, in turn
-    extern __shared__ float cols[];  // [2][H]
-    const int wave = threadIdx.x >> 6;
-    for (int k = 0; k < kPar; ++k) {
-      if (wave == k) {
-#pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-          const int v = i * 64 + tid;
-          if (v >= nvec) continue;
-#pragma unroll
-          for (int e = 0; e < kEl; ++e) {
-            const int c = v * kEl + e;
-            cols[c] = k ? cols[c] + dw[i][e] : dw[i][e];
-            cols[H + c] = k ? cols[H + c] + db[i][e] : db[i][e];
-          }
-        }
-      }
-      __syncthreads();
-    }
-    for (int c = threadIdx.x; c < 2 * H; c += 256) part[c] = cols[c];
-  } else {
+  if constexpr (kPar == 1) {
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int v = i * THREADS + tid;
@@ -440,6 +457,26 @@ norm_grad_rows(NormGradIO io, int T, int nvec) {
       for (int e = 0; e < kEl; ++e) {
         part[v * kEl + e] = dw[i][e];
         part[H + v * kEl + e] = db[i][e];
+      }
+    }
+  } else {
+    __shared__ float cols[kGradThreads * kRowValues];  // [kPar][H] of one of the two sums
+    for (int which = 0; which < 2; ++which) {
+      if (which) __syncthreads();
+#pragma unroll
+      for (int i = 0; i < VPT; ++i) {
+        const int v = i * THREADS + tid;
+        if (v >= nvec) continue;
+#pragma unroll
+        for (int e = 0; e < kEl; ++e)
+          cols[grp * H + v * kEl + e] = which ? db[i][e] : dw[i][e];
+      }
+      __syncthreads();
+      for (int c = threadIdx.x; c < H; c += kGradThreads) {
+        float sum = cols[c];
+#pragma unroll
+        for (int k = 1; k < kPar; ++k) sum += cols[k * H + c];
+        part[which * H + c] = sum;
       }
     }
   }
@@ -458,6 +495,7 @@ norm_grad_reduce(const float* __restrict__ part, int n, int H, float* __restrict
   const int c = blockIdx.x * 64 + cx * 4;
   float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   if (c < H)
+#pragma unroll 4
     for (int r = g; r < n; r += 16) {
       const float4 p = *(const float4*)(part + ((int64_t)r * 2 + blockIdx.y) * H + c);
       a.x += p.x;
@@ -478,10 +516,17 @@ norm_grad_reduce(const float* __restrict__ part, int n, int H, float* __restrict
   *(float4*)(out + c) = a;
 }
 
+// Threads of a row, by its width.
+int row_threads(int64_t width) {
+  int t = 64;
+  while (t * kRowValues < width) t *= 2;
+  return t;
+}
+
 // Workgroups of norm_grad_rows.
 int norm_grad_groups(const Shape& s) {
-  const int par = s.H <= 2048 ? 4 : 1;
-  return (int)std::min<int64_t>(((int64_t)s.T + par - 1) / par, 512);
+  const int par = kGradThreads / row_threads(s.H);
+  return (int)std::min<int64_t>(((int64_t)s.T + par - 1) / par, kGradGroups);
 }
 
 template <bool kBf16, bool kQuant>
@@ -489,19 +534,16 @@ hipError_t norm_launch(const Shape& s, const NormIO& io, hipStream_t st) {
   const int nvec = s.H / kVecEl<kBf16>;
   for (int64_t r0 = 0; r0 < s.T; r0 += kRowsPerLaunch) {
     const int64_t end = std::min<int64_t>(s.T, r0 + kRowsPerLaunch);
-#define MOE_NORM(THREADS, EPT)                                                             \
-  hipLaunchKernelGGL((norm_rows<kBf16, THREADS, EPT, kQuant>), RowOf<THREADS>::grid(end - r0), \
+#define MOE_NORM(THREADS)                                                                   \
+  hipLaunchKernelGGL((norm_rows<kBf16, THREADS, kQuant>), RowOf<THREADS>::grid(end - r0),   \
                      dim3(RowOf<THREADS>::kGroup), 0, st, io, r0, end, nvec)
-    if (s.H <= 1024)
-      MOE_NORM(64, 16);
-    else if (s.H <= 2048)
-      MOE_NORM(64, 32);
-    else if (s.H <= 4096)
-      MOE_NORM(256, 16);
-    else if (s.H <= 8192)
-      MOE_NORM(256, 32);
-    else
-      MOE_NORM(1024, 16);
+    switch (row_threads(s.H)) {
+      case 64: MOE_NORM(64); break;
+      case 128: MOE_NORM(128); break;
+      case 256: MOE_NORM(256); break;
+      case 512: MOE_NORM(512); break;
+      default: MOE_NORM(1024); break;
+    }
 #undef MOE_NORM
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
@@ -512,20 +554,17 @@ hipError_t norm_launch(const Shape& s, const NormIO& io, hipStream_t st) {
 template <bool kBf16>
 hipError_t norm_grad_launch(const Shape& s, const NormGradIO& io, hipStream_t st) {
   const int nvec = s.H / kVecEl<kBf16>, groups = norm_grad_groups(s);
-#define MOE_NORM_GRAD(THREADS, EPT)                                                              \
-  hipLaunchKernelGGL((norm_grad_rows<kBf16, THREADS, EPT>), dim3((unsigned)groups),              \
-                     dim3(RowOf<THREADS>::kGroup),                                               \
-                     (THREADS == 64 && io.partials ? 2 * (size_t)s.H * 4 : 0), st, io, s.T, nvec)
-  if (s.H <= 1024)
-    MOE_NORM_GRAD(64, 16);
-  else if (s.H <= 2048)
-    MOE_NORM_GRAD(64, 32);
-  else if (s.H <= 4096)
-    MOE_NORM_GRAD(256, 16);
-  else if (s.H <= 8192)
-    MOE_NORM_GRAD(512, 16);
-  else
-    MOE_NORM_GRAD(1024, 16);
+  const int threads = row_threads(s.H);
+#define MOE_NORM_GRAD(THREADS)                                                          \
+  hipLaunchKernelGGL((norm_grad_rows<kBf16, THREADS>), dim3((unsigned)groups),          \
+                     dim3(kGradThreads), 0, st, io, s.T, nvec)
+  switch (threads) {
+    case 64: MOE_NORM_GRAD(64); break;
+    case 128: MOE_NORM_GRAD(128); break;
+    case 256: MOE_NORM_GRAD(256); break;
+    case 512: MOE_NORM_GRAD(512); break;
+    default: MOE_NORM_GRAD(1024); break;
+  }
 #undef MOE_NORM_GRAD
   return hipGetLastError();
 }
@@ -540,18 +579,14 @@ hipError_t quantize_launch(int64_t rows, int64_t cols, const void* x, int8_t* q,
   hipLaunchKernelGGL((quantize_rows<kBf16, THREADS, EPT>), RowOf<THREADS>::grid(end - r0), \
                      dim3(RowOf<THREADS>::kGroup), 0, st, (const u32x4*)x, q, scale, r0, end, \
                      nvec, valid0, valid1)
-    if (cols <= 1024)
-      MOE_QUANTIZE(64, 16);
-    else if (cols <= 2048)
-      MOE_QUANTIZE(64, 32);
-    else if (cols <= 4096)
-      MOE_QUANTIZE(256, 16);
-    else if (cols <= 8192)
-      MOE_QUANTIZE(256, 32);
-    else if (cols <= 16384)
-      MOE_QUANTIZE(1024, 16);
-    else
-      MOE_QUANTIZE(1024, 0);
+    switch (row_threads(std::min<int64_t>(cols, 2048 * kRowValues))) {
+      case 64: MOE_QUANTIZE(64, kRowValues); break;
+      case 128: MOE_QUANTIZE(128, kRowValues); break;
+      case 256: MOE_QUANTIZE(256, kRowValues); break;
+      case 512: MOE_QUANTIZE(512, kRowValues); break;
+      case 1024: MOE_QUANTIZE(1024, kRowValues); break;
+      default: MOE_QUANTIZE(1024, 0); break;
+    }
 #undef MOE_QUANTIZE
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;

@@ -442,7 +442,7 @@ moe_status moe_layer_norm_quantize(const moe_shape* shape, const void* x, const 
                                    void* y, int8_t* q, float* scale, hipStream_t stream);
 
 /* Bytes of workspace moe_layer_norm_backward needs when it gives grad_weight or
- * grad_bias: column sums of up to 512 groups of rows.  Host-only. */
+ * grad_bias: column sums of up to 256 groups of rows.  Host-only. */
 moe_status moe_layer_norm_backward_workspace_size(const moe_shape* shape, size_t* bytes);
 
 /*

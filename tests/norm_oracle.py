@@ -25,8 +25,8 @@ def norm(s, w, b, eps):
 def norm_bound(s, w, b, eps, dtype):
     """Elementwise bound on |y - norm()|.
 
-    A thread adds at most 32 values of a row, a wave 6 partial sums, a workgroup 16: a sum over a row is off by at
-    most 54 roundings of the mean magnitude M (the division and the eps addition: two more), so
+    A thread adds at most 16 values of a row, a wave 6 partial sums, a workgroup 16: a sum over a row is off by fewer
+    than 54 roundings of the mean magnitude M (the division and the eps addition: two more), so
       |mean'| error <= 56 u M,
       d = s - mean' carries that plus one rounding of |d|,
       the sum of squares 54 + 2 roundings and twice d's error (relative to the row's spread 1/rstd); the square root
@@ -56,9 +56,10 @@ def norm_grad(gy, s, w, mean, rstd, gs):
 def norm_grad_bounds(gy, s, w, mean, rstd, gs, dtype):
     """Elementwise bounds for (grad_x, grad_weight, grad_bias).
 
-    xh carries two roundings, h one.  Row means: at most 16 (a wave: 32) values in a thread, 6 + 16 partial sums, two
-    roundings of scaling: 56 of the mean magnitude.  Column sums: a thread adds its rows one after the other (at most
-    ceil(T / 512) of them, each product with three roundings), four waves, then up to 32 + 16 partials."""
+    xh carries two roundings, h one.  Row means: at most 16 values in a thread, 6 + 16 partial sums, two roundings of
+    scaling: fewer than 56 of the mean magnitude.  Column sums: a thread adds its rows one after the other (at most
+    ceil(T / 256) of them, each product with three roundings), a workgroup up to 16 groups, then 16 partials of the 256
+    and the 16 sums of those."""
     T = s.shape[0]
     xh = np.abs((s - mean[:, None]) * rstd[:, None])
     h = np.abs(gy * w)
@@ -68,7 +69,7 @@ def norm_grad_bounds(gy, s, w, mean, rstd, gs, dtype):
     if gs is not None:
         err = err + U32 * (np.abs(gs) + r * (h + m1 + xh * m2))
     dx = np.abs(norm_grad(gy, s, w, mean, rstd, gs)[0])
-    n = -(-T // 512) + 4 + 32 + 16
+    n = -(-T // 256) + 16 + 16 + 16
     return (err + HALF_STEP[dtype] * (dx + err), (n + 4) * U32 * np.abs(gy * xh).sum(0) + 1e-30,
             n * U32 * np.abs(gy).sum(0) + 1e-30)
 

@@ -118,7 +118,7 @@ def test_norm_quantize_is_the_two_calls(dtype, H, T, residual):
 @pytest.mark.parametrize("T,residual", [(1, False), (3, True), (1531, True)])
 def test_norm_backward(dtype, H, T, residual):
     if T * H > 1531 * 4200:
-        T = 700                                     # more rows than the 512 groups, all the same
+        T = 700                                     # more rows than the 256 groups, all the same
     say(f"norm_backward {dtype} T={T} H={H}")
     s, dt = shape(T, H, dtype), no.TORCH[dtype]
     x, (w, b) = rows(T, H, dtype, 7, 1.0), params(H, 8)
