@@ -1025,8 +1025,9 @@ QuantPlan quant_plan(const Shape& s) {
   p.dst_row = take((size_t)s.A * 4);
   p.dev_err = take(4);
   p.meta_ws = take(meta_plan(s).bytes);
-  const size_t rows = (size_t)s.Tc * s.k;
-  const int nslots = s.N >= 2 ? 2 : 1;
+  // a few assignments run unsorted, all chunks at once
+  const size_t rows = few_rows(s) ? (size_t)s.A : (size_t)s.Tc * s.k;
+  const int nslots = s.N >= 2 && !few_rows(s) ? 2 : 1;
   for (int i = 0; i < nslots; ++i) p.y[i] = take(rows * s.H * s.elem);
   p.act = take(nslots * rows * s.I * s.elem);
   p.act_q = take(nslots * rows * s.I);
@@ -1176,10 +1177,21 @@ moe_status moe_quant_forward(const moe_shape* shape, const int8_t* hidden_q,
   int32_t* offsets = (int32_t*)(w + p.offsets);
   int32_t* src_row = (int32_t*)(w + p.src_row);
   int32_t* dst_row = (int32_t*)(w + p.dst_row);
-  hipError_t he = launch_route_meta(
-      s, top_k_index, (int32_t*)(w + p.counts), offsets, (int32_t*)(w + p.splits), src_row,
-      dst_row, dev_error ? dev_error : (int32_t*)(w + p.dev_err), w + p.meta_ws, stream);
+  int32_t* err = dev_error ? dev_error : (int32_t*)(w + p.dev_err);
   void* act = w + p.act;
+  if (few_rows(s)) {
+    void* y = w + p.y[0];
+    hipError_t he = launch_few_gate_up_i8(s, hidden_q, hidden_scale, top_k_index, w_gate_up_q,
+                                          w_gate_up_scale, act, dst_row, err, stream);
+    if (he == hipSuccess)
+      he = launch_few_down_i8(s, act, top_k_index, w_down_q, w_down_scale, y, stream);
+    if (he == hipSuccess)
+      he = launch_combine(s, 0, s.T, y, dst_row, top_k_weights, out, stream);
+    return hip_status(he);
+  }
+  hipError_t he = launch_route_meta(s, top_k_index, (int32_t*)(w + p.counts), offsets,
+                                    (int32_t*)(w + p.splits), src_row, dst_row, err,
+                                    w + p.meta_ws, stream);
   int8_t* act_q = (int8_t*)(w + p.act_q);
   float* act_scale = (float*)(w + p.act_scale);
   // pairs of chunks as in the pair-fused forward: each expert's weights are

@@ -108,14 +108,6 @@ __device__ __forceinline__ uint16_t to_bf16_bits(float f) {
   return __builtin_bit_cast(uint16_t, (__bf16)f);
 }
 
-// SwiGLU of one gate/up pair: silu(g) * u = g / (1 + e^-g) * u, with the
-// hardware base-2 exponential (__expf) and reciprocal (v_rcp_f32): relative
-// error about 1e-7 * (1 + |g|), far below the bf16 rounding of the result.
-// e^-g overflowing to infinity gives g * 0 = 0, the limit.
-__device__ __forceinline__ float swiglu(float g, float u) {
-  return g * __builtin_amdgcn_rcpf(1.0f + __expf(-g)) * u;
-}
-
 // Epilogue through LDS.  The K loops pass the weight fragment as the MFMA's
 // first operand and the row fragment as its second, so each 32x32 block holds
 // C transposed: lane l holds row l % 32 of columns 8*(q/4) + 4*(l/32) + q%4,

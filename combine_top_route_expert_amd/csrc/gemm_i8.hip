@@ -29,12 +29,6 @@ struct QuantArgs : TileArgs {
   const float* b_scale;  // [E][rows of B]
 };
 
-__device__ __forceinline__ float swiglu(float g, float u) {
-  // silu(g) u with the hardware exponential and reciprocal, relative error about
-  // 1e-7 (1 + |g|); e^-g overflowing to infinity gives g * 0 = 0, the limit
-  return g * __builtin_amdgcn_rcpf(1.0f + __expf(-g)) * u;
-}
-
 // The scales of a tile: BM of its rows, then BN of its columns (gate_up: the
 // gate columns, then the up columns).  Thread i fetches scale i before the K loop
 // (one register, the latency hidden behind the loop) and leaves it in LDS after

@@ -207,6 +207,16 @@ hipError_t launch_gate_up_i8(const Shape& s, const GroupedIO& io, const float* a
 hipError_t launch_down_i8(const Shape& s, const GroupedIO& io, const float* a_scale,
                           const void* w_down, const float* w_scale, hipStream_t st);
 
+// The whole 8-bit layer for a few assignments (few_rows_i8.hip): no sorting, row f of
+// act and y is assignment f.  gate_up also writes dst_row (f, or -1 for a dropped
+// id) for the combine and the dropped-id count; down quantises the act rows itself.
+bool few_rows(const Shape& s);
+hipError_t launch_few_gate_up_i8(const Shape& s, const int8_t* hidden_q, const float* hidden_scale,
+                                 const int32_t* top_k_index, const int8_t* w, const float* w_scale,
+                                 void* act, int32_t* dst_row, int32_t* dev_error, hipStream_t st);
+hipError_t launch_few_down_i8(const Shape& s, const void* act, const int32_t* top_k_index,
+                              const int8_t* w, const float* w_scale, void* y, hipStream_t st);
+
 // ---- small device helpers ----------------------------------------------------
 // A 16-byte vector of a row: eight bf16 or four fp32 elements.
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
@@ -228,6 +238,14 @@ __device__ __forceinline__ u32x4 pack_bf16x8(const float* f) {
            ((uint32_t)__builtin_bit_cast(uint16_t, hi) << 16);
   }
   return q;
+}
+
+// SwiGLU of one gate/up pair: silu(g) * u = g / (1 + e^-g) * u, with the
+// hardware base-2 exponential (__expf) and reciprocal (v_rcp_f32): relative
+// error about 1e-7 * (1 + |g|), far below the bf16 rounding of the result.
+// e^-g overflowing to infinity gives g * 0 = 0, the limit.
+__device__ __forceinline__ float swiglu(float g, float u) {
+  return g * __builtin_amdgcn_rcpf(1.0f + __expf(-g)) * u;
 }
 
 __device__ __forceinline__ uint64_t lanemask_lt() {

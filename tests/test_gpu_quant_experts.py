@@ -199,6 +199,57 @@ def test_tile_classes(dtype, N, H, I):  # noqa: E741
         assert not out[gone.all(1)].any()            # a token whose slots were all dropped
 
 
+FEW = [(1, 64, 3, 3, 64, 1), (1, 320, 8, 4, 192, 1), (1, 1088, 40, 32, 2112, 2), (1, 128, 40, 33, 64, 1),
+       (4, 448, 64, 4, 320, 3), (8, 2048, 64, 4, 1024, 1), (32, 192, 64, 1, 64, 32), (8, 192, 63, 4, 64, 1),
+       (16, 64, 70, 2, 448, 2)]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T,H,E,k,I,N", FEW)
+def test_few_assignments(dtype, T, H, E, k, I, N):  # noqa: E741
+    """Both sides of the rule for unsorted assignments (at most 32 of them, half as many as experts unless they are one
+    token's): the layer gives the bits of the sorted steps, dropped ids and repeated experts among them."""
+    for kind in ("distinct", "same", "dropped", "all dropped"):
+        say(f"few {dtype} T={T} H={H} E={E} k={k} I={I} N={N} {kind}")
+        g = np.random.default_rng(T * k)
+        if kind == "distinct":
+            counts = np.bincount(g.permutation(E)[np.arange(T * k) % E], minlength=E)
+        elif kind == "same":
+            counts = np.bincount([E - 1] * (T * k), minlength=E)
+        else:
+            counts = np.bincount(g.integers(0, E, T * k // 2 if kind == "dropped" else 0), minlength=E)
+        c = Case(T, H, E, k, I, N, dtype, counts, seed=T)
+        c.err.fill_(-7)
+        steps, out = run_steps(c), c.forward()
+        torch.cuda.synchronize()
+        assert torch.equal(steps, out)
+        assert int(c.err) == T * k - counts.sum()
+
+
+def test_few_assignments_bad_token_and_replay():
+    T, H, E, k, I = 4, 512, 64, 4, 256  # noqa: E741
+    c = Case(T, H, E, k, I, 1, "bf16", seed=40)
+    good = c.forward()
+    qs = c.qs.clone()
+    qs[2] = float("nan")
+    out = c.forward(qs=qs)
+    torch.cuda.synchronize()
+    assert bool(out[2].isnan().all()) and torch.equal(out[[0, 1, 3]], good[[0, 1, 3]])
+    ws = torch.empty(moe.moe_quant_workspace_size(c.shape), dtype=torch.uint8, device="cuda")
+    idx, got = c.idx.clone(), torch.empty_like(good)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        c.forward(ws=ws, out=got)
+    for n in range(3):
+        c.idx.copy_((idx + n) % E if n != 1 else -idx)
+        got.fill_(7.0)
+        g.replay()
+        torch.cuda.synchronize()
+        ref = c.forward()
+        torch.cuda.synchronize()
+        assert torch.equal(ref, got), n
+
+
 def test_many_experts_few_active():
     """More experts than the rows can fill: workgroups that take several tiles."""
     E = 1024
