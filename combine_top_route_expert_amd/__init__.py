@@ -316,6 +316,17 @@ def _pair_rows(shape: moe_shape, chunk: int) -> Tuple[int, int]:
     return rows0, rows1
 
 
+def _rows_of_pair(shape: moe_shape, chunk: int) -> Tuple[int, int]:
+    """_pair_rows by the chunk rule itself (a library call per chunk is a tenth of a small call);
+    an invalid chunk or count is left to the library to refuse."""
+    T, N, k = shape.T, shape.N, shape.k
+    if not 0 <= chunk < N or T < 0:
+        return _pair_rows(shape, chunk)
+    Tc = -(-T // N)
+    t0, t1, u1 = min(chunk * Tc, T), min((chunk + 1) * Tc, T), min((chunk + 2) * Tc, T)
+    return (t1 - t0) * k, (u1 - t1) * k if chunk + 1 < N else 0
+
+
 def moe_expert_gate_up_pair(shape: moe_shape, chunk: int, x_perm0, x_perm1, offsets, w_gate_up,
                             act, stream=None) -> None:
     rows0, rows1 = _pair_rows(shape, chunk)
@@ -569,9 +580,8 @@ def moe_layer_norm_backward(shape: moe_shape, grad_y, x, weight, mean, rstd, gra
             on(rstd, f32, T, "rstd"), on.optional(grad_sum, dt, n, "grad_sum"),
             on(grad_x, dt, n, "grad_x"), on.optional(grad_weight, f32, H, "grad_weight"),
             on.optional(grad_bias, f32, H, "grad_bias"))
-    params = grad_weight is not None or grad_bias is not None
-    need = moe_layer_norm_backward_workspace_size(shape) if params else 0
-    wp = on(ws, torch.uint8, need, "ws")
+    # (the library compares the workspace's size with what it needs)
+    wp = on.optional(ws, torch.uint8, 0, "ws")
     on.call("moe_layer_norm_backward", stream, ctypes.byref(shape), *args, wp,
             0 if ws is None else ws.numel())
 
@@ -589,7 +599,7 @@ def moe_quantize_rows(rows: int, cols: int, dtype: str, x, q, scale, stream=None
 # ---------------------------------------------------------------- 8-bit integer experts
 def moe_quant_gate_up_gather_pair(shape: moe_shape, chunk: int, hidden_q, hidden_scale, src_row,
                                   offsets, w_gate_up_q, w_gate_up_scale, act, stream=None) -> None:
-    rows = sum(_pair_rows(shape, chunk))
+    rows = sum(_rows_of_pair(shape, chunk))
     on, i8, i32, f32 = _OnDevice(), torch.int8, torch.int32, torch.float32
     T, H, E, I = shape.T, shape.H, shape.E, shape.I  # noqa: E741
     on.call("moe_quant_gate_up_gather_pair", stream, ctypes.byref(shape), chunk,
@@ -603,7 +613,7 @@ def moe_quant_gate_up_gather_pair(shape: moe_shape, chunk: int, hidden_q, hidden
 
 def moe_quant_act_pair(shape: moe_shape, chunk: int, act, offsets, act_q, act_scale,
                        stream=None) -> None:
-    rows = sum(_pair_rows(shape, chunk))
+    rows = sum(_rows_of_pair(shape, chunk))
     on = _OnDevice()
     on.call("moe_quant_act_pair", stream, ctypes.byref(shape), chunk,
             on(act, shape.torch_dtype, rows * shape.I, "act"),
@@ -614,7 +624,7 @@ def moe_quant_act_pair(shape: moe_shape, chunk: int, act, offsets, act_q, act_sc
 
 def moe_quant_down_pair(shape: moe_shape, chunk: int, act_q, act_scale, offsets, w_down_q,
                         w_down_scale, y0, y1, stream=None) -> None:
-    rows0, rows1 = _pair_rows(shape, chunk)
+    rows0, rows1 = _rows_of_pair(shape, chunk)
     on, i8, f32, dt = _OnDevice(), torch.int8, torch.float32, shape.torch_dtype
     H, E, I = shape.H, shape.E, shape.I  # noqa: E741
     on.call("moe_quant_down_pair", stream, ctypes.byref(shape), chunk,
@@ -646,5 +656,6 @@ def moe_quant_forward(shape: moe_shape, hidden_q, hidden_scale, top_k_index, top
             on(w_down_q, i8, E * H * I, "w_down_q"), on(w_down_scale, f32, E * H, "w_down_scale"),
             on(out, shape.torch_dtype, T * H, "out"),
             on.optional(dev_error, i32, 1, "dev_error"))
-    wp = on(ws, torch.uint8, moe_quant_workspace_size(shape), "ws")
+    # (the library compares the workspace's size with what it needs)
+    wp = on(ws, torch.uint8, 1, "ws")
     on.call("moe_quant_forward", stream, ctypes.byref(shape), *args, wp, ws.numel())

@@ -60,20 +60,24 @@ __device__ __forceinline__ float fetch_scale(const QuantArgs& a, const TileRows&
 
 // Epilogue.  Lane l holds row l % 32 of each 32 x 32 block and its columns
 // 8 (q / 4) + 4 (l / 32) + q % 4, q = 0..15, so a lane needs one row scale per
-// block and four consecutive column scales per group of four accumulators.
-// bf16 output leaves through the freed stage buffers as 16-byte row segments;
-// fp32 output (the small tile only) is stored from the registers, four columns at
-// a time.
+// block and four consecutive column scales per group of four accumulators.  The
+// tile goes through the freed stage buffers, row-major, and leaves as 16-byte row
+// segments.  (Stored from the registers instead, 32 bytes of a row at a time: the
+// packed 16k down GEMM 352 -> 411 us, partial lines.)
 template <bool kGateUp, bool kBf16, int FM, int FN, int BM, int BN, int WM, int WN, int NT>
 __device__ __forceinline__ void store_tile_i8(const QuantArgs& a, const i32x16 (&acc)[FM][FN],
                                               const TileRows& tr, int nt, int row0, int nblk,
                                               int wn, int lane, char* smem,
                                               const float* scales) {
-  constexpr int CT = kGateUp ? BN / 2 : BN;  // tile columns of C
-  constexpr int CPR = CT / 8;                // 16-byte chunks per bf16 tile row
+  typedef std::conditional_t<kBf16, uint16_t, float> out_t;
+  constexpr int ES = sizeof(out_t), EV = 16 / ES;  // bytes of an element, elements of 16 bytes
+  constexpr int CT = kGateUp ? BN / 2 : BN;        // tile columns of C
+  constexpr int CPR = CT / EV;                     // 16-byte chunks per tile row
   static_assert(CPR >= 8, "chunk swizzle needs 8 chunks per row");
+  // chunk ch of row r at slot ch ^ (r mod CPR): the 32 rows of one write fall in
+  // distinct slots
   auto lds_at = [](int r, int c) {
-    return r * (CT * 2) + (((c >> 3) ^ (r & (CPR - 1))) << 4) + (c & 7) * 2;
+    return r * (CT * ES) + (((c / EV) ^ (r & (CPR - 1))) << 4) + (c % EV) * ES;
   };
   typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
   constexpr int FC = kGateUp ? FN / 2 : FN;  // 32-column blocks of C
@@ -105,24 +109,22 @@ __device__ __forceinline__ void store_tile_i8(const QuantArgs& a, const i32x16 (
 #pragma unroll
           for (int t = 0; t < 4; ++t) v[t] = (float)acc[i][j][4 * g4 + t] * rs * cs[t];
         }
-        if constexpr (kBf16) {
+        if constexpr (kBf16)
           *(bf16x4*)(smem + lds_at(r, c)) =
               bf16x4{(__bf16)v[0], (__bf16)v[1], (__bf16)v[2], (__bf16)v[3]};
-        } else if (r < tr.rows && col0 + c < a.ncols) {
-          const float* const cbase[2] = {(const float*)a.C[0], (const float*)a.C[1]};
-          float* dst = (float*)row_ptr(cbase, a.c_split, tr, tr.v0 + r, a.ncols);
-          *(float4*)(dst + col0 + c) = make_float4(v[0], v[1], v[2], v[3]);
-        }
+        else
+          *(float4*)(smem + lds_at(r, c)) = make_float4(v[0], v[1], v[2], v[3]);
       }
   }
-  if constexpr (!kBf16) return;
   __syncthreads();
-  const uint16_t* const cbase[2] = {(const uint16_t*)a.C[0], (const uint16_t*)a.C[1]};
+  const out_t* const cbase[2] = {(const out_t*)a.C[0], (const out_t*)a.C[1]};
   for (int ch = threadIdx.x; ch < BM * CPR; ch += NT) {
-    const int r = ch / CPR, c = (ch % CPR) * 8;
+    const int r = ch / CPR, c = (ch % CPR) * EV;
     if (r >= tr.rows || col0 + c >= a.ncols) continue;
     const u32x4 v = *(const u32x4*)(smem + lds_at(r, c));
-    uint16_t* dst = (uint16_t*)row_ptr(cbase, a.c_split, tr, tr.v0 + r, a.ncols);
+    out_t* dst = (out_t*)row_ptr(cbase, a.c_split, tr, tr.v0 + r, a.ncols);
+    // streamed (gate_up's act kept in the caches for the quantiser measured 4%
+    // slower over the DeepSeek-V3-shaped layer)
     __builtin_nontemporal_store(v, (u32x4*)(dst + col0 + c));
   }
 }
@@ -141,7 +143,7 @@ __global__ void __launch_bounds__(64 * WAVES_M * WAVES_N) grouped_gemm_i8(QuantA
   static_assert(WM % 32 == 0 && WN % 32 == 0, "wave tile");
   static_assert(!kGateUp || WN % 64 == 0, "gate/up halves");
   static_assert(STAGES >= 2, "pipeline depth");
-  static_assert((STAGES - 2) * (Loader::LA + Loader::LB) <= 24, "wait_loads range");
+  static_assert((STAGES - 1) * (Loader::LA + Loader::LB) <= 24, "wait_loads range");
   constexpr int kSmemBytes =
       cmax(kRoles ? 2 * Loader::A_BYTES + 3 * Loader::B_BYTES : STAGES * Loader::STAGE_BYTES,
            FM >= 4 ? cmax(3 * Loader::template small_stage<160>(),
@@ -220,8 +222,8 @@ __global__ void __launch_bounds__(64 * WAVES_M * WAVES_N) grouped_gemm_i8(QuantA
       run_k(std::true_type{});
     else
       run_k(std::false_type{});
-    // the freed stage buffers hold the bf16 C tile, then the scales
-    constexpr int kScales = BM * (kGateUp ? BN / 2 : BN) * 2;
+    // the freed stage buffers hold the C tile, then the scales
+    constexpr int kScales = BM * (kGateUp ? BN / 2 : BN) * (kBf16 ? 2 : 4);
     static_assert(kScales + (BM + BN) * 4 <= kSmemBytes, "C tile and scales fit the buffers");
     __syncthreads();  // every wave is done with the stage buffers
     float* scales = (float*)(smem + kScales);
@@ -243,7 +245,23 @@ __global__ void __launch_bounds__(64 * WAVES_M * WAVES_N) grouped_gemm_i8(QuantA
   }
 }
 
-bool prefer_wide(int64_t rows_bound) { return rows_bound >= 4096; }
+// The 256 x 256 tile (its loop for up to 160 rows included) or the 64 x 128 one, for
+// bf16 output.  The large tile reads an expert's weights once for up to 256 rows;
+// the small one starts and ends in less time, fills the chip with fewer columns,
+// and wins while most experts fit its 64 rows (times in us, large / small):
+//   E = 16, K = 4096 and 2048, 200 rows an expert: 80 / 136 and 45 / 67; 32: 64 / 60, 26 / 24
+//   E = 128, K = 2048 and 768, 128 rows: 102 / 125 and 76 / 70; 32: 78 / 71, 56 / 45
+//   E = 256, K = 7168 and 2048, 64 rows: 1302 / 1611 and 781 / 880; 8: 1103 / 1083, 628 / 586
+//   E = 8, K = 2048 and 1408 (88 and 64 large tiles), 200 rows: 30 / 22 and 23 / 13
+// So: at least 64 rows an expert on average, K of 2048 or more and a large tile for
+// every CU.  From 4096 rows on always the large one: the counts are known only on
+// the device, and when two of 256 experts get 8000 rows between them the small one
+// takes about twice as long, against at most a seventh lost on even counts.
+bool prefer_wide(const QuantArgs& a, int64_t rows_bound, int n_tiles) {
+  if (rows_bound >= 4096) return true;
+  return rows_bound >= 64 * (int64_t)a.E && a.row_bytes >= 2048 &&
+         (int64_t)a.E * n_tiles >= 256;
+}
 
 template <bool kGateUp, bool kBf16, int BM, int BN, int WM_, int WN_, bool kBuf>
 hipError_t launch_instance(QuantArgs a, const Shape& s, int64_t rows_bound, hipStream_t st) {
@@ -271,8 +289,10 @@ template <bool kGateUp, bool kBuf>
 hipError_t launch_kind(const QuantArgs& a, const Shape& s, int64_t rows_bound, hipStream_t st) {
   if (s.dtype != MOE_BF16)
     return launch_instance<kGateUp, false, 64, 128, 2, 2, kBuf>(a, s, rows_bound, st);
+  // a 256-column gate_up tile holds 128 intermediate columns
   const bool wide_ok = !kGateUp || s.I % 128 == 0;
-  if (prefer_wide(rows_bound) && wide_ok)
+  const int n_tiles = kGateUp ? s.I / 128 : (s.H + 255) / 256;
+  if (wide_ok && prefer_wide(a, rows_bound, n_tiles))
     return launch_instance<kGateUp, true, 256, 256, 2, 4, kBuf>(a, s, rows_bound, st);
   return launch_instance<kGateUp, true, 64, 128, 2, 2, kBuf>(a, s, rows_bound, st);
 }

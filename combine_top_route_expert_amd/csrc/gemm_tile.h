@@ -27,10 +27,17 @@ typedef __attribute__((address_space(3))) void lds_void;
 // instruction multiplies) and leave the same 32 x 32 accumulator layout.
 // kHalfStage: rows are multiples of 64 bytes, so the last stage may hold only
 // its first half (bf16 rows of H % 64 == 0 values always fill their stages).
+// kRefill: k_loop keeps all STAGES in flight at the start of a step and refills a
+// buffer at its end, behind a second barrier, instead of keeping STAGES - 1 and
+// refilling at the start.  For int8 on the small tile, whose steps hold little
+// matrix work: 2 rows per expert, gate_up 988 -> 963 and down 506 -> 485 us; 62 rows
+// per expert 68 -> 61 and 40 -> 36 us.  (k_loop_small: 1520 -> 1590 us at 128
+// rows per expert, where the waves issue no loads beside each other's MFMAs any more.)
 struct MmaBf16 {
   typedef bf16x8 frag;
   typedef f32x16 acc;
   static constexpr bool kHalfStage = false;
+  static constexpr bool kRefill = false;
   static __device__ __forceinline__ acc mma(frag b, frag a, acc c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(b, a, c, 0, 0, 0);
   }
@@ -39,6 +46,7 @@ struct MmaI8 {
   typedef i32x4 frag;
   typedef i32x16 acc;
   static constexpr bool kHalfStage = true;
+  static constexpr bool kRefill = true;
   static __device__ __forceinline__ acc mma(frag b, frag a, acc c) {
     return __builtin_amdgcn_mfma_i32_32x32x32_i8(b, a, c, 0, 0, 0);
   }
@@ -355,13 +363,15 @@ __device__ __forceinline__ void k_loop(typename Loader::Mma::acc (&acc)[FM][FN],
   using G = StageGeom<SB>;
   using Frag = typename Loader::Mma::frag;
   constexpr int KS = SB / 32;  // MFMA sub-steps per stage
+  constexpr bool kRefill = Loader::Mma::kRefill;
+  constexpr int kAhead = kRefill ? STAGES : STAGES - 1;  // stages in flight at a step's start
   // nothing of the lgkm class (scalar loads included) is pending on entry, so
   // the waits before each sub-step's MFMAs can count the LDS reads in order
   __builtin_amdgcn_s_waitcnt(kWaitLgkm0);
   const int tid = ld.wave * 64 + lane;
   for (int kt = 0; kt < KT; ++kt) {
     // stage kt has landed once only the newer stages issued so far are pending
-    const int newer = KT - 1 - kt < STAGES - 2 ? KT - 1 - kt : STAGES - 2;
+    const int newer = KT - 1 - kt < kAhead - 1 ? KT - 1 - kt : kAhead - 1;
     wait_loads(newer * per_stage);
     __builtin_amdgcn_s_barrier();
     char* sa = smem + (kt % STAGES) * Loader::STAGE_BYTES;
@@ -381,7 +391,7 @@ __device__ __forceinline__ void k_loop(typename Loader::Mma::acc (&acc)[FM][FN],
           bfr[b][j] = *(const Frag*)(sb + (wn * WN + j * 32) * G::ROW_BYTES + fo);
       };
       frag(0, 0);  // ahead of the next stage's loads, so the first MFMAs start sooner
-      if (kt + STAGES - 1 < KT)
+      if (!kRefill && kt + STAGES - 1 < KT)
         ld.template issue<kNt>(smem, kt + STAGES - 1, (kt + STAGES - 1) % STAGES);
 #pragma unroll
       for (int kk = 0; kk < KS; ++kk) {
@@ -396,11 +406,15 @@ __device__ __forceinline__ void k_loop(typename Loader::Mma::acc (&acc)[FM][FN],
         __builtin_amdgcn_sched_barrier(0);
       }
     } else {
-      if (kt + STAGES - 1 < KT)
+      if (!kRefill && kt + STAGES - 1 < KT)
         ld.template issue<kNt>(smem, kt + STAGES - 1, (kt + STAGES - 1) % STAGES);
     }
     // this stage's LDS reads are complete before any wave refills its buffer
     __builtin_amdgcn_s_waitcnt(kWaitLgkm0);
+    if (kRefill && kt + STAGES < KT) {
+      __builtin_amdgcn_s_barrier();
+      ld.template issue<kNt>(smem, kt + STAGES, kt % STAGES);
+    }
   }
 }
 
@@ -489,7 +503,7 @@ __device__ __forceinline__ void wide_k(typename Loader::Mma::acc (&acc)[FM][FN],
     }
   } else {
 #pragma unroll
-    for (int s = 0; s < STAGES - 1; ++s)
+    for (int s = 0; s < (Loader::Mma::kRefill ? STAGES : STAGES - 1); ++s)
       if (s < KT) ld.template issue<kNt>(smem, s, s);
   }
   const int band_rows = rows - wm * WM;

@@ -99,3 +99,14 @@ def test_binding_refuses():
     z = torch.zeros(1 << 14, dtype=torch.int8)
     with pytest.raises(ValueError):                 # host tensors
         moe.moe_quant_forward(s, z, z, z, z, z, z, z, z, z, z)
+
+
+def test_binding_rows_of_a_pair_are_the_librarys():
+    for T in (0, 1, 2, 3, 10, 97):
+        for N in (1, 2, 3, 4, 7, 50):
+            s = shape(T=T, N=N, k=3)
+            for c in range(N):
+                assert moe._rows_of_pair(s, c) == moe._pair_rows(s, c), (T, N, c)
+            for bad in (-1, N):
+                with pytest.raises(moe.MoeError):
+                    moe._rows_of_pair(s, bad)
