@@ -488,77 +488,78 @@ def moe_permute_backward(shape: moe_shape, chunk: int, grad_x_perm, dst_row, gra
 
 
 # ---------------------------------------------------------------- layer norm, row quantisation
-class _OnDevice:
-    """Pointers of one call's tensors, which must all live on one device; the call is made with
-    that device current, on the given stream or the device's current one."""
+# A call of a few microseconds on the device is bound by what the host does for it, so these
+# functions test all of a call's tensors in one loop, and word what is wrong only when something is.
+def _pointers(*specs):
+    """(device index, [pointers]) of one call's tensors, each given as (tensor, dtype, elements it
+    has to hold, name) or, where None will do, (tensor, dtype, elements, name, True).  All tensors
+    have to live on one device (index -1: there was no tensor)."""
+    index, out = -1, []
+    for spec in specs:
+        t = spec[0]
+        if t is None and len(spec) == 5:
+            out.append(None)
+            continue
+        if not (isinstance(t, torch.Tensor) and t.dtype is spec[1] and t.is_contiguous()
+                and t.numel() >= spec[2] and t.get_device() >= 0):
+            out.append(_ptr(*spec[:4]))  # raises, or None for an empty array
+            continue
+        at = t.get_device()
+        if at != index:
+            if index >= 0:
+                raise ValueError(f"{spec[3]} is on {t.device}, the tensors before it on "
+                                 f"cuda:{index}")
+            index = at
+        out.append(t.data_ptr())
+    return index, out
 
-    __slots__ = ("index",)
 
-    def __init__(self):
-        self.index = -1
-
-    def __call__(self, t, dtype, min_numel: int, name: str) -> Optional[int]:
-        # one test of everything for a good tensor; _ptr words what is wrong with another
-        if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype
-                and t.is_contiguous() and t.numel() >= min_numel):
-            p = _ptr(t, dtype, min_numel, name)
-            if t is None:
-                return p
-        index = t.get_device()
-        if index != self.index:
-            if self.index >= 0:
-                raise ValueError(f"{name} is on {t.device}, the tensors before it on "
-                                 f"cuda:{self.index}")
-            self.index = index
-        return t.data_ptr()
-
-    def optional(self, t, dtype, min_numel: int, name: str) -> Optional[int]:
-        return None if t is None else self(t, dtype, min_numel, name)
-
-    def call(self, fn: str, stream, *args) -> None:
-        f = getattr(_lib or load_library(), fn)
-        if self.index < 0 or self.index == torch.cuda.current_device():
-            code = f(*args, self._stream(stream))
-        else:
-            with torch.cuda.device(self.index):
-                code = f(*args, self._stream(stream))
-        if code != 0:
-            raise MoeError(fn, code)
-
-    def _stream(self, stream) -> int:
-        if stream is None:
-            if self.index < 0:
-                return torch.cuda.current_stream().cuda_stream
-            return torch._C._cuda_getCurrentRawStream(self.index)
-        if isinstance(stream, int):
-            return stream
-        if self.index >= 0 and stream.device.index != self.index:
-            raise ValueError(f"stream is on {stream.device}, the tensors on cuda:{self.index}")
-        return stream.cuda_stream
+def _call(fn: str, index: int, stream, *args) -> None:
+    """Calls the library with the tensors' device current, on `stream` (a torch stream of that
+    device or a raw handle) or the device's current stream."""
+    f = getattr(_lib or load_library(), fn)
+    if stream is None:
+        raw = (torch._C._cuda_getCurrentRawStream(index) if index >= 0
+               else torch.cuda.current_stream().cuda_stream)
+    elif isinstance(stream, int):
+        raw = stream
+    else:
+        if index >= 0 and stream.device.index != index:
+            raise ValueError(f"stream is on {stream.device}, the tensors on cuda:{index}")
+        raw = stream.cuda_stream
+    if index < 0 or index == torch.cuda.current_device():
+        code = f(*args, raw)
+    else:
+        with torch.cuda.device(index):
+            code = f(*args, raw)
+    if code != 0:
+        raise MoeError(fn, code)
 
 
 def moe_layer_norm(shape: moe_shape, x, residual, weight, bias, eps: float, sum_out, y, mean=None,
                    rstd=None, stream=None) -> None:
     """y = layer norm of x (or of x + residual, which goes to sum_out); weight, bias, mean and rstd
     are float32 and may be None."""
-    on, dt, f32, T, H = _OnDevice(), shape.torch_dtype, torch.float32, shape.T, shape.H
+    dt, f32, T, H = shape.torch_dtype, torch.float32, shape.num_tokens, shape.hidden
     n = T * H
-    on.call("moe_layer_norm", stream, ctypes.byref(shape), on(x, dt, n, "x"),
-            on.optional(residual, dt, n, "residual"), on.optional(weight, f32, H, "weight"),
-            on.optional(bias, f32, H, "bias"), eps, on.optional(sum_out, dt, n, "sum"),
-            on(y, dt, n, "y"), on.optional(mean, f32, T, "mean"),
-            on.optional(rstd, f32, T, "rstd"))
+    index, (xp, rp, wp, bp, sp, yp, mp, dp) = _pointers(
+        (x, dt, n, "x"), (residual, dt, n, "residual", True), (weight, f32, H, "weight", True),
+        (bias, f32, H, "bias", True), (sum_out, dt, n, "sum", True), (y, dt, n, "y"),
+        (mean, f32, T, "mean", True), (rstd, f32, T, "rstd", True))
+    _call("moe_layer_norm", index, stream, ctypes.byref(shape), xp, rp, wp, bp, eps, sp, yp, mp, dp)
 
 
 def moe_layer_norm_quantize(shape: moe_shape, x, residual, weight, bias, eps: float, sum_out, y, q,
                             scale, stream=None) -> None:
     """moe_layer_norm whose rows are also quantised into q (int8) and scale; y may be None."""
-    on, dt, f32, T, H = _OnDevice(), shape.torch_dtype, torch.float32, shape.T, shape.H
+    dt, f32, T, H = shape.torch_dtype, torch.float32, shape.num_tokens, shape.hidden
     n = T * H
-    on.call("moe_layer_norm_quantize", stream, ctypes.byref(shape), on(x, dt, n, "x"),
-            on.optional(residual, dt, n, "residual"), on.optional(weight, f32, H, "weight"),
-            on.optional(bias, f32, H, "bias"), eps, on.optional(sum_out, dt, n, "sum"),
-            on.optional(y, dt, n, "y"), on(q, torch.int8, n, "q"), on(scale, f32, T, "scale"))
+    index, (xp, rp, wp, bp, sp, yp, qp, cp) = _pointers(
+        (x, dt, n, "x"), (residual, dt, n, "residual", True), (weight, f32, H, "weight", True),
+        (bias, f32, H, "bias", True), (sum_out, dt, n, "sum", True), (y, dt, n, "y", True),
+        (q, torch.int8, n, "q"), (scale, f32, T, "scale"))
+    _call("moe_layer_norm_quantize", index, stream, ctypes.byref(shape), xp, rp, wp, bp, eps, sp,
+          yp, qp, cp)
 
 
 def moe_layer_norm_backward_workspace_size(shape: moe_shape) -> int:
@@ -573,66 +574,65 @@ def moe_layer_norm_backward(shape: moe_shape, grad_y, x, weight, mean, rstd, gra
                             grad_weight=None, grad_bias=None, ws=None, stream=None) -> None:
     """Gradient of moe_layer_norm: x holds the normalised rows (sum_out where there was a
     residual); grad_sum, grad_weight and grad_bias may be None."""
-    on, dt, f32, T, H = _OnDevice(), shape.torch_dtype, torch.float32, shape.T, shape.H
+    dt, f32, T, H = shape.torch_dtype, torch.float32, shape.num_tokens, shape.hidden
     n = T * H
-    args = (on(grad_y, dt, n, "grad_y"), on(x, dt, n, "x"),
-            on.optional(weight, f32, H, "weight"), on(mean, f32, T, "mean"),
-            on(rstd, f32, T, "rstd"), on.optional(grad_sum, dt, n, "grad_sum"),
-            on(grad_x, dt, n, "grad_x"), on.optional(grad_weight, f32, H, "grad_weight"),
-            on.optional(grad_bias, f32, H, "grad_bias"))
     # (the library compares the workspace's size with what it needs)
-    wp = on.optional(ws, torch.uint8, 0, "ws")
-    on.call("moe_layer_norm_backward", stream, ctypes.byref(shape), *args, wp,
-            0 if ws is None else ws.numel())
+    index, ptrs = _pointers(
+        (grad_y, dt, n, "grad_y"), (x, dt, n, "x"), (weight, f32, H, "weight", True),
+        (mean, f32, T, "mean"), (rstd, f32, T, "rstd"), (grad_sum, dt, n, "grad_sum", True),
+        (grad_x, dt, n, "grad_x"), (grad_weight, f32, H, "grad_weight", True),
+        (grad_bias, f32, H, "grad_bias", True), (ws, torch.uint8, 0, "ws", True))
+    _call("moe_layer_norm_backward", index, stream, ctypes.byref(shape), *ptrs,
+          0 if ws is None else ws.numel())
 
 
 def moe_quantize_rows(rows: int, cols: int, dtype: str, x, q, scale, stream=None) -> None:
     """Rows of x ("bf16" or "f32") as int8 q with one float32 scale each."""
     if dtype not in ("bf16", "f32"):
         raise ValueError(f"dtype must be 'bf16' or 'f32', got {dtype!r}")
-    on, bf16 = _OnDevice(), dtype == "bf16"
-    on.call("moe_quantize_rows", stream, rows, cols, MOE_BF16 if bf16 else MOE_F32,
-            on(x, torch.bfloat16 if bf16 else torch.float32, rows * cols, "x"),
-            on(q, torch.int8, rows * cols, "q"), on(scale, torch.float32, rows, "scale"))
+    bf16, n = dtype == "bf16", rows * cols
+    index, ptrs = _pointers((x, torch.bfloat16 if bf16 else torch.float32, n, "x"),
+                            (q, torch.int8, n, "q"), (scale, torch.float32, rows, "scale"))
+    _call("moe_quantize_rows", index, stream, rows, cols, MOE_BF16 if bf16 else MOE_F32, *ptrs)
 
 
 # ---------------------------------------------------------------- 8-bit integer experts
 def moe_quant_gate_up_gather_pair(shape: moe_shape, chunk: int, hidden_q, hidden_scale, src_row,
                                   offsets, w_gate_up_q, w_gate_up_scale, act, stream=None) -> None:
     rows = sum(_rows_of_pair(shape, chunk))
-    on, i8, i32, f32 = _OnDevice(), torch.int8, torch.int32, torch.float32
-    T, H, E, I = shape.T, shape.H, shape.E, shape.I  # noqa: E741
-    on.call("moe_quant_gate_up_gather_pair", stream, ctypes.byref(shape), chunk,
-            on(hidden_q, i8, T * H, "hidden_q"), on(hidden_scale, f32, T, "hidden_scale"),
-            on(src_row, i32, T * shape.k, "src_row"),
-            on(offsets, i32, shape.N * (E + 1), "offsets"),
-            on(w_gate_up_q, i8, E * 2 * I * H, "w_gate_up_q"),
-            on(w_gate_up_scale, f32, E * 2 * I, "w_gate_up_scale"),
-            on(act, shape.torch_dtype, rows * I, "act"))
+    i8, i32, f32 = torch.int8, torch.int32, torch.float32
+    T, H, E, I = shape.num_tokens, shape.hidden, shape.num_experts, shape.intermediate  # noqa: E741
+    index, ptrs = _pointers(
+        (hidden_q, i8, T * H, "hidden_q"), (hidden_scale, f32, T, "hidden_scale"),
+        (src_row, i32, T * shape.top_k, "src_row"), (offsets, i32, shape.N * (E + 1), "offsets"),
+        (w_gate_up_q, i8, E * 2 * I * H, "w_gate_up_q"),
+        (w_gate_up_scale, f32, E * 2 * I, "w_gate_up_scale"),
+        (act, shape.torch_dtype, rows * I, "act"))
+    _call("moe_quant_gate_up_gather_pair", index, stream, ctypes.byref(shape), chunk, *ptrs)
 
 
 def moe_quant_act_pair(shape: moe_shape, chunk: int, act, offsets, act_q, act_scale,
                        stream=None) -> None:
     rows = sum(_rows_of_pair(shape, chunk))
-    on = _OnDevice()
-    on.call("moe_quant_act_pair", stream, ctypes.byref(shape), chunk,
-            on(act, shape.torch_dtype, rows * shape.I, "act"),
-            on(offsets, torch.int32, shape.N * (shape.E + 1), "offsets"),
-            on(act_q, torch.int8, rows * shape.I, "act_q"),
-            on(act_scale, torch.float32, rows, "act_scale"))
+    n = rows * shape.intermediate
+    index, ptrs = _pointers(
+        (act, shape.torch_dtype, n, "act"),
+        (offsets, torch.int32, shape.N * (shape.num_experts + 1), "offsets"),
+        (act_q, torch.int8, n, "act_q"), (act_scale, torch.float32, rows, "act_scale"))
+    _call("moe_quant_act_pair", index, stream, ctypes.byref(shape), chunk, *ptrs)
 
 
 def moe_quant_down_pair(shape: moe_shape, chunk: int, act_q, act_scale, offsets, w_down_q,
                         w_down_scale, y0, y1, stream=None) -> None:
     rows0, rows1 = _rows_of_pair(shape, chunk)
-    on, i8, f32, dt = _OnDevice(), torch.int8, torch.float32, shape.torch_dtype
-    H, E, I = shape.H, shape.E, shape.I  # noqa: E741
-    on.call("moe_quant_down_pair", stream, ctypes.byref(shape), chunk,
-            on(act_q, i8, (rows0 + rows1) * I, "act_q"),
-            on(act_scale, f32, rows0 + rows1, "act_scale"),
-            on(offsets, torch.int32, shape.N * (E + 1), "offsets"),
-            on(w_down_q, i8, E * H * I, "w_down_q"), on(w_down_scale, f32, E * H, "w_down_scale"),
-            on(y0, dt, rows0 * H, "y0"), on(y1, dt, rows1 * H, "y1"))
+    i8, f32, dt = torch.int8, torch.float32, shape.torch_dtype
+    H, E, I = shape.hidden, shape.num_experts, shape.intermediate  # noqa: E741
+    index, ptrs = _pointers(
+        (act_q, i8, (rows0 + rows1) * I, "act_q"), (act_scale, f32, rows0 + rows1, "act_scale"),
+        (offsets, torch.int32, shape.N * (E + 1), "offsets"), (w_down_q, i8, E * H * I, "w_down_q"),
+        (w_down_scale, f32, E * H, "w_down_scale"), (y0, dt, rows0 * H, "y0"),
+        (y1, dt, rows1 * H, "y1"))
+    _call("moe_quant_down_pair", index, stream, ctypes.byref(shape), chunk, *ptrs)
 
 
 def moe_quant_workspace_size(shape: moe_shape) -> int:
@@ -646,16 +646,16 @@ def moe_quant_forward(shape: moe_shape, hidden_q, hidden_scale, top_k_index, top
                       w_gate_up_q, w_gate_up_scale, w_down_q, w_down_scale, out, ws,
                       dev_error=None, stream=None) -> None:
     """The layer on quantised hidden rows and weights; out in the shape's dtype."""
-    on, i8, i32, f32 = _OnDevice(), torch.int8, torch.int32, torch.float32
-    T, H, E, k, I = shape.T, shape.H, shape.E, shape.k, shape.I  # noqa: E741
-    args = (on(hidden_q, i8, T * H, "hidden_q"), on(hidden_scale, f32, T, "hidden_scale"),
-            on(top_k_index, i32, T * k, "top_k_index"),
-            on(top_k_weights, f32, T * k, "top_k_weights"),
-            on(w_gate_up_q, i8, E * 2 * I * H, "w_gate_up_q"),
-            on(w_gate_up_scale, f32, E * 2 * I, "w_gate_up_scale"),
-            on(w_down_q, i8, E * H * I, "w_down_q"), on(w_down_scale, f32, E * H, "w_down_scale"),
-            on(out, shape.torch_dtype, T * H, "out"),
-            on.optional(dev_error, i32, 1, "dev_error"))
+    i8, i32, f32 = torch.int8, torch.int32, torch.float32
+    T, H, E, I = shape.num_tokens, shape.hidden, shape.num_experts, shape.intermediate  # noqa: E741
+    A = T * shape.top_k
     # (the library compares the workspace's size with what it needs)
-    wp = on(ws, torch.uint8, 1, "ws")
-    on.call("moe_quant_forward", stream, ctypes.byref(shape), *args, wp, ws.numel())
+    index, ptrs = _pointers(
+        (hidden_q, i8, T * H, "hidden_q"), (hidden_scale, f32, T, "hidden_scale"),
+        (top_k_index, i32, A, "top_k_index"), (top_k_weights, f32, A, "top_k_weights"),
+        (w_gate_up_q, i8, E * 2 * I * H, "w_gate_up_q"),
+        (w_gate_up_scale, f32, E * 2 * I, "w_gate_up_scale"),
+        (w_down_q, i8, E * H * I, "w_down_q"), (w_down_scale, f32, E * H, "w_down_scale"),
+        (out, shape.torch_dtype, T * H, "out"), (dev_error, i32, 1, "dev_error", True),
+        (ws, torch.uint8, 1, "ws"))
+    _call("moe_quant_forward", index, stream, ctypes.byref(shape), *ptrs, ws.numel())

@@ -1,6 +1,7 @@
 // C-ABI entry points: argument checks, workspace planning and the Chunk MoE
 // two-stream schedules.  Every function only enqueues work; none synchronises
 // with the device or copies anything to the host.
+#include <algorithm>
 #include <mutex>
 #include <vector>
 
@@ -1025,11 +1026,11 @@ QuantPlan quant_plan(const Shape& s) {
   p.dst_row = take((size_t)s.A * 4);
   p.dev_err = take(4);
   p.meta_ws = take(meta_plan(s).bytes);
-  // a few assignments run unsorted, all chunks at once
-  const size_t rows = few_rows(s) ? (size_t)s.A : (size_t)s.Tc * s.k;
-  const int nslots = s.N >= 2 && !few_rows(s) ? 2 : 1;
+  const size_t rows = (size_t)s.Tc * s.k;
+  const int nslots = s.N >= 2 ? 2 : 1;
   for (int i = 0; i < nslots; ++i) p.y[i] = take(rows * s.H * s.elem);
-  p.act = take(nslots * rows * s.I * s.elem);
+  // (a few assignments run unsorted, all chunks at once)
+  p.act = take(std::max(nslots * rows, few_rows(s) ? (size_t)s.A : 0) * s.I * s.elem);
   p.act_q = take(nslots * rows * s.I);
   p.act_scale = take(nslots * rows * 4);
   p.bytes = o;
@@ -1179,16 +1180,10 @@ moe_status moe_quant_forward(const moe_shape* shape, const int8_t* hidden_q,
   int32_t* dst_row = (int32_t*)(w + p.dst_row);
   int32_t* err = dev_error ? dev_error : (int32_t*)(w + p.dev_err);
   void* act = w + p.act;
-  if (few_rows(s)) {
-    void* y = w + p.y[0];
-    hipError_t he = launch_few_gate_up_i8(s, hidden_q, hidden_scale, top_k_index, w_gate_up_q,
-                                          w_gate_up_scale, act, dst_row, err, stream);
-    if (he == hipSuccess)
-      he = launch_few_down_i8(s, act, top_k_index, w_down_q, w_down_scale, y, stream);
-    if (he == hipSuccess)
-      he = launch_combine(s, 0, s.T, y, dst_row, top_k_weights, out, stream);
-    return hip_status(he);
-  }
+  if (few_rows(s))
+    return hip_status(launch_few_i8(s, hidden_q, hidden_scale, top_k_index, top_k_weights,
+                                    w_gate_up_q, w_gate_up_scale, w_down_q, w_down_scale, act, out,
+                                    err, stream));
   hipError_t he = launch_route_meta(s, top_k_index, (int32_t*)(w + p.counts), offsets,
                                     (int32_t*)(w + p.splits), src_row, dst_row, err,
                                     w + p.meta_ws, stream);

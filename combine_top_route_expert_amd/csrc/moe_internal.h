@@ -207,15 +207,14 @@ hipError_t launch_gate_up_i8(const Shape& s, const GroupedIO& io, const float* a
 hipError_t launch_down_i8(const Shape& s, const GroupedIO& io, const float* a_scale,
                           const void* w_down, const float* w_scale, hipStream_t st);
 
-// The whole 8-bit layer for a few assignments (few_rows_i8.hip): no sorting, row f of
-// act and y is assignment f.  gate_up also writes dst_row (f, or -1 for a dropped
-// id) for the combine and the dropped-id count; down quantises the act rows itself.
+// The whole 8-bit layer for a few assignments (few_rows_i8.hip): nothing is sorted,
+// act [T*k][I] holds row f for assignment f; also counts the dropped ids.
 bool few_rows(const Shape& s);
-hipError_t launch_few_gate_up_i8(const Shape& s, const int8_t* hidden_q, const float* hidden_scale,
-                                 const int32_t* top_k_index, const int8_t* w, const float* w_scale,
-                                 void* act, int32_t* dst_row, int32_t* dev_error, hipStream_t st);
-hipError_t launch_few_down_i8(const Shape& s, const void* act, const int32_t* top_k_index,
-                              const int8_t* w, const float* w_scale, void* y, hipStream_t st);
+hipError_t launch_few_i8(const Shape& s, const int8_t* hidden_q, const float* hidden_scale,
+                         const int32_t* top_k_index, const float* top_k_weights,
+                         const int8_t* w_gate_up, const float* w_gate_up_scale,
+                         const int8_t* w_down, const float* w_down_scale, void* act, void* out,
+                         int32_t* dev_error, hipStream_t st);
 
 // ---- small device helpers ----------------------------------------------------
 // A 16-byte vector of a row: eight bf16 or four fp32 elements.

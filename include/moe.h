@@ -540,8 +540,8 @@ moe_status moe_quant_down_pair(const moe_shape* shape, int32_t chunk, const int8
                                void* y1, hipStream_t stream);
 
 /* Bytes of workspace moe_quant_forward needs: the metadata plus min(N,2) slots
- * of ceil(T/N)*k rows (T*k rows once, where those are 32 or fewer) of (H + I)
- * elements, I bytes and a scale.  Host-only. */
+ * of ceil(T/N)*k rows of (H + I) elements, I bytes and a scale (act: at least
+ * T*k rows, where those are 32 or fewer).  Host-only. */
 moe_status moe_quant_workspace_size(const moe_shape* shape, size_t* bytes);
 
 /*

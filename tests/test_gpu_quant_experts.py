@@ -201,14 +201,16 @@ def test_tile_classes(dtype, N, H, I):  # noqa: E741
 
 FEW = [(1, 64, 3, 3, 64, 1), (1, 320, 8, 4, 192, 1), (1, 1088, 40, 32, 2112, 2), (1, 128, 40, 33, 64, 1),
        (4, 448, 64, 4, 320, 3), (8, 2048, 64, 4, 1024, 1), (32, 192, 64, 1, 64, 32), (8, 192, 63, 4, 64, 1),
-       (16, 64, 70, 2, 448, 2)]
+       (16, 64, 70, 2, 448, 2), (8, 192, 32, 4, 64, 1), (16, 64, 31, 2, 128, 1),
+       (1, 64, 9, 8, 8192, 1), (1, 64, 9, 8, 8256, 1)]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("T,H,E,k,I,N", FEW)
 def test_few_assignments(dtype, T, H, E, k, I, N):  # noqa: E741
-    """Both sides of the rule for unsorted assignments (at most 32 of them, half as many as experts unless they are one
-    token's): the layer gives the bits of the sorted steps, dropped ids and repeated experts among them."""
+    """Both sides of the rule for unsorted assignments (at most 32 of them, as many as experts unless they are one
+    token's, and 64 KB of quantised rows): the layer gives the bits of the sorted steps, dropped ids and repeated experts
+    among them."""
     for kind in ("distinct", "same", "dropped", "all dropped"):
         say(f"few {dtype} T={T} H={H} E={E} k={k} I={I} N={N} {kind}")
         g = np.random.default_rng(T * k)
