@@ -919,6 +919,7 @@ moe_status norm_shape(const moe_shape* shape, Shape* s) {
 moe_status norm_args(const Shape& s, const NormIO& io) {
   if (!(io.eps > 0.0f) || io.eps > 3.0e38f) return MOE_ERR_INVALID_ARG;
   if ((io.residual == nullptr) != (io.sum == nullptr)) return MOE_ERR_INVALID_ARG;
+  if (io.sum && io.sum == io.y) return MOE_ERR_INVALID_ARG;
   if (s.T > 0 && !io.x) return MOE_ERR_INVALID_ARG;
   if (!aligned(io.x, 16) || !aligned(io.residual, 16) || !aligned(io.sum, 16) ||
       !aligned(io.y, 16) || !aligned(io.weight, 4) || !aligned(io.bias, 4) ||

@@ -62,7 +62,7 @@ permute_rows(const u32x4* __restrict__ hidden, const int32_t* __restrict__ dst_r
 // One wave per token; each lane holds kVecPerLane 16-byte vectors of the row.
 // Few tokens (kSplitTokens at most) spread a row's vectors over gridDim.y
 // workgroups, every one with its own part: 64 tokens of 7168 values and 8 slots
-// kept 16 workgroups busy for 22 us.
+// kept 16 workgroups busy for 22 us, 8 us spread out.
 // Tokens [t0, t_mid) read their rows from y0, tokens [t_mid, t1) from y1 (a
 // chunk pair whose expert outputs sit in two slots; row indices are
 // chunk-local).
@@ -235,9 +235,8 @@ hipError_t launch_combine_pair(const Shape& s, int t0, int t_mid, int t1, const 
   if (t1 <= t0) return hipSuccess;
   const int nvec = (int)((int64_t)s.H * s.elem / 16);
   const unsigned blocks = (unsigned)((t1 - t0 + kWavesPerBlock - 1) / kWavesPerBlock);
-  const unsigned parts = t1 - t0 <= kSplitTokens
-                             ? (unsigned)((nvec + 64 * kVecPerLane - 1) / (64 * kVecPerLane))
-                             : 1u;
+  const int spans = (nvec + 64 * kVecPerLane - 1) / (64 * kVecPerLane);
+  const unsigned parts = t1 - t0 <= kSplitTokens ? (unsigned)(spans < 256 ? spans : 256) : 1u;
   if (s.dtype == MOE_BF16)
     hipLaunchKernelGGL(combine_rows<true>, dim3(blocks, parts), dim3(64 * kWavesPerBlock), 0, st,
                        (const u32x4*)y0, (const u32x4*)y1, t_mid, dst_row, w, (u32x4*)out, t0,

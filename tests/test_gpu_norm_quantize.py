@@ -221,6 +221,27 @@ def test_norm_in_place_and_bad_rows():
             assert torch.equal(y2[row], y3[row]), row
 
 
+def test_parameters_at_any_float():
+    """weight, bias, mean, rstd and scale need only their own four bytes' alignment."""
+    for dtype, H in (("bf16", 2112), ("f32", 1028)):
+        T, s = 7, shape(7, H, dtype)
+        x, (w, b) = rows(T, H, dtype, 30), params(H + 1, 31)
+        y, y2, q, q2 = torch.empty_like(x), torch.empty_like(x), *(torch.empty(T, H, dtype=torch.int8, device="cuda")
+                                                                   for _ in range(2))
+        st, st2 = torch.empty(4, T + 1, device="cuda"), torch.empty(4, T, device="cuda")
+        moe.moe_layer_norm(s, x, None, w[1:], b[1:], EPS, None, y, st[0, 1:], st[1, 1:])
+        moe.moe_layer_norm(s, x, None, w[1:].clone(), b[1:].clone(), EPS, None, y2, st2[0], st2[1])
+        moe.moe_layer_norm_quantize(s, x, None, w[1:], b[1:], EPS, None, None, q, st[2, 1:])
+        moe.moe_quantize_rows(T, H, dtype, y2, q2, st2[2])
+        torch.cuda.synchronize()
+        assert torch.equal(y, y2) and torch.equal(q, q2) and torch.equal(st[:3, 1:], st2[:3])
+        gx, gx2, gw = torch.empty_like(x), torch.empty_like(x), torch.empty(H, device="cuda")
+        ws = torch.empty(moe.moe_layer_norm_backward_workspace_size(s), dtype=torch.uint8, device="cuda")
+        moe.moe_layer_norm_backward(s, x, x, w[1:], st[0, 1:], st[1, 1:], None, gx, gw, None, ws)
+        moe.moe_layer_norm_backward(s, x, x, w[1:].clone(), st2[0], st2[1], None, gx2, gw.clone(), None, ws)
+        assert torch.equal(gx, gx2)
+
+
 def test_constant_rows_keep_their_precision():
     """A large common offset: the variance is that of the distances from the mean."""
     T, H = 4, 4096

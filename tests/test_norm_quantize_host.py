@@ -34,7 +34,7 @@ def grad(s, gy=P, x=P, w=P, mean=P, rstd=P, gs=None, gx=P, gw=P, gb=P, ws=P, n=N
 
 @pytest.mark.parametrize("kw", [dict(x=None), dict(y=None), dict(x=P + 2), dict(y=P + 8), dict(w=P + 2),
                                 dict(b=P + 1), dict(mean=P + 2), dict(rstd=P + 3), dict(res=P), dict(sm=P),
-                                dict(res=P + 4, sm=P), dict(res=P, sm=P + 4), dict(eps=0.0), dict(eps=-1.0),
+                                dict(res=P + 4, sm=P), dict(res=P, sm=P + 4), dict(res=2 * P, sm=P, y=P), dict(eps=0.0), dict(eps=-1.0),
                                 dict(eps=float("nan")), dict(eps=float("inf"))])
 def test_norm_refuses(kw):
     assert norm(shape(), **kw) == INVALID
