@@ -298,11 +298,15 @@ struct MTileMap {
   }
 
   static __device__ __forceinline__ int wave_incl_scan(int v) {
-    const int lane = __lane_id();
-    for (int d = 1; d < 64; d <<= 1) {
-      const int n = __shfl_up(v, d);
-      if (lane >= d) v += n;
-    }
+    // within rows of 16 lanes, then each row's last lane into the rows after it
+    // (data-parallel shifts: a shift through LDS costs 60 cycles or more, and a tile's
+    // workgroup does nothing else meanwhile)
+    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, false);  // row_shr:1
+    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false);  // row_bcast:15
+    v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false);  // row_bcast:31
     return v;
   }
 
@@ -331,8 +335,9 @@ struct MTileMap {
     incl_small[1] = wave_incl_scan(p34);
     excl_small[0] = incl_small[0] - p12;
     excl_small[1] = incl_small[1] - p34;
-    large = __shfl(incl_large, 63);
-    const int t12 = __shfl(incl_small[0], 63), t34 = __shfl(incl_small[1], 63);
+    large = __builtin_amdgcn_readlane(incl_large, 63);
+    const int t12 = __builtin_amdgcn_readlane(incl_small[0], 63);
+    const int t34 = __builtin_amdgcn_readlane(incl_small[1], 63);
     start[0] = 0;
     start[1] = large;
     start[2] = start[1] + (t12 & 0xFFFF);
@@ -407,13 +412,13 @@ struct MTileMap {
     // the owner's values, broadcast to the wave, are wave-uniform: kept in
     // scalar registers (as vector registers they stayed live across the K loop)
     TileRows r;
-    r.e = __builtin_amdgcn_readfirstlane(__shfl(fe, owner));
-    r.v0 = __builtin_amdgcn_readfirstlane(__shfl(fv0, owner));
-    r.rows = __builtin_amdgcn_readfirstlane(__shfl(frows, owner));
-    r.lo0 = __builtin_amdgcn_readfirstlane(__shfl(flo0, owner));
-    r.n0 = __builtin_amdgcn_readfirstlane(__shfl(fn0, owner));
-    r.lo1 = __builtin_amdgcn_readfirstlane(__shfl(flo1, owner));
-    r.single = __builtin_amdgcn_readfirstlane(__shfl(fsingle, owner));
+    r.e = __builtin_amdgcn_readlane(fe, owner);
+    r.v0 = __builtin_amdgcn_readlane(fv0, owner);
+    r.rows = __builtin_amdgcn_readlane(frows, owner);
+    r.lo0 = __builtin_amdgcn_readlane(flo0, owner);
+    r.n0 = __builtin_amdgcn_readlane(fn0, owner);
+    r.lo1 = __builtin_amdgcn_readlane(flo1, owner);
+    r.single = __builtin_amdgcn_readlane(fsingle, owner);
     return r;
   }
 };
