@@ -17,6 +17,10 @@
  * The expert FFN form (SwiGLU, no bias) is not spelled out on the pages; it is
  * the reading this library takes.
  *
+ * Around the layer: layer norm of its input rows (moe_layer_norm, its backward
+ * and its quantising form) and, for inference, the layer with 8-bit integer
+ * experts (moe_quantize_rows, moe_quant_*).
+ *
  * Conventions shared by every entry point
  * ---------------------------------------
  *  - Pointers named as tensors are DEVICE memory owned by the caller.  The
