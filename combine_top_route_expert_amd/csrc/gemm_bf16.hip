@@ -12,6 +12,8 @@
 // rows straight from hidden_states through src_row (GroupedIO::gather): the
 // permute fused into the A loader's addresses.
 //
+// (Stage loads and K loops, shared with the int8 GEMMs, are in gemm_tile.h.)
+//
 // Pipeline: K advances 64 at a time.  Each stage of the A (rows) and B
 // (weight) tiles is copied HBM -> LDS by the direct-to-LDS load (64 lanes x 16
 // bytes land as one contiguous 1 KB block), so loads need no VGPRs and

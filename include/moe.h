@@ -507,7 +507,7 @@ moe_status moe_quantize_rows(int64_t rows, int64_t cols, int32_t dtype, const vo
  * a row with an infinity or a NaN) gives NaN in its own output row only.
  * Limits: H % 64 == 0 and I % 64 == 0 for every dtype, H and I <= 131008
  * (MOE_ERR_UNSUPPORTED otherwise).  MOE_BF16 is the tuned form; MOE_F32 keeps
- * act, y and out in float32 and always runs the small tile.
+ * act, y and out in float32 and runs the small tiles only.
  * --------------------------------------------------------------------------- */
 
 /*

@@ -115,7 +115,7 @@ def test_norm_quantize_is_the_two_calls(dtype, H, T, residual):
 
 
 @pytest.mark.parametrize("dtype,H", WIDTHS)
-@pytest.mark.parametrize("T,residual", [(1, False), (3, True), (1531, True)])
+@pytest.mark.parametrize("T,residual", [(1, False), (3, True), (5, True), (33, False), (1531, True)])
 def test_norm_backward(dtype, H, T, residual):
     if T * H > 1531 * 4200:
         T = 700                                     # more rows than the 256 groups, all the same
