@@ -464,3 +464,45 @@ def test_norm_around_the_layer_as_trained():
         # float32 throughout; the layer's own fp32 backward is held to 1e-5 of its rows' largest value
         err = (got.double().cpu() - lf.grad).abs().max() / lf.grad.abs().max()
         assert float(err) < 2e-5
+
+
+def test_large_tiles_below_4096_rows():
+    """Few experts with many rows each: the large tile for both products, for one of them, and (K too short) for none."""
+    for T, H, E, I in ((600, 2048, 32, 2048), (600, 2048, 16, 2048), (640, 1984, 40, 1024)):  # noqa: E741
+        say(f"quant T={T} H={H} E={E} I={I}")
+        c = Case(T, H, E, 4, I, 1, "bf16", seed=50)
+        steps, out = run_steps(c), c.forward()
+        torch.cuda.synchronize()
+        assert torch.equal(steps, out)
+
+
+def test_random_shapes():
+    rng = np.random.default_rng(60)
+    for n in range(16):
+        k = int(rng.integers(1, 9))
+        E, T = int(rng.integers(max(1, k // 2), 70)), int(np.exp(rng.uniform(0, np.log(1500))))
+        H, I = 64 * int(rng.integers(1, 14)), 64 * int(rng.integers(1, 14))  # noqa: E741
+        N, dtype = int(rng.integers(1, 5)), ("bf16", "f32")[n % 2]
+        say(f"quant random {n}: {dtype} T={T} H={H} E={E} k={k} I={I} N={N}")
+        c = Case(T, H, E, k, I, N, dtype, seed=100 + n)
+        steps, out = run_steps(c), c.forward()
+        torch.cuda.synchronize()
+        assert torch.equal(steps, out)
+
+
+def test_two_layers_at_once():
+    """Two streams, a workspace each, twenty layers on either without a wait between them."""
+    cases = [Case(900, 320, 12, 5, 256, 1, "bf16", seed=70), Case(3, 512, 16, 4, 256, 1, "bf16", seed=71)]
+    ref = [c.forward() for c in cases]
+    outs = [[torch.empty_like(r) for _ in range(20)] for r in ref]
+    ws = [torch.empty(moe.moe_quant_workspace_size(c.shape), dtype=torch.uint8, device="cuda") for c in cases]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()                        # every buffer is ready before either stream starts
+    for n in range(20):
+        for c, st, o, w in zip(cases, streams, outs, ws):
+            with torch.cuda.stream(st):
+                c.forward(ws=w, out=o[n])
+    torch.cuda.synchronize()
+    for r, o in zip(ref, outs):
+        for t in o:
+            assert torch.equal(r, t)
