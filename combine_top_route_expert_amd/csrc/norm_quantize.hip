@@ -94,8 +94,8 @@ struct RowOf {
 constexpr int64_t kRowsPerLaunch = 1 << 21;
 
 template <bool kBf16, int THREADS, bool kQuant>
-__global__ void __launch_bounds__(RowOf<THREADS>::kGroup) norm_rows(NormIO io, int64_t row0, int64_t rows,
-                                                                     int nvec) {
+__global__ void __launch_bounds__(RowOf<THREADS>::kGroup)
+norm_rows(NormIO io, int64_t row0, int64_t rows, int nvec) {
   constexpr int kEl = kVecEl<kBf16>, VPT = kRowValues / kEl, NW = THREADS / 64;
   const int64_t row = row0 + RowOf<THREADS>::row();
   if (row >= rows) return;
