@@ -30,10 +30,16 @@ namespace moe {
 
 namespace {
 
+// Sum over the wave: within rows of 16 lanes, then each row's total into the row
+// after it, so that lane 63 ends with all of it.
 __device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-  for (int d = 32; d > 0; d >>= 1) v += __shfl_xor(v, d);
-  return v;
+  v += __int_as_float(wave_shift<0x111, 0xf>(__float_as_int(v)));
+  v += __int_as_float(wave_shift<0x112, 0xf>(__float_as_int(v)));
+  v += __int_as_float(wave_shift<0x114, 0xf>(__float_as_int(v)));
+  v += __int_as_float(wave_shift<0x118, 0xf>(__float_as_int(v)));
+  v += __int_as_float(wave_shift<0x142, 0xa>(__float_as_int(v)));
+  v += __int_as_float(wave_shift<0x143, 0xc>(__float_as_int(v)));
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
 }
 
 // Reductions over the THREADS threads of a row; `red` is a slot of THREADS / 64

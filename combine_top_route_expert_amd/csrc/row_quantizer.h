@@ -33,13 +33,24 @@ __device__ __forceinline__ u32x4 pack(const float* f) {
   }
 }
 
+// v of another lane by a data-parallel shift (a few cycles; through LDS it would be
+// some sixty), zero where there is none: 0x111..0x118 from 1..8 lanes before in the
+// same row of 16, 0x142 / 0x143 from the last lane of the row / half before.  All
+// lanes have to be active.
+template <int kControl, int kRowMask>
+__device__ __forceinline__ int wave_shift(int v) {
+  return __builtin_amdgcn_update_dpp(0, v, kControl, kRowMask, 0xf, false);
+}
+
 __device__ __forceinline__ uint32_t wave_max(uint32_t v) {
-#pragma unroll
-  for (int d = 32; d > 0; d >>= 1) {
-    const uint32_t o = __shfl_xor(v, d);
-    v = o > v ? o : v;
-  }
-  return v;
+  auto with = [&](uint32_t o) __attribute__((always_inline)) { v = o > v ? o : v; };
+  with(wave_shift<0x111, 0xf>(v));
+  with(wave_shift<0x112, 0xf>(v));
+  with(wave_shift<0x114, 0xf>(v));
+  with(wave_shift<0x118, 0xf>(v));
+  with(wave_shift<0x142, 0xa>(v));
+  with(wave_shift<0x143, 0xc>(v));
+  return __builtin_amdgcn_readlane(v, 63);
 }
 
 // One row's quantiser, from the bits of its largest magnitude (as an unsigned
