@@ -10,8 +10,13 @@
 //
 // All of it is bound by memory: a row is read once, held in registers as fp32
 // while its statistics are reduced, and written once.  The variance is the
-// mean of the squared distances from the mean (a second pass over registers),
-// so a large common offset costs no precision.
+// mean of the squared distances from the mean (a second pass over registers).
+// A common offset costs no precision, since the mean is that of an exact or
+// nearly exact sum: bf16 values of one binade sum to 22 bits at most and fp32
+// holds them; fp32 rows are summed in fp64 and their mean is subtracted as two
+// floats (one fp32 mean: values around 1000 that spread by 0.01 had y off by 0.01;
+// at most 1% more time, 6.4 -> 6.5 us for 1000 x 2052).  fp64 for bf16
+// rows too: one token 4.0 -> 4.15 us, 16384 x 8192 124 -> 129 us, and nothing gained.
 //
 // A row takes 64 to 1024 threads of at most 16 values each (up to 1024 values: a
 // wave's row, four to a workgroup, no barrier).  Threads take 16-byte vectors round
@@ -22,6 +27,7 @@
 // streamed non-temporally (54.3 -> 52 us and 52.8 -> 48.2 us: 5.2 and 4.9 TB/s, against
 // 4.75 of a large device copy).
 #include <algorithm>
+#include <cfloat>
 #include <type_traits>
 
 #include "row_quantizer.h"
@@ -42,11 +48,28 @@ __device__ __forceinline__ float wave_sum(float v) {
   return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
 }
 
+__device__ __forceinline__ double wave_sum(double v) {
+  auto add = [&](auto control, auto rows) __attribute__((always_inline)) {
+    constexpr int kControl = decltype(control)::value, kRows = decltype(rows)::value;
+    v += __hiloint2double(wave_shift<kControl, kRows>(__double2hiint(v)),
+                          wave_shift<kControl, kRows>(__double2loint(v)));
+  };
+  const std::integral_constant<int, 0xf> all{};
+  add(std::integral_constant<int, 0x111>{}, all);
+  add(std::integral_constant<int, 0x112>{}, all);
+  add(std::integral_constant<int, 0x114>{}, all);
+  add(std::integral_constant<int, 0x118>{}, all);
+  add(std::integral_constant<int, 0x142>{}, std::integral_constant<int, 0xa>{});
+  add(std::integral_constant<int, 0x143>{}, std::integral_constant<int, 0xc>{});
+  return __hiloint2double(__builtin_amdgcn_readlane(__double2hiint(v), 63),
+                          __builtin_amdgcn_readlane(__double2loint(v), 63));
+}
+
 // Reductions over the THREADS threads of a row; `red` is a slot of THREADS / 64
-// words used by no other reduction that a barrier does not separate.  Every
+// values used by no other reduction that a barrier does not separate.  Every
 // thread gets the same bits.
-template <int THREADS>
-__device__ __forceinline__ float row_sum(float v, float* red) {
+template <int THREADS, class T>
+__device__ __forceinline__ T row_sum(T v, T* red) {
   v = wave_sum(v);
   if constexpr (THREADS > 64) {
     if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
@@ -105,7 +128,9 @@ norm_rows(NormIO io, int64_t row0, int64_t rows, int nvec) {
   constexpr int kEl = kVecEl<kBf16>, VPT = kRowValues / kEl, NW = THREADS / 64;
   const int64_t row = row0 + RowOf<THREADS>::row();
   if (row >= rows) return;
-  __shared__ float red[3][NW];
+  typedef std::conditional_t<kBf16, float, double> sum_t;
+  __shared__ sum_t red_total[NW];
+  __shared__ float red[2][NW];
   const int tid = RowOf<THREADS>::tid();
   const u32x4* x = (const u32x4*)io.x + row * nvec;
   u32x4 xv[VPT], rv[VPT];
@@ -119,7 +144,7 @@ norm_rows(NormIO io, int64_t row0, int64_t rows, int nvec) {
       if (i * THREADS + tid < nvec) rv[i] = __builtin_nontemporal_load(&r[i * THREADS + tid]);
   }
   float f[VPT][kEl];
-  float total = 0.0f;
+  sum_t total = 0;
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
     const int v = i * THREADS + tid;
@@ -137,10 +162,15 @@ norm_rows(NormIO io, int64_t row0, int64_t rows, int nvec) {
       unpack<kBf16>(p, f[i]);
     }
 #pragma unroll
-    for (int e = 0; e < kEl; ++e) total += f[i][e];
+    for (int e = 0; e < kEl; ++e) total += (sum_t)f[i][e];
   }
   const float h = (float)(nvec * kEl);
-  const float mean = row_sum<THREADS>(total, red[0]) / h;
+  const sum_t sum = row_sum<THREADS>(total, red_total);
+  sum_t exact = sum / (sum_t)h;
+  // a sum past fp32's range has no mean in it: NaN, as for a row with an infinity
+  if constexpr (!kBf16)
+    if (!(fabs(sum) <= (double)FLT_MAX)) exact = __builtin_nan("");
+  const float mean = (float)exact, mean_low = (float)(exact - (sum_t)mean);
   float sq = 0.0f;
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
@@ -148,10 +178,11 @@ norm_rows(NormIO io, int64_t row0, int64_t rows, int nvec) {
 #pragma unroll
     for (int e = 0; e < kEl; ++e) {
       f[i][e] -= mean;
+      if constexpr (!kBf16) f[i][e] -= mean_low;
       sq = __builtin_fmaf(f[i][e], f[i][e], sq);
     }
   }
-  const float rstd = 1.0f / sqrtf(row_sum<THREADS>(sq, red[1]) / h + io.eps);
+  const float rstd = 1.0f / sqrtf(row_sum<THREADS>(sq, red[0]) / h + io.eps);
   if (tid == 0) {
     if (io.mean) io.mean[row] = mean;
     if (io.rstd) io.rstd[row] = rstd;
@@ -176,7 +207,7 @@ norm_rows(NormIO io, int64_t row0, int64_t rows, int nvec) {
     }
   }
   if constexpr (kQuant) {
-    const RowQuantizer<kBf16> quant(row_max<THREADS>(big, (uint32_t*)red[2]));
+    const RowQuantizer<kBf16> quant(row_max<THREADS>(big, (uint32_t*)red[1]));
     if (tid == 0) io.scale[row] = quant.scale;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {

@@ -414,9 +414,11 @@ moe_status moe_permute_backward(const moe_shape* shape, int32_t chunk, const voi
  * Layer norm of the rows that enter the layer, and their 8-bit integer form.
  *
  * The norm's weight and bias and its statistics are float32 for every dtype (as
- * top_k_weights are); statistics and gradient sums are held in fp32, every
- * [T][H] output is rounded to the layer's dtype once.  Limit: H <= 16384
- * (MOE_ERR_UNSUPPORTED beyond).  Only T, H and dtype of the shape matter here.
+ * top_k_weights are).  A row's mean is taken closely enough (fp32 rows are summed
+ * in fp64) that a common offset of its values costs y no precision; the other
+ * sums are held in fp32; every [T][H] output is rounded to the layer's dtype
+ * once.  Limit: H <= 16384 (MOE_ERR_UNSUPPORTED beyond).  Only T, H and dtype of
+ * the shape matter here (its other fields have to be valid).
  * --------------------------------------------------------------------------- */
 
 /*
@@ -457,7 +459,8 @@ moe_status moe_layer_norm_backward_workspace_size(const moe_shape* shape, size_t
  *  grad_y     [T][H]: the gradient of y (from moe_chunked_backward's
  *             grad_hidden_states, for the layer behind the norm)
  *  x          [T][H]: the rows that were normalised (sum, where there was a
- *             residual); mean, rstd [T]: as moe_layer_norm left them
+ *             residual); mean, rstd [T]: as moe_layer_norm left them (xh is
+ *             that of the float32 mean: off by up to 2^-24 |mean| rstd)
  *  grad_sum   [T][H], nullable: gradient that reaches the rows past the norm
  *             (the residual stream), added to grad_x before the one rounding;
  *             grad_x is then the gradient of both x and residual

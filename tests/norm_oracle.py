@@ -43,6 +43,43 @@ def norm_bound(s, w, b, eps, dtype):
     return err + HALF_STEP[dtype] * (y + err)
 
 
+def norm_bound_about_mean(s, w, b, eps, dtype):
+    """Elementwise bounds on |y - norm()|, |mean - norm()| and |rstd / norm() - 1| that do not grow with a row's common
+    offset.  f32: for a mean that is summed in float64 and subtracted as two float32 parts; bf16: for rows whose values
+    lie in one binade, so that float32 holds their sums (8 + 14 bits) and only the mean is rounded, to c = U |mean| where
+    neighbouring values of a row are 2^-8 |mean| apart.
+
+    Fewer than 54 additions and a division in float64 leave the mean within v = 56 2^-53 M, M = mean|s| + |mean|; its
+    second part is at most U |mean| and rounded once, so
+      d = (s - high) - low is off by 2 U |d| (two subtractions) and at most c = 3 U^2 |mean| + v.
+    The sum of squares adds 54 roundings and two more for the division and eps, d's error twice 2 U and 2 c rstd; the
+    square root halves them, it and the reciprocal add one each; y = (d rstd) w + b adds two."""
+    _, mean, rstd = norm(s, w, b, eps)
+    r, m = rstd[:, None], np.abs(mean)[:, None]
+    v = 56 * 2.0 ** -53 * (np.abs(s).mean(1, keepdims=True) + m)
+    c = 3 * U32 ** 2 * m + v if dtype == "f32" else U32 * m
+    d = np.abs(s - mean[:, None])
+    rel = (30 + 2) * U32 + c * r
+    err = (r * (2 * U32 * d + c) + r * d * (rel + 2 * U32)) * np.abs(w) + 2 * U32 * np.abs(b)
+    y = np.abs((s - mean[:, None]) * r * w + b)
+    return err + HALF_STEP[dtype] * (y + err), (U32 * m + v)[:, 0], rel[:, 0]
+
+
+# (H, offset, spread) of rows whose values share a large offset; float32 resolves the spread in 16 to 160 steps
+OFFSETS = [(324, 1000.1, 0.01), (1020, -1e4, 0.02), (2052, 1000.1, 0.01), (4100, 3e5, 0.6), (8196, 1e4, 0.02),
+           (16384, 1000.1, 0.01)]
+
+
+# the same for bf16 within a binade, the spread 4, 9 and 1.5 of its steps
+OFFSETS_BF16 = [(320, 768.0, 16.0), (2112, -24.0, 1.125), (16384, 3.0 * 2 ** 20, 24576.0)]
+
+
+def offset_rows(T, H, offset, spread):
+    """Values around the offset, at most a quarter of it away."""
+    x = spread * np.random.default_rng(H).normal(size=(T, H))
+    return (offset + np.clip(x, -abs(offset) / 4, abs(offset) / 4)).astype(np.float32)
+
+
 def norm_grad(gy, s, w, mean, rstd, gs):
     xh = (s - mean[:, None]) * rstd[:, None]
     h = gy * w

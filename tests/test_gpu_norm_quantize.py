@@ -357,3 +357,32 @@ def test_streams_and_graph_replays():
         torch.cuda.synchronize()
         for k in keys:
             assert torch.equal(other[k], graph[k]), (n, k)
+
+
+@pytest.mark.parametrize("dtype,H,offset,spread", [("f32", *c) for c in no.OFFSETS] +
+                         [("bf16", *c) for c in no.OFFSETS_BF16])
+def test_common_offset_costs_no_precision(dtype, H, offset, spread):
+    """Rows far from zero, held to bounds that do not grow with the offset; rows of one value give exactly the bias."""
+    T = 6
+    say(f"norm offset {dtype} H={H} offset={offset}")
+    s, (w, b), dt = shape(T, H, dtype), params(H, 40), no.TORCH[dtype]
+    x = torch.from_numpy(no.offset_rows(T, H, offset, spread)).cuda().to(dt)
+    x[4], x[5] = offset, 1.7e10
+    y, mean, rstd = torch.empty_like(x), torch.empty(T, device="cuda"), torch.empty(T, device="cuda")
+    for p in ((w, b), (None, None)):
+        moe.moe_layer_norm(s, x, None, *p, EPS, None, y, mean, rstd)
+        torch.cuda.synchronize()
+        w64, b64 = (f64(w), f64(b)) if p[0] is not None else (np.ones(H), np.zeros(H))
+        ref, m64, r64 = no.norm(f64(x), w64, b64, EPS)
+        by, bm, br = no.norm_bound_about_mean(f64(x), w64, b64, EPS, dtype)
+        within(y[:4], ref[:4], by[:4], "y")
+        within(mean, m64, bm, "mean")
+        within(rstd[:4], r64[:4], br[:4] * r64[:4], "rstd")
+        assert torch.equal(y[4:], (b if p[0] is not None else torch.zeros(H, device="cuda")).to(dt).expand(2, H))
+    # the residual form and the quantising form read the same rows
+    half, sm, y2 = x * 0.5, torch.empty_like(x), torch.empty_like(x)
+    q, sc = torch.empty(T, H, dtype=torch.int8, device="cuda"), torch.empty(T, device="cuda")
+    moe.moe_layer_norm_quantize(s, half, half, None, None, EPS, sm, y2, q, sc)
+    torch.cuda.synchronize()
+    assert torch.equal(sm, x) and torch.equal(y2, y)
+    quantizes(y, q, sc)

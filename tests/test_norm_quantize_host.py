@@ -123,3 +123,29 @@ def test_quantizer_oracle_by_hand():
     q, scale = no.quantize(x)
     assert q.tolist() == [[127, 0, 2, -2, -127], [0] * 5, [127, 64, -64, 0, 1], [0] * 5, [0] * 5]
     assert scale[0] == 1.0 and scale[1] == 0.0 and np.isnan(scale[3:]).all()
+
+
+@pytest.mark.parametrize("H,offset,spread", no.OFFSETS)
+def test_bound_about_the_mean_sees_mistakes(H, offset, spread):
+    """float32 models of the norm: a float64 mean in two parts is within the bound; a row of zeros, flipped signs, a
+    variance from the sum of squares, and a mean from one float32 sum or rounded to one float32 are not."""
+    x = no.offset_rows(3, H, offset, spread)
+    ref = no.norm(x.astype(np.float64), 1.0, 0.0, EPS)[0]
+    bound = no.norm_bound_about_mean(x.astype(np.float64), np.ones(H), np.zeros(H), EPS, "f32")[0]
+    f = np.float32
+
+    def y_of(d, var=None):
+        var = (d * d).sum(1, dtype=f) / f(H) if var is None else var
+        return d * (f(1) / np.sqrt(var + f(EPS)))[:, None]
+
+    within = lambda y: bool((np.abs(y.astype(np.float64) - ref) <= bound).all())  # noqa: E731
+    mean = x.astype(np.float64).mean(1, keepdims=True)
+    high = mean.astype(f)
+    good = y_of((x - high) - (mean - high).astype(f))
+    assert good.dtype == f and within(good)
+    assert not within(np.zeros_like(x)) and not within(-good)
+    one_pass = np.maximum((x * x).sum(1, dtype=f) / f(H) - high[:, 0] * high[:, 0], f(0))
+    assert not within(y_of(x - high, one_pass))
+    assert not within(y_of(x - high))
+    single = x.reshape(3, -1, 4).cumsum(1, dtype=f)[:, -1].sum(1, dtype=f, keepdims=True) / f(H)
+    assert not within(y_of(x - single))
