@@ -182,7 +182,9 @@ norm_rows(NormIO io, int64_t row0, int64_t rows, int nvec) {
       sq = __builtin_fmaf(f[i][e], f[i][e], sq);
     }
   }
-  const float rstd = 1.0f / sqrtf(row_sum<THREADS>(sq, red[0]) / h + io.eps);
+  // squares past fp32's range would leave rstd 0 and y the bias: NaN instead, as above
+  const float var = row_sum<THREADS>(sq, red[0]) / h + io.eps;
+  const float rstd = var < __builtin_inff() ? 1.0f / sqrtf(var) : __builtin_nanf("");
   if (tid == 0) {
     if (io.mean) io.mean[row] = mean;
     if (io.rstd) io.rstd[row] = rstd;

@@ -432,7 +432,8 @@ moe_status moe_permute_backward(const moe_shape* shape, int32_t chunk, const voi
  *  eps            > 0 and finite
  *  mean, rstd     [T] (out, each nullable): what moe_layer_norm_backward reads
  * sum and y may each be x or residual (not each other).  A row that holds an
- * infinity or a NaN gives NaN in that row only.
+ * infinity or a NaN gives NaN in that row only; so does a row of finite values
+ * whose sum, or whose squared distances' sum, float32 cannot hold.
  */
 moe_status moe_layer_norm(const moe_shape* shape, const void* x, const void* residual,
                           const float* weight, const float* bias, float eps, void* sum, void* y,

@@ -386,3 +386,38 @@ def test_common_offset_costs_no_precision(dtype, H, offset, spread):
     torch.cuda.synchronize()
     assert torch.equal(sm, x) and torch.equal(y2, y)
     quantizes(y, q, sc)
+
+
+@pytest.mark.parametrize("dtype,H", [("bf16", 320), ("bf16", 2048), ("bf16", 7168), ("f32", 324), ("f32", 2052)])
+def test_rows_past_the_range_of_the_sums(dtype, H):
+    """Finite rows whose squared distances add up to more than float32 holds give NaN, as rows with an infinity do, and no
+    other row changes; just inside the range a row is right."""
+    T = 9
+    s, (w, b), dt = shape(T, H, dtype), params(H, 41), no.TORCH[dtype]
+    x = rows(T, H, dtype, 42)
+    sign = 1.0 - 2.0 * (torch.arange(H, device="cuda") % 2)
+    big = x.clone()
+    edge = (3.4e38 / H) ** 0.5                      # squares of this size just reach the end of the range
+    for row, size in ((1, 1e25), (3, 1.25 * edge), (4, 0.5 * edge), (6, 3e38), (7, 1e36)):
+        big[row] = (size * sign).to(dt)
+    big[7, 1:] = 0.0                                # one value alone
+    y, y2 = torch.empty_like(x), torch.empty_like(x)
+    st = torch.empty(2, T, device="cuda")
+    q, sc = torch.full((T, H), 9, dtype=torch.int8, device="cuda"), torch.empty(T, device="cuda")
+    moe.moe_layer_norm(s, x, None, w, b, EPS, None, y)
+    moe.moe_layer_norm(s, big, None, w, b, EPS, None, y2, st[0], st[1])
+    torch.cuda.synchronize()
+    for row in range(T):
+        if row in (1, 3, 6, 7):
+            assert bool(y2[row].isnan().all()) and bool(st[1, row].isnan()), row
+        elif row == 4:
+            r = f64(big[4:5])
+            within(y2[4:5], no.norm(r, f64(w), f64(b), EPS)[0], no.norm_bound(r, f64(w), f64(b), EPS, dtype), "y")
+        else:
+            assert torch.equal(y2[row], y[row]), row
+    moe.moe_layer_norm_quantize(s, big, None, w, b, EPS, None, y, q, sc)
+    torch.cuda.synchronize()
+    assert torch.equal(y.isnan(), y2.isnan())
+    for row in (1, 3, 6, 7):
+        assert bool(sc[row].isnan()) and not q[row].any(), row
+    assert bool(sc[[0, 2, 4, 5, 8]].isfinite().all())
