@@ -108,7 +108,7 @@ __global__ void __launch_bounds__(64 * kWaves) few_gate_up_i8(FewArgs a) {
   }
   // gate sums are in lanes 0..31, the up sums of the same columns in lanes 32..63
   const float v = (float)wave_sum8(acc, lane) * rs * cs;
-  const float o = swiglu(v, __shfl_xor(v, 32));
+  const float o = swiglu<kBf16>(v, __shfl_xor(v, 32));
   if (lane & 7 || lane >= 32) return;
   const int64_t at = (int64_t)f * a.ncols + c0 + my;
   if constexpr (kBf16)

@@ -159,7 +159,7 @@ __device__ __forceinline__ void store_tile_lds(const GemmArgs& a, const f32x16 (
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
               const float g = acc[i][j][4 * g4 + t], u = acc[i][j + FN / 2][4 * g4 + t];
-              v[t] = plane == 0 ? swiglu(g, u) : plane == 1 ? g : u;
+              v[t] = plane == 0 ? swiglu<true>(g, u) : plane == 1 ? g : u;
             }
             *(bf16x4*)(smem + lds_at(r, c)) =
                 bf16x4{(__bf16)v[0], (__bf16)v[1], (__bf16)v[2], (__bf16)v[3]};

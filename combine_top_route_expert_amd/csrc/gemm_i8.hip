@@ -112,7 +112,7 @@ __device__ __forceinline__ void store_tile_i8(const QuantArgs& a, const i32x16 (
           const float us[4] = {s1.x, s1.y, s1.z, s1.w};
 #pragma unroll
           for (int t = 0; t < 4; ++t)
-            v[t] = swiglu((float)acc[i][j][4 * g4 + t] * rs * cs[t],
+            v[t] = swiglu<kBf16>((float)acc[i][j][4 * g4 + t] * rs * cs[t],
                           (float)acc[i][j + FC][4 * g4 + t] * rs * us[t]);
         } else {
 #pragma unroll

@@ -239,12 +239,17 @@ __device__ __forceinline__ u32x4 pack_bf16x8(const float* f) {
   return q;
 }
 
-// SwiGLU of one gate/up pair: silu(g) * u = g / (1 + e^-g) * u, with the
-// hardware base-2 exponential (__expf) and reciprocal (v_rcp_f32): relative
-// error about 1e-7 * (1 + |g|), far below the bf16 rounding of the result.
-// e^-g overflowing to infinity gives g * 0 = 0, the limit.
+// SwiGLU of one gate/up pair: silu(g) * u = g / (1 + e^-g) * u.  For a bf16 result
+// with the hardware base-2 exponential (__expf) and reciprocal (v_rcp_f32): relative
+// error about 1e-7 * (1 + |g|), far below its rounding.  For an fp32 result with expf
+// and a division, a few units whatever the size of g.  e^-g overflowing to infinity
+// gives g * 0 = 0, the limit.
+template <bool kBf16>
 __device__ __forceinline__ float swiglu(float g, float u) {
-  return g * __builtin_amdgcn_rcpf(1.0f + __expf(-g)) * u;
+  if constexpr (kBf16)
+    return g * __builtin_amdgcn_rcpf(1.0f + __expf(-g)) * u;
+  else
+    return g / (1.0f + expf(-g)) * u;
 }
 
 __device__ __forceinline__ uint64_t lanemask_lt() {

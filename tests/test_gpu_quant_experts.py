@@ -506,3 +506,25 @@ def test_two_layers_at_once():
     for r, o in zip(ref, outs):
         for t in o:
             assert torch.equal(r, t)
+
+
+def test_fp32_act_is_exact_to_its_roundings():
+    """gate and up are exact in float32 here (integer sums below 2^24, scales that are powers of two), so what is left in
+    act is the exponential (within 3 units, 6 half units), the sum, the quotient and the product: 9 half units, and a tenth
+    for their products, whatever the size of gate."""
+    T, H, E, I = 700, 64, 3, 64  # noqa: E741
+    c = Case(T, H, E, 1, I, 1, "f32", seed=80)
+    c.qs.fill_(2.0 ** -6)
+    c.wgus.fill_(2.0 ** -4)
+    c.wgu.copy_(torch.randint(-30, 31, c.wgu.shape, generator=gen(81), device="cuda"))
+    act = torch.empty(T, I, device="cuda")
+    moe.moe_quant_gate_up_gather_pair(c.shape, 0, c.q, c.qs, c.src, c.offsets, c.wgu, c.wgus, act)
+    torch.cuda.synchronize()
+    _, _, exp, _ = c.pair_rows(0)
+    token = c.src.long()
+    p = products(c.q[token], c.qs[token], exp, c.wgu, c.wgus)
+    assert torch.equal(p, p.float().double())
+    g, u = p.chunk(2, 1)
+    assert -80 < float(g.min()) < -30  # no result below float32's normal range
+    ref = g * torch.sigmoid(g) * u
+    within(act, ref, 10 * U * ref.abs(), "act")
