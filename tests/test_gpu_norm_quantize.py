@@ -421,3 +421,42 @@ def test_rows_past_the_range_of_the_sums(dtype, H):
     for row in (1, 3, 6, 7):
         assert bool(sc[row].isnan()) and not q[row].any(), row
     assert bool(sc[[0, 2, 4, 5, 8]].isfinite().all())
+
+
+# rows that a workgroup of the gradient holds at a time (1024 threads of at most 16 values)
+GRAD_WIDTHS = [("bf16", 64, 16), ("bf16", 320, 16), ("bf16", 1024, 16), ("f32", 1020, 16), ("bf16", 1088, 8),
+               ("bf16", 2048, 8), ("f32", 1028, 8), ("bf16", 4096, 4), ("f32", 4100, 2), ("bf16", 7168, 2),
+               ("bf16", 8256, 1), ("f32", 16384, 1)]
+
+
+@pytest.mark.parametrize("dtype,H,par", GRAD_WIDTHS)
+def test_norm_backward_over_several_rows(dtype, H, par):
+    """Both sides of one workgroup (twice the rows it holds), of 256 workgroups, and several rows after one another in
+    each, the last of them ragged."""
+    for T, residual in ((par + 1, False), (2 * par, True), (2 * par + 1, False), (256 * par, True),
+                        (256 * par + 1, False), (563 * par + 7, True)):
+        say(f"norm_backward {dtype} T={T} H={H}")
+        s, dt = shape(T, H, dtype), no.TORCH[dtype]
+        x, (w, _) = rows(T, H, dtype, 43, 1.0), params(H, 44)
+        gy, gs = rows(T, H, dtype, 45), rows(T, H, dtype, 46) if residual else None
+        xd = x.double()
+        mean = xd.mean(1)
+        rstd = ((xd - mean[:, None]).square().mean(1) + EPS).rsqrt()
+        mean, rstd = mean.float(), rstd.float()
+        gx = torch.full((T, H), 7.0, dtype=dt, device="cuda")
+        wholew, gw = guarded(H, 4, torch.float32, 7.0)
+        wholeb, gb = guarded(H, 4, torch.float32, 7.0)
+        need = moe.moe_layer_norm_backward_workspace_size(s)
+        ws = torch.full((need + 256,), 0xff, dtype=torch.uint8, device="cuda")
+        moe.moe_layer_norm_backward(s, gy, x, w, mean, rstd, gs, gx, gw, gb, ws[:need])
+        torch.cuda.synchronize()
+        args = (f64(gy), f64(x), f64(w), f64(mean), f64(rstd), f64(gs) if residual else None)
+        for got, ref, bound, what in zip((gx, gw, gb), no.norm_grad(*args), no.norm_grad_bounds(*args, dtype),
+                                         ("grad_x", "grad_weight", "grad_bias")):
+            within(got, ref, bound, f"{what} of {T} rows")
+        assert bool((wholew[H:] == 7.0).all()) and bool((wholeb[H:] == 7.0).all()) and bool((ws[need:] == 0xff).all())
+        gx2, gw2, gb2 = torch.empty_like(gx), torch.empty_like(gw), torch.empty_like(gb)
+        ws.fill_(0xa5)
+        moe.moe_layer_norm_backward(s, gy, x, w, mean, rstd, gs, gx2, gw2, gb2, ws)
+        torch.cuda.synchronize()
+        assert torch.equal(gx, gx2) and torch.equal(gw, gw2) and torch.equal(gb, gb2)
