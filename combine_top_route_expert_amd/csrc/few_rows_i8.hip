@@ -7,15 +7,18 @@
 // between 5 us of sorting, 4 us of quantising and 4 us of combining.  Here nothing is
 // sorted: row f of act belongs to assignment f, whose expert is top_k_index[f].
 //  few_gate_up  every wave takes 4 gate rows and the up rows of the same columns for
-//               one assignment (5.6 us for that token)
+//               one assignment (5.8 us for that token)
 //  few_down     a workgroup takes one token's 16 output columns: it quantises the
 //               token's act rows into LDS (its waves take them in turn), then each
 //               wave multiplies 4 columns with two of the token's experts at a time
-//               and adds the weighted results in slot order (8.4 us)
+//               and adds the weighted results in slot order (8.6 us)
 // A wave's lanes hold 16 bytes of each kilobyte of K of 8 weight rows, so that 8 KB
-// or more are in flight, and a launch has as many waves as the weights have rows.
-// Memory bounds both from about E = 256, H = 7168 on (one token: 6 TB/s);
-// below that their own latency does.  An expert that two assignments share is read
+// or more are in flight.  few_gate_up has A I / 4 waves, one for every 8 weight
+// rows, few_down T H / 4, one for every 4 k rows: 1024 and 512 for that token, the
+// latter in 128 workgroups, half a wave for each SIMD.  Memory bounds both from about
+// E = 256, H = 7168 on (one token: 6 TB/s).  Below that their own latency does, and
+// few_down, with half the bytes, takes longer: fewer waves, slots in dependent rounds
+// of two, and the quantiser before the first weight load.  An expert that two assignments share is read
 // twice, mostly from the caches; few_rows() says when that is worth it.
 //
 // Dot products of four bytes at a time (v_dot4_i32_i8) give each lane 8 exact partial
@@ -172,6 +175,8 @@ __global__ void __launch_bounds__(64 * kWaves) few_down_i8(FewArgs a) {
     const int me = my_slot ? e[1] : e[0];
     float y = (float)wave_sum8(acc, lane);
     if (me >= 0) y = y * row_scale[j + my_slot] * a.b_scale[(int64_t)me * a.ncols + c0 + my_col];
+    // nothing is stored here, but the sorted path keeps y in bf16 (written and read
+    // again there, which fp32 would double), and both give the same bits
     if constexpr (kBf16) y = (float)(__bf16)y;
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
@@ -198,6 +203,9 @@ __global__ void __launch_bounds__(64 * kWaves) few_down_i8(FewArgs a) {
 //   E = 16, H = I = 2880, k = 4:  4: 58 / 29, 16: 93 / 70, 32: 97 / 127
 //   E = 8, H = 4096, I = 2048, k = 2:  2: 44 / 18, 8: 50 / 36, 16: 54 / 68
 //   E = 4, H = 2048, I = 1408, k = 2:  4: 33 / 14, 16: 34 / 21, 32: 34 / 36
+// The bound by E is on the safe side: it also leaves small experts that are shared
+// a few times, whose repeats come from the caches, to the slower sorted tiles (E = 4,
+// 16 assignments: 34 instead of 21 us).
 bool few_rows(const Shape& s) {
   return s.A > 0 && s.A <= 32 && (s.T == 1 || s.A <= s.E) && (int64_t)s.k * s.I <= kLdsRows;
 }

@@ -265,7 +265,13 @@ __global__ void __launch_bounds__(64 * WAVES_M * WAVES_N) grouped_gemm_i8(QuantA
 // So: at least 64 rows an expert on average, K of 2048 or more and a large tile for
 // every CU.  From 4096 rows on always the large one: the counts are known only on
 // the device, and when two of 256 experts get 8000 rows between them the small one
-// takes about twice as long, against at most a seventh lost on even counts.
+// takes about twice as long.  What that loses on even counts is a seventh where large
+// tiles fill the chip, and up to half where few experts with few column tiles make less
+// than one for every CU (E = 8 and 16 alike, gate_up / down, large against small):
+//   H = 2048, I = 256:  4096 rows 29 / 13 against 15 / 12;  8192: 29 / 24 against 20 / 18;
+//                      16384: 31 / 36 against 33 / 32
+//   H = 512, I = 2048:  4096 rows 30 / 27 against 26 / 14;  8192: 45 / 28 against 44 / 20;
+//                      16384: 76 / 30 against 81 / 32
 bool prefer_wide(const QuantArgs& a, int64_t rows_bound, int n_tiles) {
   if (rows_bound >= 4096) return true;
   return rows_bound >= 64 * (int64_t)a.E && a.row_bytes >= 2048 &&
