@@ -1,0 +1,521 @@
+"""Cases of the router in front of the MoE layer (forward and gradient), of the dropout behind it, of 4-bit expert weights
+and of the layer that multiplies with them, each with a plain torch form of the same mathematics.
+
+``own`` selects between the two: False runs elementary torch operations in float32 (float64 where a choice between two
+values is made), True the library's entry points.  ``exact`` computes the same outputs from the definition in float64.
+
+Definitions (rd rounds to the layer's dtype):
+  route      score = softmax or sigmoid of the logits; the k experts with the largest keys, ties to the lower id.  Key: the
+             logit, or where there is a bias or a group limit score + bias; a limit keeps the groups with the largest sum
+             of their two largest keys.  Weight: the score, divided by the chosen ones' sum if asked to, times a factor.
+             A logit of -inf is never chosen; a slot with no expert left has id -1 and weight 0
+  route_grad gradient of the logits from that of the weights
+  dropout    out = rd(residual + (x / (1 - p) where kept, else 0)); element 8 v + j is kept where the 16-bit half j of
+             Philox-4x32-10(counter v, offset; key seed) is at least p 2^16
+  weights    groups of 32 values of a row as E2M1 numbers (0 .5 1 1.5 2 3 4 6 and their negatives) times 2^s, s the least
+             integer with max|group| <= 6 2^s; then back
+  experts    act = rd(silu(g) u), y = rd(act W_down), out[t] = rd(sum_j top_k_weights[t][j] y of slot j); ids outside
+             [0, E) contribute nothing
+
+Packed 4-bit weights of R rows and C columns: values [R/32][C/64][64][16 bytes], where entry 32 h + r of block (b, k) holds
+row 32 b + r, columns 64 k + 32 h + 0..31, two to a byte, the even column in the low half; scales [R/32][ceil(C/256)][64][4
+bytes], where byte k % 4 of entry 32 h + r is that group's s + 127.
+"""
+import math
+
+import torch
+
+own = False
+
+
+def listed():
+    return [
+        # a decode batch through a router of 256 experts in 8 groups, 4 of them open to a token: the call's latency
+        dict(name="route_decode64", op="route", T=64, E=256, k=8, G=8, limit=4, score="sigmoid", bias=True, renorm=True,
+             factor=2.5, dtype="f32", mask=0.0),
+        # a packed 16k-token batch, bfloat16 logits (ties among them), some experts masked
+        dict(name="route_packed16k", op="route", T=16384, E=128, k=8, G=1, limit=0, score="softmax", bias=False,
+             renorm=True, factor=1.0, dtype="bf16", mask=0.05),
+        # the gradient of a ragged batch over a number of experts off every power of two
+        dict(name="route_grad_odd", op="route_grad", T=1531, E=60, k=4, score="sigmoid", renorm=True, factor=1.0,
+             dtype="f32", mask=0.1),
+        # the gradient of a packed 16k-token batch where every logit gets one
+        dict(name="route_grad_packed16k", op="route_grad", T=16384, E=256, k=8, score="softmax", renorm=False,
+             factor=1.0, dtype="f32", mask=0.0),
+        # the layer's output of a small micro-batch into the residual stream
+        dict(name="dropout_microbatch", op="dropout", T=64, H=7168, dtype="bf16", residual=True, p=0.1),
+        # its gradient for a packed 16k-token batch: no residual
+        dict(name="dropout_grad_packed16k", op="dropout", T=16384, H=2048, dtype="bf16", residual=False, p=0.1),
+        # a small float32 matrix to 4 bits and back
+        dict(name="weights_f32_odd", op="weights", rows=384, cols=320, dtype="f32"),
+        # gate and up rows of 8 large experts to 4 bits and back, as when a model is loaded
+        dict(name="weights_experts", op="weights", rows=8 * 4096, cols=7168, dtype="bf16"),
+        # one decoded token through the experts: the calls' latency
+        dict(name="experts_one_token", op="experts", T=1, H=2048, E=64, k=4, I=1024, N=1, skew=0.0, drop=0.0),
+        # a packed 16k-token batch in two chunks, uneven experts, some slots dropped by the router
+        dict(name="experts_packed16k", op="experts", T=16384, H=2048, E=128, k=8, I=768, N=2, skew=0.3, drop=0.02),
+        # a decode batch: bound by the experts' weights
+        dict(name="experts_decode64", op="experts", T=64, H=7168, E=256, k=8, I=2048, N=1, skew=0.0, drop=0.0),
+        # a prompt of 4096 tokens through the same layer
+        dict(name="experts_prompt4096", op="experts", T=4096, H=7168, E=256, k=8, I=2048, N=1, skew=0.0, drop=0.0),
+    ]
+
+
+def _spread(rng, lo, hi):
+    return int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))
+
+
+def draw(rng):
+    """A case of the same ranges: token counts over their logarithm, widths on the layer's granularity."""
+    op = rng.choice(["route", "route", "route_grad", "dropout", "weights", "experts", "experts", "experts"])
+    dtype = rng.choice(["bf16", "f32"])
+    T = _spread(rng, 1, 16384)
+    if op in ("route", "route_grad"):
+        E = _spread(rng, 2, 512)
+        c = dict(op=op, T=T, E=E, k=rng.randint(1, min(8, E)), score=rng.choice(["softmax", "sigmoid"]),
+                 renorm=rng.random() < 0.6, factor=rng.choice([1.0, 2.5]), dtype=dtype, mask=rng.choice([0.0, 0.1]))
+        if op == "route":
+            G = rng.choice([g for g in (1, 2, 3, 4, 8) if E % g == 0])
+            c.update(G=G, limit=rng.randint(0, G - 1) if G > 1 else 0, bias=rng.random() < 0.5)
+        return c
+    if op == "dropout":
+        step = 64 if dtype == "bf16" else 4
+        H = max(step, _spread(rng, 64, 8192) // step * step)
+        T = max(1, min(T, (16384 * 7168) // H))
+        return dict(op=op, T=T, H=H, dtype=dtype, residual=rng.random() < 0.5, p=rng.choice([0.0, 0.05, 0.1, 0.5]))
+    if op == "weights":
+        return dict(op=op, rows=32 * _spread(rng, 1, 512), cols=64 * _spread(rng, 1, 112), dtype=dtype)
+    T, k = _spread(rng, 1, 8192), rng.randint(1, 8)
+    H, I = 64 * rng.randint(2, 64), 64 * rng.randint(1, 32)  # noqa: E741
+    return dict(op=op, T=T, H=H, E=max(k, _spread(rng, 4, 128)), k=k, I=I, N=rng.randint(1, 3),
+                skew=round(rng.uniform(0.0, 0.6), 2), drop=rng.choice([0.0, 0.0, 0.05]))
+
+
+def _torch_dtype(case):
+    return torch.float32 if case.get("dtype") == "f32" else torch.bfloat16
+
+
+def _generator(seed):
+    return torch.Generator(device="cuda").manual_seed(int(seed))
+
+
+def _logits(case, g):
+    """Router logits whose experts differ in popularity; masked: some experts closed to all tokens, some rows wholly."""
+    T, E = case["T"], case["E"]
+    x = 1.5 * torch.randn(T, E, generator=g, device="cuda") + 0.7 * torch.randn(E, generator=g, device="cuda")
+    if case["mask"] > 0.0:
+        x[:, torch.rand(E, generator=g, device="cuda") < case["mask"]] = -math.inf
+        x[torch.rand(T, generator=g, device="cuda") < 0.1 * case["mask"]] = -math.inf
+    return x.to(_torch_dtype(case))
+
+
+def _routing(case, g):
+    """Expert choices of a router whose experts differ in popularity, and softmax weights over the chosen ones."""
+    T, E, k = case["T"], case["E"], case["k"]
+    rank = torch.argsort(torch.rand(E, generator=g, device="cuda")) + 1
+    logits = torch.randn(T, E, generator=g, device="cuda") - case["skew"] * torch.log(rank.float())
+    top, idx = torch.topk(logits, k, dim=1)
+    w = torch.softmax(top, dim=1)
+    idx = idx.to(torch.int32)
+    if case["drop"] > 0.0:
+        gone = torch.rand(T, k, generator=g, device="cuda") < case["drop"]
+        idx = torch.where(gone, torch.full_like(idx, -1), idx)
+    return idx.contiguous(), w.contiguous()
+
+
+def _packed(E, rows, cols, g):
+    """Packed weights of E experts as a serving program keeps them: values of a normal distribution in 4 bits, scales
+    that differ from group to group by a factor of four."""
+    nb, nk, nq = rows // 32, cols // 64, -(-cols // 256)
+    q = torch.empty(E, nb * nk * 1024, dtype=torch.uint8, device="cuda")
+    bounds = torch.tensor([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0], device="cuda")
+    for e in range(E):
+        x = torch.randn(nb * nk * 2048, generator=g, device="cuda").mul_(2.2)
+        code = torch.bucketize(x.abs(), bounds, out_int32=True) + 8 * (x < 0).int()
+        q[e] = (code[0::2] + 16 * code[1::2]).to(torch.uint8)
+    base = 127 - 1 - int(round(math.log2(2.2 * math.sqrt(cols))))
+    scale = torch.randint(base - 1, base + 2, (E, nb * nq * 256), generator=g, device="cuda", dtype=torch.uint8)
+    return q, scale
+
+
+def prepare(case, seed):
+    g, dt, op = _generator(seed), _torch_dtype(case), case["op"]
+    dev = dict(device="cuda")
+    s = dict(case)
+    if op in ("route", "route_grad"):
+        T, E, k = case["T"], case["E"], case["k"]
+        s["logits"] = _logits(case, g)
+        if op == "route":
+            s["b"] = 0.1 * torch.randn(E, generator=g, **dev) if case["bias"] else None
+            s["idx"], s["w"] = torch.empty(T, k, dtype=torch.int32, **dev), torch.empty(T, k, **dev)
+        else:
+            top, idx = torch.sort(s["logits"].float(), dim=1, descending=True, stable=True)
+            s["idx"] = torch.where(top > -math.inf, idx, torch.full_like(idx, -1))[:, :k].to(torch.int32).contiguous()
+            s["grad_w"] = 0.1 * torch.randn(T, k, generator=g, **dev)
+            s["grad"] = torch.empty(T, E, dtype=dt, **dev)
+        return s
+    if op == "dropout":
+        T, H = case["T"], case["H"]
+        s["x"] = torch.randn(T, H, generator=g, **dev).to(dt)
+        s["res"] = torch.randn(T, H, generator=g, **dev).to(dt) if case["residual"] else None
+        s["seed_offset"] = torch.randint(-(1 << 62), 1 << 62, (2,), generator=g, **dev)
+        s["out"] = torch.empty(T, H, dtype=dt, **dev)
+        return s
+    if op == "weights":
+        rows, cols = case["rows"], case["cols"]
+        # rows of different size, a group of zeros now and then
+        x = torch.randn(rows, cols, generator=g, **dev) * (0.02 * torch.exp(torch.randn(rows, 1, generator=g, **dev)))
+        x.view(rows, cols // 32, 32)[torch.rand(rows, cols // 32, generator=g, **dev) < 0.01] = 0.0
+        s["x"] = x.to(dt)
+        s["q"] = torch.empty(rows * cols // 2, dtype=torch.uint8, **dev)
+        s["scale"] = torch.empty(rows * 8 * -(-cols // 256), dtype=torch.uint8, **dev)
+        s["back"] = torch.empty(rows, cols, dtype=dt, **dev)
+        return s
+    T, H, E, I = case["T"], case["H"], case["E"], case["I"]  # noqa: E741
+    s["idx"], s["w"] = _routing(case, g)
+    s["x"] = torch.randn(T, H, generator=g, **dev).to(dt)
+    s["wgu"], s["wgu_scale"] = _packed(E, 2 * I, H, g)
+    s["wd"], s["wd_scale"] = _packed(E, H, I, g)
+    s["out"] = torch.empty(T, H, dtype=dt, **dev)
+    s["dropped"] = torch.zeros(1, dtype=torch.int32, **dev)
+    return s
+
+
+# ------------------------------------------------------------------ plain forms
+def _plain_scores(x, score):
+    """Scores of all experts; 0 where a logit is -inf, also where all of a row are."""
+    if score == "sigmoid":
+        return 1.0 / (1.0 + torch.exp(-x))
+    m = x.amax(1, keepdim=True)
+    e = torch.exp(x - torch.where(m > -math.inf, m, torch.zeros_like(m)))
+    total = e.sum(1, keepdim=True)
+    return e / torch.where(total > 0, total, torch.ones_like(total))
+
+
+def _plain_route(s):
+    x = s["logits"].double()
+    T, E = x.shape
+    score = _plain_scores(x, s["score"])
+    key, open_ = x, x > -math.inf
+    if s["b"] is not None or s["limit"] > 0:
+        key = score if s["b"] is None else score + s["b"].double()
+        key = torch.where(open_, key, torch.full_like(key, -math.inf))
+        if s["limit"] > 0:
+            G = s["G"]
+            best = torch.sort(key.view(T, G, E // G), dim=2, descending=True).values[:, :, :2].sum(2)
+            order = torch.sort(best, dim=1, descending=True, stable=True).indices
+            kept = torch.zeros(T, G, dtype=torch.bool, device=x.device)
+            kept.scatter_(1, order[:, : s["limit"]], True)
+            key = torch.where(kept.repeat_interleave(E // G, 1), key, torch.full_like(key, -math.inf))
+    top, idx = torch.sort(key, dim=1, descending=True, stable=True)
+    top, idx = top[:, : s["k"]], idx[:, : s["k"]]
+    w = torch.where(top > -math.inf, score.gather(1, idx), torch.zeros_like(top))
+    if s["renorm"]:
+        total = w.sum(1, keepdim=True)
+        w = w / torch.where(total > 0, total, torch.ones_like(total))
+    return {"idx": torch.where(top > -math.inf, idx, torch.full_like(idx, -1)).to(torch.int32),
+            "w": (w * s["factor"]).float()}
+
+
+def _plain_route_grad(s):
+    x = s["logits"].float()
+    score = _plain_scores(x, s["score"])
+    kept = s["idx"] >= 0
+    at = s["idx"].clamp_min(0).long()
+    gw = torch.where(kept, s["grad_w"] * s["factor"], torch.zeros_like(s["grad_w"]))
+    p = torch.where(kept, score.gather(1, at), torch.zeros_like(gw))
+    if s["renorm"]:
+        total = p.sum(1, keepdim=True)
+        total = torch.where(total > 0, total, torch.ones_like(total))
+        gw = torch.where(kept, (gw - (gw * p).sum(1, keepdim=True) / total) / total, torch.zeros_like(gw))
+    grad = torch.zeros_like(x).scatter_add_(1, at, gw)
+    if s["score"] == "sigmoid":
+        grad = grad * score * (1.0 - score)
+    else:
+        grad = score * (grad - (gw * p).sum(1, keepdim=True))
+    return grad.to(s["logits"].dtype)
+
+
+def _philox(v, offset, seed):
+    """Four 32-bit words (as int64) for every counter (v, offset) under the key `seed`, ten rounds."""
+    low = 0xFFFFFFFF
+    c = [v & low, v >> 32, (offset & low).expand_as(v), ((offset >> 32) & low).expand_as(v)]
+    k0, k1 = seed & low, (seed >> 32) & low
+
+    def product(a, m):
+        """High and low word of the 64-bit product of a 32-bit a and the constant m."""
+        t0 = (a & 0xFFFF) * m
+        t1 = (a >> 16) * m + (t0 >> 16)
+        return t1 >> 16, ((t1 & 0xFFFF) << 16) | (t0 & 0xFFFF)
+
+    for _ in range(10):
+        h0, l0 = product(c[0], 0xD2511F53)
+        h1, l1 = product(c[2], 0xCD9E8D57)
+        c = [h1 ^ c[1] ^ k0, l1, h0 ^ c[3] ^ k1, l0]
+        k0, k1 = (k0 + 0x9E3779B9) & low, (k1 + 0xBB67AE85) & low
+    return c
+
+
+def _plain_kept(s):
+    """Which of the T * H elements are kept, and the factor of those that are."""
+    n = s["T"] * s["H"]
+    seed, offset = s["seed_offset"][0], s["seed_offset"][1]
+    words = _philox(torch.arange(-(-n // 8), device="cuda"), offset, seed)
+    half = torch.stack([h for w in words for h in (w & 0xFFFF, w >> 16)], 1).reshape(-1)[:n]
+    least = min(65535, round(s["p"] * 65536))
+    return (half >= least).view(s["T"], s["H"]), 65536.0 / (65536 - least)
+
+
+def _plain_dropout(s):
+    kept, factor = _plain_kept(s)
+    x = s["x"].float()
+    out = torch.where(kept, x * factor, torch.zeros_like(x))
+    return (out if s["res"] is None else out + s["res"].float()).to(s["x"].dtype)
+
+
+def _plain_weights(x):
+    v = x.float().view(x.shape[0], -1, 32)
+    big = v.abs().amax(2, keepdim=True)
+    m, e = torch.frexp(big)  # big = m 2^e, m in [0.5, 1); 6 = 0.75 2^3
+    step = torch.ldexp(torch.ones_like(big), e - 3 + (m > 0.75).int())
+    t = v / step
+    a = t.abs()
+    # E2M1 numbers lie 0.5 apart up to 2, 1 apart up to 4, 2 apart up to 6
+    gap = torch.where(a < 2.0, 0.5, torch.where(a < 4.0, 1.0, 2.0))
+    return (torch.round(t / gap) * gap * step).to(x.dtype).view_as(x)
+
+
+_E2M1 = (0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0)
+
+
+def _unpacked(q, scale, rows, cols):
+    """float32 values of packed weights of several experts: [e][rows][cols]."""
+    e, nb, nk, nq = q.shape[0], rows // 32, cols // 64, -(-cols // 256)
+    one = torch.tensor(_E2M1 + tuple(-v for v in _E2M1), device=q.device)
+    pairs = torch.stack([one.repeat(16), one.repeat_interleave(16)], 1)  # of a byte: its low half, its high half
+    v = pairs.index_select(0, q.reshape(-1).int()).view(e, nb, nk, 2, 32, 32)
+    power = torch.exp2(scale.float() - 127.0).view(e, nb, nq, 2, 32, 4).permute(0, 1, 2, 5, 3, 4)
+    v = v * power.reshape(e, nb, nq * 4, 2, 32)[:, :, :nk, :, :, None]
+    return v.permute(0, 1, 4, 2, 3, 5).reshape(e, rows, cols)
+
+
+def _slots(flat, E):
+    """Padded place [expert][position] of every assignment (the last place takes what is dropped), and the padding."""
+    key = torch.where((flat >= 0) & (flat < E), flat, torch.full_like(flat, E)).long()
+    order = torch.argsort(key, stable=True)
+    count = torch.bincount(key, minlength=E + 1)
+    cap = max(1, int(count[:E].max()))
+    first = torch.cumsum(count, 0) - count
+    place = key[order] * cap + torch.arange(key.numel(), device=key.device) - first[key[order]]
+    slot = torch.empty_like(order)
+    slot[order] = torch.where(key[order] < E, place, torch.full_like(place, E * cap))
+    return slot, cap
+
+
+def _plain_experts(s):
+    E, k, H, I = s["E"], s["k"], s["H"], s["I"]  # noqa: E741
+    T = s["T"]
+    slot, cap = _slots(s["idx"].reshape(-1), E)
+    token = torch.full((E * cap + 1,), T, dtype=torch.long, device="cuda")
+    token[slot] = torch.arange(T * k, device="cuda") // k
+    x = torch.cat([s["x"].float(), torch.zeros(1, H, device="cuda")])
+    y = torch.zeros(E * cap + 1, H, device="cuda")
+    step = max(1, (1 << 28) // (2 * I * H))  # experts whose weights are laid out in float32 at a time
+    for e in range(0, E, step):
+        n = min(step, E - e)
+        rows = x[token[e * cap: (e + n) * cap]].view(n, cap, H).transpose(1, 2).contiguous()
+        p = torch.bmm(_unpacked(s["wgu"][e: e + n], s["wgu_scale"][e: e + n], 2 * I, H), rows)
+        g, u = p.chunk(2, dim=1)
+        act = (g / (1.0 + torch.exp(-g)) * u).contiguous()
+        r = torch.bmm(_unpacked(s["wd"][e: e + n], s["wd_scale"][e: e + n], H, I), act)
+        y[e * cap: (e + n) * cap] = r.transpose(1, 2).reshape(n * cap, H)
+    y[E * cap] = 0.0
+    return (y[slot].view(T, k, H) * s["w"][:, :, None]).sum(1).to(s["x"].dtype)
+
+
+def run(state):
+    s = state
+    if own:
+        return _run_own(s)
+    op = s["op"]
+    if op == "route":
+        return _plain_route(s)
+    if op == "route_grad":
+        return _plain_route_grad(s)
+    if op == "dropout":
+        return _plain_dropout(s)
+    if op == "weights":
+        return _plain_weights(s["x"])
+    return _plain_experts(s)
+
+
+# ------------------------------------------------------------------ the library's entry points
+def _run_own(s):
+    import combine_top_route_expert_amd as moe
+
+    op = s["op"]
+    if op == "weights":
+        moe.moe_quantize_fp4(s["rows"], s["cols"], s["dtype"], s["x"], s["q"], s["scale"])
+        moe.moe_dequantize_fp4(s["rows"], s["cols"], s["dtype"], s["q"], s["scale"], s["back"])
+        return s["back"]
+    shape = s.get("shape")
+    if shape is None:
+        shape = moe.make_shape(s["T"], s.get("H", 64), s.get("E", 1), s.get("k", 1), s.get("I", 64), s.get("G", 1),
+                               s.get("N", 1), s.get("dtype", "bf16"))
+        s["shape"] = shape
+        if op == "experts":
+            s["ws"] = torch.empty(moe.moe_fp4_workspace_size(shape), dtype=torch.uint8, device="cuda")
+    if op == "route":
+        moe.moe_router_top_k(shape, s["logits"], s["b"], s["score"], s["limit"], s["renorm"], s["factor"], s["idx"],
+                             s["w"])
+        return {"idx": s["idx"], "w": s["w"]}
+    if op == "route_grad":
+        moe.moe_router_top_k_backward(shape, s["logits"], s["idx"], s["grad_w"], s["score"], s["renorm"], s["factor"],
+                                      s["grad"])
+        return s["grad"]
+    if op == "dropout":
+        moe.moe_dropout_add(shape, s["x"], s["res"], s["p"], s["seed_offset"], s["out"])
+        return s["out"]
+    moe.moe_fp4_forward(shape, s["x"], s["idx"], s["w"], s["wgu"], s["wgu_scale"], s["wd"], s["wd_scale"], s["out"],
+                        s["ws"], s["dropped"])
+    return s["out"]
+
+
+# ------------------------------------------------------------------ cost and the values in 64 bits
+def work(case):
+    op, el = case["op"], 4 if case.get("dtype") == "f32" else 2
+    if op == "weights":
+        n = case["rows"] * case["cols"]
+        # values read, 4 bits and a byte for 32 written, then the other way
+        return {"bytes": 2 * n * (el + 17 / 32), "flops": 6 * n}
+    T = case["T"]
+    if op == "route":
+        return {"bytes": T * (case["E"] * el + 8 * case["k"]) + 4 * case["E"], "flops": 8 * T * case["E"]}
+    if op == "route_grad":
+        return {"bytes": T * (2 * case["E"] * el + 8 * case["k"]), "flops": 8 * T * case["E"]}
+    if op == "dropout":
+        return {"bytes": T * case["H"] * el * (3 if case["residual"] else 2) + 16, "flops": 12 * T * case["H"]}
+    H, E, k, I = case["H"], case["E"], case["k"], case["I"]  # noqa: E741
+    active = E * (1.0 - (1.0 - k / E) ** T)  # experts that T tokens reach when they choose evenly
+    return {"bytes": active * 3 * H * I * 17 / 32 + 2 * T * H * el + 8 * T * k, "flops": 6 * T * k * H * I}
+
+
+def _exact_route(s):
+    x = s["logits"].double().cpu()
+    T, E = x.shape
+    if s["score"] == "sigmoid":
+        score = torch.sigmoid(x)
+    else:
+        score = torch.softmax(x, 1).nan_to_num(0.0)
+    key = x.clone()
+    if s["b"] is not None or s["limit"] > 0:
+        key = score + (s["b"].double().cpu() if s["b"] is not None else 0.0)
+        key[x == -math.inf] = -math.inf
+    idx, w = torch.full((T, s["k"]), -1, dtype=torch.int32), torch.zeros(T, s["k"], dtype=torch.float64)
+    if s["limit"] > 0:
+        G = s["G"]
+        part = key.view(T, G, -1)
+        first = part.max(2)
+        rest = part.clone().scatter_(2, first.indices[:, :, None], -math.inf)
+        total = first.values + (rest.max(2).values if E > G else 0.0)
+        closed = torch.ones(T, G, dtype=torch.bool)
+        for _ in range(s["limit"]):
+            best = total.max(1, keepdim=True).values
+            at = ((total == best) & closed).int().argmax(1)  # the first of the largest
+            closed[torch.arange(T), at] = False
+            total[torch.arange(T), at] = math.nan
+            total = torch.where(total.isnan(), torch.full_like(total, -math.inf), total)
+        part[closed] = -math.inf
+    for j in range(s["k"]):
+        best = key.max(1, keepdim=True).values
+        at = (key == best).int().argmax(1)
+        ok = best[:, 0] > -math.inf
+        idx[ok, j] = at[ok].int()
+        w[ok, j] = score[torch.arange(T), at][ok]
+        key[torch.arange(T), at] = -math.inf
+    if s["renorm"]:
+        w = (w / w.sum(1, keepdim=True)).nan_to_num(0.0)
+    return {"idx": idx.cuda(), "w": (w * s["factor"]).cuda()}
+
+
+def _exact_route_grad(s):
+    x = s["logits"].double().requires_grad_()
+    none = (x == -math.inf).all(1, keepdim=True)
+    safe = torch.where(none, torch.zeros_like(x), x)
+    score = torch.sigmoid(safe) if s["score"] == "sigmoid" else torch.softmax(safe, 1)
+    kept = s["idx"] >= 0
+    w = torch.where(kept, score.gather(1, s["idx"].clamp_min(0).long()), 0.0)
+    if s["renorm"]:
+        w = w / torch.where(none, 1.0, w.sum(1, keepdim=True))
+    (w * s["factor"] * s["grad_w"].double()).sum().backward()
+    return torch.where(torch.isfinite(s["logits"]), x.grad, 0.0)
+
+
+def _exact_kept(s):
+    """The mask by Python-independent arithmetic: 64-bit products in numpy's unsigned integers."""
+    import numpy as np
+    n = s["T"] * s["H"]
+    v = np.arange(-(-n // 8), dtype=np.uint64)
+    seed, off = (int(t) & 0xFFFFFFFFFFFFFFFF for t in s["seed_offset"].tolist())
+    low = np.uint64(0xFFFFFFFF)
+    x, y = v & low, v >> np.uint64(32)
+    z, t = np.full_like(v, off & 0xFFFFFFFF), np.full_like(v, off >> 32)
+    ka, kb = seed & 0xFFFFFFFF, seed >> 32
+    for r in range(10):
+        a, b = x * np.uint64(0xD2511F53), z * np.uint64(0xCD9E8D57)
+        x, y, z, t = ((b >> np.uint64(32)) ^ y ^ np.uint64((ka + r * 0x9E3779B9) & 0xFFFFFFFF), b & low,
+                      (a >> np.uint64(32)) ^ t ^ np.uint64((kb + r * 0xBB67AE85) & 0xFFFFFFFF), a & low)
+    halves = np.stack([x, y, z, t], 1).astype(np.uint32).view(np.uint16).reshape(-1)[:n]
+    return torch.from_numpy((halves >= min(65535, round(s["p"] * 65536)))).view(s["T"], s["H"]).cuda()
+
+
+def _exact_weights(x):
+    v = x.double().view(x.shape[0], -1, 32)
+    big = v.abs().amax(2, keepdim=True)
+    step = torch.exp2(torch.ceil(torch.log2(big.clamp_min(1e-300) / 6.0)))
+    step = torch.where(big > 6.0 * step, 2.0 * step, torch.where(big <= 3.0 * step, 0.5 * step, step))
+    grid = torch.tensor(_E2M1, dtype=torch.float64, device=x.device)
+    a = v.abs() / step
+    at = torch.bucketize(a.contiguous(), (grid[1:] + grid[:-1]) / 2)  # a tie stays below
+    even = torch.where((at < 7) & (at % 2 == 1) & (a == ((grid[1:] + grid[:-1]) / 2)[at.clamp_max(6)]), at + 1, at)
+    return (torch.sign(v) * grid[even] * step).view_as(x)
+
+
+def _exact_matrix(q, scale, rows, cols):
+    """One expert's packed matrix in float64, nibble by nibble."""
+    nk = cols // 64
+    lo, hi = (q & 15).long(), (q >> 4).long()
+    code = torch.stack([lo, hi], -1).view(rows // 32, nk, 2, 32, 32)
+    grid = torch.tensor(_E2M1, dtype=torch.float64, device=q.device)
+    v = grid[code & 7] * (1 - 2 * (code >> 3)).double()
+    c = torch.arange(cols // 32, device=q.device)
+    r = torch.arange(rows, device=q.device)[:, None]
+    at = ((r // 32) * -(-cols // 256) + c // 8) * 256 + ((c % 2) * 32 + r % 32) * 4 + (c // 2) % 4
+    power = torch.ldexp(torch.ones(rows, cols // 32, dtype=torch.float64, device=q.device), scale[at].int() - 127)
+    return v.permute(0, 3, 1, 2, 4).reshape(rows, cols) * power.repeat_interleave(32, 1)
+
+
+def exact(case, seed):
+    s, op = prepare(case, seed), case["op"]
+    if op == "route":
+        return _exact_route(s)
+    if op == "route_grad":
+        return _exact_route_grad(s)
+    if op == "dropout":
+        least = min(65535, round(s["p"] * 65536))
+        out = torch.where(_exact_kept(s), s["x"].double() * (65536.0 / (65536 - least)), 0.0)
+        return out if s["res"] is None else out + s["res"].double()
+    if op == "weights":
+        return _exact_weights(s["x"])
+    H, E, I = case["H"], case["E"], case["I"]  # noqa: E741
+    res = torch.zeros(case["T"], H, dtype=torch.float64, device="cuda")
+    hidden = s["x"].double()
+    for e in range(E):
+        t, j = torch.nonzero(s["idx"] == e, as_tuple=True)
+        if t.numel() == 0:
+            continue
+        p = hidden[t] @ _exact_matrix(s["wgu"][e], s["wgu_scale"][e], 2 * I, H).T.contiguous()
+        act = p[:, :I] * torch.sigmoid(p[:, :I]) * p[:, I:]
+        y = act @ _exact_matrix(s["wd"][e], s["wd_scale"][e], H, I).T.contiguous()
+        res.index_add_(0, t, y * s["w"][t, j].double()[:, None])
+    return res
