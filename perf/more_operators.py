@@ -355,8 +355,8 @@ def _run_own(s):
 
     op = s["op"]
     if op == "weights":
-        moe.moe_quantize_fp4(s["rows"], s["cols"], s["dtype"], s["x"], s["q"], s["scale"])
-        moe.moe_dequantize_fp4(s["rows"], s["cols"], s["dtype"], s["q"], s["scale"], s["back"])
+        moe.moe_quantize_mx(s["rows"], s["cols"], s["dtype"], s["x"], s["q"], s["scale"])
+        moe.moe_dequantize_mx(s["rows"], s["cols"], s["dtype"], s["q"], s["scale"], s["back"])
         return s["back"]
     shape = s.get("shape")
     if shape is None:
@@ -364,7 +364,7 @@ def _run_own(s):
                                s.get("N", 1), s.get("dtype", "bf16"))
         s["shape"] = shape
         if op == "experts":
-            s["ws"] = torch.empty(moe.moe_fp4_workspace_size(shape), dtype=torch.uint8, device="cuda")
+            s["ws"] = torch.empty(moe.moe_mx_workspace_size(shape), dtype=torch.uint8, device="cuda")
     if op == "route":
         moe.moe_router_top_k(shape, s["logits"], s["b"], s["score"], s["limit"], s["renorm"], s["factor"], s["idx"],
                              s["w"])
@@ -376,7 +376,7 @@ def _run_own(s):
     if op == "dropout":
         moe.moe_dropout_add(shape, s["x"], s["res"], s["p"], s["seed_offset"], s["out"])
         return s["out"]
-    moe.moe_fp4_forward(shape, s["x"], s["idx"], s["w"], s["wgu"], s["wgu_scale"], s["wd"], s["wd_scale"], s["out"],
+    moe.moe_mx_forward(shape, s["x"], s["idx"], s["w"], s["wgu"], s["wgu_scale"], s["wd"], s["wd_scale"], s["out"],
                         s["ws"], s["dropped"])
     return s["out"]
 
