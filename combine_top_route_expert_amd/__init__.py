@@ -30,7 +30,8 @@ __all__ = [
     "moe_chunked_forward_noalloc", "moe_layer_norm", "moe_layer_norm_quantize",
     "moe_layer_norm_backward_workspace_size", "moe_layer_norm_backward", "moe_quantize_rows",
     "moe_quant_gate_up_gather_pair", "moe_quant_act_pair", "moe_quant_down_pair",
-    "moe_quant_workspace_size", "moe_quant_forward",
+    "moe_quant_workspace_size", "moe_quant_forward", "moe_router_top_k", "moe_router_top_k_backward",
+    "moe_dropout_add", "moe_mx_scale_size", "moe_quantize_mx", "moe_pack_mx", "moe_dequantize_mx",
 ]
 
 MOE_F32, MOE_BF16 = 0, 1
@@ -50,6 +51,8 @@ EXPORTED_SYMBOLS = (
     "moe_layer_norm", "moe_layer_norm_quantize", "moe_layer_norm_backward_workspace_size",
     "moe_layer_norm_backward", "moe_quantize_rows", "moe_quant_gate_up_gather_pair",
     "moe_quant_act_pair", "moe_quant_down_pair", "moe_quant_workspace_size", "moe_quant_forward",
+    "moe_router_top_k", "moe_router_top_k_backward", "moe_dropout_add", "moe_mx_scale_size",
+    "moe_quantize_mx", "moe_pack_mx", "moe_dequantize_mx",
 )
 
 
@@ -168,6 +171,20 @@ def load_library() -> ctypes.CDLL:
         "moe_quant_workspace_size": (ctypes.c_int, [_SP, ctypes.POINTER(ctypes.c_size_t)]),
         "moe_quant_forward": (ctypes.c_int, [_SP, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P,
                                              ctypes.c_size_t, _P]),
+        "moe_router_top_k": (ctypes.c_int, [_SP, ctypes.c_int32, _P, _P, ctypes.c_int32,
+                                            ctypes.c_int32, ctypes.c_int32, ctypes.c_float, _P, _P,
+                                            _P]),
+        "moe_router_top_k_backward": (ctypes.c_int, [_SP, ctypes.c_int32, _P, _P, _P,
+                                                     ctypes.c_int32, ctypes.c_int32,
+                                                     ctypes.c_float, _P, _P]),
+        "moe_dropout_add": (ctypes.c_int, [_SP, _P, _P, ctypes.c_double, _P, _P, _P]),
+        "moe_mx_scale_size": (ctypes.c_int, [ctypes.c_int64, ctypes.c_int64,
+                                              ctypes.POINTER(ctypes.c_size_t)]),
+        "moe_quantize_mx": (ctypes.c_int, [ctypes.c_int64, ctypes.c_int64, ctypes.c_int32, _P, _P,
+                                            _P, _P]),
+        "moe_pack_mx": (ctypes.c_int, [ctypes.c_int64, ctypes.c_int64, _P, _P, _P, _P, _P]),
+        "moe_dequantize_mx": (ctypes.c_int, [ctypes.c_int64, ctypes.c_int64, ctypes.c_int32, _P,
+                                              _P, _P, _P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -659,3 +676,100 @@ def moe_quant_forward(shape: moe_shape, hidden_q, hidden_scale, top_k_index, top
         (out, shape.torch_dtype, T * H, "out"), (dev_error, i32, 1, "dev_error", True),
         (ws, torch.uint8, 1, "ws"))
     _call("moe_quant_forward", index, stream, ctypes.byref(shape), *ptrs, ws.numel())
+
+
+# ---------------------------------------------------------------- router, dropout
+_SCORE = {"softmax": 0, "sigmoid": 1}
+
+
+def _score(score: str) -> int:
+    if score not in _SCORE:
+        raise ValueError(f"score must be 'softmax' or 'sigmoid', got {score!r}")
+    return _SCORE[score]
+
+
+def _logits_dtype(logits) -> torch.dtype:
+    return logits.dtype if getattr(logits, "dtype", None) is torch.bfloat16 else torch.float32
+
+
+def moe_router_top_k(shape: moe_shape, logits, bias, score: str, group_limit: int,
+                     renormalize: bool, factor: float, top_k_index, top_k_weights,
+                     stream=None) -> None:
+    """Each token's k experts and weights from its logits (float32 or bfloat16); bias may be None,
+    group_limit 0."""
+    T, E = shape.num_tokens, shape.num_experts
+    A, dt, kind = T * shape.top_k, _logits_dtype(logits), _score(score)
+    index, (lp, bp, ip, wp) = _pointers(
+        (logits, dt, T * E, "logits"), (bias, torch.float32, E, "bias", True),
+        (top_k_index, torch.int32, A, "top_k_index"),
+        (top_k_weights, torch.float32, A, "top_k_weights"))
+    _call("moe_router_top_k", index, stream, ctypes.byref(shape),
+          MOE_BF16 if dt is torch.bfloat16 else MOE_F32, lp, bp, kind, group_limit,
+          1 if renormalize else 0, factor, ip, wp)
+
+
+def moe_router_top_k_backward(shape: moe_shape, logits, top_k_index, grad_top_k_weights, score: str,
+                              renormalize: bool, factor: float, grad_logits, stream=None) -> None:
+    """Gradient of the logits (in their dtype) from that of top_k_weights."""
+    n = shape.num_tokens * shape.num_experts
+    A, dt, kind = shape.num_tokens * shape.top_k, _logits_dtype(logits), _score(score)
+    index, (lp, ip, gp, dp) = _pointers(
+        (logits, dt, n, "logits"), (top_k_index, torch.int32, A, "top_k_index"),
+        (grad_top_k_weights, torch.float32, A, "grad_top_k_weights"),
+        (grad_logits, dt, n, "grad_logits"))
+    _call("moe_router_top_k_backward", index, stream, ctypes.byref(shape),
+          MOE_BF16 if dt is torch.bfloat16 else MOE_F32, lp, ip, gp, kind,
+          1 if renormalize else 0, factor, dp)
+
+
+def moe_dropout_add(shape: moe_shape, x, residual, p: float, seed_offset, out, stream=None) -> None:
+    """out = residual + dropout of x (residual may be None); seed_offset: two int64 on the device.
+    The gradient of x: the same call on the gradient of out, without a residual."""
+    dt, n = shape.torch_dtype, shape.num_tokens * shape.hidden
+    index, (xp, rp, sp, op) = _pointers(
+        (x, dt, n, "x"), (residual, dt, n, "residual", True),
+        (seed_offset, torch.int64, 2, "seed_offset"), (out, dt, n, "out"))
+    _call("moe_dropout_add", index, stream, ctypes.byref(shape), xp, rp, p, sp, op)
+
+
+# ---------------------------------------------------------------- 4-bit weights
+def moe_mx_scale_size(rows: int, cols: int) -> int:
+    b = ctypes.c_size_t()
+    _check("moe_mx_scale_size", load_library().moe_mx_scale_size(rows, cols, ctypes.byref(b)))
+    return b.value
+
+
+def _fp4_matrix(rows: int, cols: int, dtype: str):
+    """(torch dtype, moe_dtype, bytes of the values, bytes of the scales) of a packed matrix; sizes
+    that the library refuses need no buffer here."""
+    if dtype not in ("bf16", "f32"):
+        raise ValueError(f"dtype must be 'bf16' or 'f32', got {dtype!r}")
+    bf16 = dtype == "bf16"
+    return (torch.bfloat16 if bf16 else torch.float32, MOE_BF16 if bf16 else MOE_F32,
+            rows * cols // 2, rows // 32 * -(-cols // 256) * 256)
+
+
+def moe_quantize_mx(rows: int, cols: int, dtype: str, x, q, scale, stream=None) -> None:
+    """x ("bf16" or "f32") as a packed 4-bit matrix: q and scale uint8."""
+    dt, code, nq, ns = _fp4_matrix(rows, cols, dtype)
+    index, ptrs = _pointers((x, dt, rows * cols, "x"), (q, torch.uint8, nq, "q"),
+                            (scale, torch.uint8, ns, "scale"))
+    _call("moe_quantize_mx", index, stream, rows, cols, code, *ptrs)
+
+
+def moe_pack_mx(rows: int, cols: int, q_rows, scale_rows, q, scale, stream=None) -> None:
+    """A matrix already in 4 bits, row by row, as a packed one."""
+    _, _, nq, ns = _fp4_matrix(rows, cols, "bf16")
+    u8 = torch.uint8
+    index, ptrs = _pointers((q_rows, u8, nq, "q_rows"),
+                            (scale_rows, u8, rows * cols // 32, "scale_rows"), (q, u8, nq, "q"),
+                            (scale, u8, ns, "scale"))
+    _call("moe_pack_mx", index, stream, rows, cols, *ptrs)
+
+
+def moe_dequantize_mx(rows: int, cols: int, dtype: str, q, scale, x, stream=None) -> None:
+    """The values of a packed 4-bit matrix as x ("bf16" or "f32")."""
+    dt, code, nq, ns = _fp4_matrix(rows, cols, dtype)
+    index, ptrs = _pointers((q, torch.uint8, nq, "q"), (scale, torch.uint8, ns, "scale"),
+                            (x, dt, rows * cols, "x"))
+    _call("moe_dequantize_mx", index, stream, rows, cols, code, *ptrs)

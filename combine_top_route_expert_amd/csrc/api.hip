@@ -5,6 +5,7 @@
 #include <mutex>
 #include <vector>
 
+#include "fp4_layout.h"
 #include "moe_internal.h"
 
 namespace moe {
@@ -1214,6 +1215,122 @@ moe_status moe_quant_forward(const moe_shape* shape, const int8_t* hidden_q,
                      : launch_combine(s, t0, t1, y0, dst_row, top_k_weights, out, stream);
   }
   return hip_status(he);
+}
+
+namespace moe {
+namespace {
+
+moe_status router_args(const moe_shape* shape, int32_t dtype, const void* logits, int32_t score,
+                       float factor, const void* idx, const void* w, Shape* s) {
+  const moe_status st = resolve_shape(shape, s);
+  if (st != MOE_OK) return st;
+  if ((dtype != MOE_F32 && dtype != MOE_BF16) ||
+      (score != MOE_SCORE_SOFTMAX && score != MOE_SCORE_SIGMOID) ||
+      !(factor >= -3.4028235e38f && factor <= 3.4028235e38f))
+    return MOE_ERR_INVALID_ARG;
+  if (s->T > 0 && (!buf_ok(logits, 1) || !idx || !w || !aligned(idx, 4) || !aligned(w, 4)))
+    return MOE_ERR_INVALID_ARG;
+  return MOE_OK;
+}
+
+// Limits of the packed 4-bit matrices; *empty where there is nothing to do.
+moe_status fp4_matrix(int64_t rows, int64_t cols, bool* empty) {
+  if (rows < 0 || cols < 1) return MOE_ERR_INVALID_ARG;
+  if (rows % kFp4BlockRows || cols % kFp4BlockCols) return MOE_ERR_UNSUPPORTED;
+  if (rows > 0 && fp4_scale_quads(cols) > 0x7fffffffLL / (rows / kFp4BlockRows))
+    return MOE_ERR_UNSUPPORTED;
+  *empty = rows == 0;
+  return MOE_OK;
+}
+
+}  // namespace
+}  // namespace moe
+
+moe_status moe_router_top_k(const moe_shape* shape, int32_t logits_dtype, const void* logits,
+                            const float* bias, int32_t score, int32_t group_limit,
+                            int32_t renormalize, float factor, int32_t* top_k_index,
+                            float* top_k_weights, hipStream_t stream) {
+  Shape s;
+  const moe_status st =
+      router_args(shape, logits_dtype, logits, score, factor, top_k_index, top_k_weights, &s);
+  if (st != MOE_OK) return st;
+  if (group_limit < 0 || group_limit > s.G || !aligned(bias, 4)) return MOE_ERR_INVALID_ARG;
+  if (!router_limit_ok(s, group_limit)) return MOE_ERR_UNSUPPORTED;
+  if (s.T == 0) return MOE_OK;
+  const RouterIO io{logits, logits_dtype == MOE_BF16, bias, score == MOE_SCORE_SIGMOID,
+                    group_limit, renormalize != 0, factor, top_k_index, top_k_weights,
+                    nullptr, nullptr};
+  return hip_status(launch_router_top_k(s, io, stream));
+}
+
+moe_status moe_router_top_k_backward(const moe_shape* shape, int32_t logits_dtype,
+                                     const void* logits, const int32_t* top_k_index,
+                                     const float* grad_top_k_weights, int32_t score,
+                                     int32_t renormalize, float factor, void* grad_logits,
+                                     hipStream_t stream) {
+  Shape s;
+  const moe_status st =
+      router_args(shape, logits_dtype, logits, score, factor, top_k_index, grad_top_k_weights, &s);
+  if (st != MOE_OK) return st;
+  if (s.T == 0) return MOE_OK;
+  if (!buf_ok(grad_logits, 1) || grad_logits == logits) return MOE_ERR_INVALID_ARG;
+  const RouterIO io{logits, logits_dtype == MOE_BF16, nullptr, score == MOE_SCORE_SIGMOID,
+                    0, renormalize != 0, factor, const_cast<int32_t*>(top_k_index), nullptr,
+                    grad_top_k_weights, grad_logits};
+  return hip_status(launch_router_top_k_backward(s, io, stream));
+}
+
+moe_status moe_dropout_add(const moe_shape* shape, const void* x, const void* residual, double p,
+                           const uint64_t* seed_offset, void* out, hipStream_t stream) {
+  Shape s;
+  const moe_status st = resolve_shape(shape, &s);
+  if (st != MOE_OK) return st;
+  if (!(p >= 0.0 && p < 1.0)) return MOE_ERR_INVALID_ARG;
+  if (s.T == 0) return MOE_OK;
+  if (!buf_ok(x, 1) || !aligned(residual, 16) || !seed_offset || !aligned(seed_offset, 8) ||
+      !buf_ok(out, 1))
+    return MOE_ERR_INVALID_ARG;
+  return hip_status(launch_dropout_add(s, x, residual, p, seed_offset, out, stream));
+}
+
+moe_status moe_mx_scale_size(int64_t rows, int64_t cols, size_t* bytes) {
+  bool empty;
+  const moe_status st = fp4_matrix(rows, cols, &empty);
+  if (st != MOE_OK) return st;
+  if (!bytes) return MOE_ERR_INVALID_ARG;
+  *bytes = (size_t)fp4_scale_bytes(rows, cols);
+  return MOE_OK;
+}
+
+moe_status moe_quantize_mx(int64_t rows, int64_t cols, int32_t dtype, const void* x, uint8_t* q,
+                            uint8_t* scale, hipStream_t stream) {
+  if (dtype != MOE_F32 && dtype != MOE_BF16) return MOE_ERR_INVALID_ARG;
+  bool empty;
+  const moe_status st = fp4_matrix(rows, cols, &empty);
+  if (st != MOE_OK || empty) return st;
+  if (!buf_ok(x, 1) || !buf_ok(q, 1) || !buf_ok(scale, 1)) return MOE_ERR_INVALID_ARG;
+  return hip_status(launch_quantize_fp4(rows, cols, dtype == MOE_BF16, x, q, scale, stream));
+}
+
+moe_status moe_pack_mx(int64_t rows, int64_t cols, const uint8_t* q_rows,
+                        const uint8_t* scale_rows, uint8_t* q, uint8_t* scale,
+                        hipStream_t stream) {
+  bool empty;
+  const moe_status st = fp4_matrix(rows, cols, &empty);
+  if (st != MOE_OK || empty) return st;
+  if (!q_rows || !aligned(q_rows, 4) || !scale_rows || !buf_ok(q, 1) || !buf_ok(scale, 1))
+    return MOE_ERR_INVALID_ARG;
+  return hip_status(launch_pack_fp4(rows, cols, q_rows, scale_rows, q, scale, stream));
+}
+
+moe_status moe_dequantize_mx(int64_t rows, int64_t cols, int32_t dtype, const uint8_t* q,
+                              const uint8_t* scale, void* x, hipStream_t stream) {
+  if (dtype != MOE_F32 && dtype != MOE_BF16) return MOE_ERR_INVALID_ARG;
+  bool empty;
+  const moe_status st = fp4_matrix(rows, cols, &empty);
+  if (st != MOE_OK || empty) return st;
+  if (!buf_ok(x, 1) || !buf_ok(q, 1) || !buf_ok(scale, 1)) return MOE_ERR_INVALID_ARG;
+  return hip_status(launch_dequantize_fp4(rows, cols, dtype == MOE_BF16, q, scale, x, stream));
 }
 
 }  // extern "C"

@@ -123,6 +123,39 @@ hipError_t launch_quantize_rows(int64_t rows, int64_t cols, bool bf16, const voi
                                 float* scale, const int32_t* valid0, const int32_t* valid1,
                                 hipStream_t st);
 
+// ---- router (router.hip) ---------------------------------------------------------
+struct RouterIO {
+  const void* logits;    // [T][E], bf16 or fp32
+  bool bf16;
+  const float* bias;     // [E], optional
+  bool sigmoid;          // scores: sigmoid, else softmax
+  int limit;             // groups that a token may use (<= 0: all)
+  bool renorm;
+  float factor;
+  int32_t* idx;          // [T][k]
+  float* w;              // [T][k]
+  const float* grad_w;   // backward: [T][k]
+  void* grad;            // backward: [T][E], type of the logits
+};
+bool router_limit_ok(const Shape& s, int limit);
+hipError_t launch_router_top_k(const Shape& s, const RouterIO& io, hipStream_t st);
+hipError_t launch_router_top_k_backward(const Shape& s, const RouterIO& io, hipStream_t st);
+
+// ---- dropout (dropout.hip) -------------------------------------------------------
+// out = rd(residual + dropout of x), element by element over [T][H]; residual optional;
+// seed_offset: two device words.
+hipError_t launch_dropout_add(const Shape& s, const void* x, const void* residual, double p,
+                              const uint64_t* seed_offset, void* out, hipStream_t st);
+
+// ---- 4-bit weights (fp4_weights.hip) ----------------------------------------------
+// Packed values and scales of [rows][cols] matrices: fp4_layout.h.
+hipError_t launch_quantize_fp4(int64_t rows, int64_t cols, bool bf16, const void* x, uint8_t* q,
+                               uint8_t* scale, hipStream_t st);
+hipError_t launch_pack_fp4(int64_t rows, int64_t cols, const uint8_t* q_rows,
+                           const uint8_t* scale_rows, uint8_t* q, uint8_t* scale, hipStream_t st);
+hipError_t launch_dequantize_fp4(int64_t rows, int64_t cols, bool bf16, const uint8_t* q,
+                                 const uint8_t* scale, void* x, hipStream_t st);
+
 // ---- weight warm-up (prefetch.hip) -------------------------------------------
 // Reads the first head_bytes (a multiple of 16) of each of `rows` rows of
 // row_bytes so they sit in the caches; writes nothing but, at most, *sink.

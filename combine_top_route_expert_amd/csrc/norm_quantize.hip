@@ -37,35 +37,6 @@ namespace moe {
 
 namespace {
 
-// Sum over the wave: within rows of 16 lanes, then each row's total into the row
-// after it, so that lane 63 ends with all of it.
-__device__ __forceinline__ float wave_sum(float v) {
-  v += __int_as_float(wave_shift<0x111, 0xf>(__float_as_int(v)));
-  v += __int_as_float(wave_shift<0x112, 0xf>(__float_as_int(v)));
-  v += __int_as_float(wave_shift<0x114, 0xf>(__float_as_int(v)));
-  v += __int_as_float(wave_shift<0x118, 0xf>(__float_as_int(v)));
-  v += __int_as_float(wave_shift<0x142, 0xa>(__float_as_int(v)));
-  v += __int_as_float(wave_shift<0x143, 0xc>(__float_as_int(v)));
-  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
-}
-
-__device__ __forceinline__ double wave_sum(double v) {
-  auto add = [&](auto control, auto rows) __attribute__((always_inline)) {
-    constexpr int kControl = decltype(control)::value, kRows = decltype(rows)::value;
-    v += __hiloint2double(wave_shift<kControl, kRows>(__double2hiint(v)),
-                          wave_shift<kControl, kRows>(__double2loint(v)));
-  };
-  const std::integral_constant<int, 0xf> all{};
-  add(std::integral_constant<int, 0x111>{}, all);
-  add(std::integral_constant<int, 0x112>{}, all);
-  add(std::integral_constant<int, 0x114>{}, all);
-  add(std::integral_constant<int, 0x118>{}, all);
-  add(std::integral_constant<int, 0x142>{}, std::integral_constant<int, 0xa>{});
-  add(std::integral_constant<int, 0x143>{}, std::integral_constant<int, 0xc>{});
-  return __hiloint2double(__builtin_amdgcn_readlane(__double2hiint(v), 63),
-                          __builtin_amdgcn_readlane(__double2loint(v), 63));
-}
-
 // Reductions over the THREADS threads of a row; `red` is a slot of THREADS / 64
 // values used by no other reduction that a barrier does not separate.  Every
 // thread gets the same bits.

@@ -19,7 +19,9 @@
  *
  * Around the layer: layer norm of its input rows (moe_layer_norm, its backward
  * and its quantising form) and, for inference, the layer with 8-bit integer
- * experts (moe_quantize_rows, moe_quant_*).
+ * experts (moe_quantize_rows, moe_quant_*); the router that makes its ids and weights
+ * (moe_router_top_k and its backward), dropout behind it (moe_dropout_add), and 4-bit
+ * expert weights (moe_quantize_mx, moe_pack_mx, moe_dequantize_mx).
  *
  * Conventions shared by every entry point
  * ---------------------------------------
@@ -566,6 +568,120 @@ moe_status moe_quant_forward(const moe_shape* shape, const int8_t* hidden_q,
                              const float* w_gate_up_scale, const int8_t* w_down_q,
                              const float* w_down_scale, void* out, int32_t* dev_error, void* ws,
                              size_t ws_bytes, hipStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * The router in front of the layer: what makes top_k_index and top_k_weights, and
+ * takes the grad_top_k_weights of moe_chunked_backward.
+ * --------------------------------------------------------------------------- */
+
+/* Scores of a token's experts from its logits. */
+typedef enum moe_score {
+  MOE_SCORE_SOFTMAX = 0,  /* e^l_e / sum of e^l over all E experts */
+  MOE_SCORE_SIGMOID = 1   /* 1 / (1 + e^-l_e) */
+} moe_score;
+
+/*
+ * Each token's k experts and their weights.
+ *  logits        [T][E] of logits_dtype (a moe_dtype; the layer's does not matter here)
+ *  bias          [E] float32, nullable: added to the scores for the choice only
+ *  score         a moe_score
+ *  group_limit   0: none.  Else a token's experts come from the group_limit groups (of
+ *                shape's num_groups groups of E / G consecutive experts) with the
+ *                largest sum of their two largest keys; num_groups <= 64
+ *                (MOE_ERR_UNSUPPORTED beyond)
+ *  renormalize   nonzero: weights are divided by the sum of the token's chosen scores
+ *  factor        finite: multiplies the weights
+ *  top_k_index   [T][k] int32 (out), top_k_weights [T][k] float32 (out)
+ * The k experts with the largest keys are chosen, the larger key first, equal keys by
+ * the lower id.  The key is the logit; with a bias or a group limit it is score + bias,
+ * evaluated in 64 bits.  A logit of -inf, and a bias that is not finite, close the expert:
+ * it is never chosen, and a slot for which no expert is left has id -1 (the layer drops
+ * it) and weight 0.  A token with a NaN or +inf among its logits has no order: it gets
+ * ids 0, 1, ... and NaN weights, so that its output row is NaN and no other one.
+ * Weights are computed in fp32.  Only T, E, k and num_groups of the shape matter here
+ * (its other fields have to be valid), k may exceed E.
+ */
+moe_status moe_router_top_k(const moe_shape* shape, int32_t logits_dtype, const void* logits,
+                            const float* bias, int32_t score, int32_t group_limit,
+                            int32_t renormalize, float factor, int32_t* top_k_index,
+                            float* top_k_weights, hipStream_t stream);
+
+/*
+ * Gradient of the logits from that of top_k_weights (the choice has none):
+ * grad_logits [T][E] of logits_dtype, every element written.  score, renormalize and
+ * factor as in moe_router_top_k; top_k_index as it left it.  A slot whose id lies outside
+ * [0, E) or whose logit is -inf adds nothing; an id that several slots hold adds for
+ * each.  A token with a NaN or +inf among its logits gets NaN in its own row.
+ */
+moe_status moe_router_top_k_backward(const moe_shape* shape, int32_t logits_dtype,
+                                     const void* logits, const int32_t* top_k_index,
+                                     const float* grad_top_k_weights, int32_t score,
+                                     int32_t renormalize, float factor, void* grad_logits,
+                                     hipStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Dropout of the layer's output on its way into the residual stream.
+ * --------------------------------------------------------------------------- */
+
+/*
+ * out = residual + (kept ? x / (1 - p) : 0) over [T][H] in the shape's dtype, rounded
+ * once; residual nullable (0).  The gradient of x is the same call on the gradient of
+ * out without a residual and with the same seed_offset (that of residual is out's own):
+ * the mask is computed again, never stored.
+ *  p            0 <= p < 1, taken as the multiple of 2^-16 next to it (at most 1 - 2^-16)
+ *  seed_offset  [2] 64-bit words in device memory (8-byte aligned): a seed, and an offset
+ *               that differs for every call that wants a mask of its own.  In device
+ *               memory, so that a captured HIP graph can advance them between replays
+ * Element 8 v + j of the T * H is kept where the 16-bit half j (low halves first) of
+ * Philox 4x32-10's four words for counter (v, offset) and key seed is at least 2^16 p: the
+ * mask depends on nothing else.  A dropped element is 0 whatever x holds there.
+ * out may be x or residual.
+ */
+moe_status moe_dropout_add(const moe_shape* shape, const void* x, const void* residual, double p,
+                           const uint64_t* seed_offset, void* out, hipStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * 4-bit floating point weights with a power of two for each group of 32 values.
+ *
+ * A value is an E2M1 number (0, 0.5, 1, 1.5, 2, 3, 4, 6; code: sign, two exponent bits, a
+ * mantissa bit) times 2^s, s one byte (s + 127; 255 makes the group NaN) for the 32
+ * consecutive columns of a row that share it; 17/32 of a byte a value.  All of them are
+ * exact in bf16 (a product past 2^128 is an infinity).
+ *
+ * Packed matrices [rows][cols], rows % 32 == 0 and cols % 64 == 0, hold
+ *   q      [rows/32][cols/64][64][16 bytes]: entry 32 h + r of block (b, c) holds row 32 b + r,
+ *          columns 64 c + 32 h + 0..31, two to a byte, the even column in the low half
+ *   scale  [rows/32][ceil(cols/256)][64][4 bytes]: byte c % 4 of entry 32 h + r is the one of
+ *          the group that entry 32 h + r of block (b, c) holds
+ * so q has rows * cols / 2 bytes and scale moe_mx_scale_size bytes.
+ * --------------------------------------------------------------------------- */
+
+/* Bytes of a packed matrix's scales.  Host-only. */
+moe_status moe_mx_scale_size(int64_t rows, int64_t cols, size_t* bytes);
+
+/*
+ * Quantises x [rows][cols] of dtype (a moe_dtype) into a packed matrix: s is the least
+ * integer (at least -127) with max|group| <= 6 * 2^s, every value x / 2^s rounded to the nearest E2M1
+ * number, ties to the one with an even code; no value is clipped, but one whose
+ * rounding would reach 2^128 is held at 3 * 2^126.  A group of zeros has scale byte 0; a
+ * group that holds an infinity or a NaN has scale byte 255, so that every product with
+ * its row is NaN.  Experts' w_gate_up is E*2I rows of H, w_down E*H rows of I, each in
+ * one call or expert by expert.  MOE_ERR_UNSUPPORTED where rows % 32 or cols % 64 is not
+ * 0 or rows / 32 * ceil(cols / 256) passes 2^31 - 1.  q, scale and x must not overlap.
+ */
+moe_status moe_quantize_mx(int64_t rows, int64_t cols, int32_t dtype, const void* x, uint8_t* q,
+                            uint8_t* scale, hipStream_t stream);
+
+/* Packs a matrix that is already in 4 bits, row by row: q_rows [rows][cols/2] (even column in
+ * the low half), scale_rows [rows][cols/32].  Limits as for moe_quantize_mx. */
+moe_status moe_pack_mx(int64_t rows, int64_t cols, const uint8_t* q_rows,
+                        const uint8_t* scale_rows, uint8_t* q, uint8_t* scale,
+                        hipStream_t stream);
+
+/* The values of a packed matrix as x [rows][cols] of dtype: exact.  Limits as for
+ * moe_quantize_mx. */
+moe_status moe_dequantize_mx(int64_t rows, int64_t cols, int32_t dtype, const uint8_t* q,
+                              const uint8_t* scale, void* x, hipStream_t stream);
 
 #ifdef __cplusplus
 }
