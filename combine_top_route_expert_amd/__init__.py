@@ -32,6 +32,7 @@ __all__ = [
     "moe_quant_gate_up_gather_pair", "moe_quant_act_pair", "moe_quant_down_pair",
     "moe_quant_workspace_size", "moe_quant_forward", "moe_router_top_k", "moe_router_top_k_backward",
     "moe_dropout_add", "moe_mx_scale_size", "moe_quantize_mx", "moe_pack_mx", "moe_dequantize_mx",
+    "moe_mx_gate_up_gather_pair", "moe_mx_down_pair", "moe_mx_workspace_size", "moe_mx_forward",
 ]
 
 MOE_F32, MOE_BF16 = 0, 1
@@ -52,7 +53,8 @@ EXPORTED_SYMBOLS = (
     "moe_layer_norm_backward", "moe_quantize_rows", "moe_quant_gate_up_gather_pair",
     "moe_quant_act_pair", "moe_quant_down_pair", "moe_quant_workspace_size", "moe_quant_forward",
     "moe_router_top_k", "moe_router_top_k_backward", "moe_dropout_add", "moe_mx_scale_size",
-    "moe_quantize_mx", "moe_pack_mx", "moe_dequantize_mx",
+    "moe_quantize_mx", "moe_pack_mx", "moe_dequantize_mx", "moe_mx_gate_up_gather_pair",
+    "moe_mx_down_pair", "moe_mx_workspace_size", "moe_mx_forward",
 )
 
 
@@ -184,7 +186,13 @@ def load_library() -> ctypes.CDLL:
                                             _P, _P]),
         "moe_pack_mx": (ctypes.c_int, [ctypes.c_int64, ctypes.c_int64, _P, _P, _P, _P, _P]),
         "moe_dequantize_mx": (ctypes.c_int, [ctypes.c_int64, ctypes.c_int64, ctypes.c_int32, _P,
-                                              _P, _P, _P]),
+                                             _P, _P, _P]),
+        "moe_mx_gate_up_gather_pair": (ctypes.c_int, [_SP, ctypes.c_int32, _P, _P, _P, _P, _P, _P,
+                                                      _P]),
+        "moe_mx_down_pair": (ctypes.c_int, [_SP, ctypes.c_int32, _P, _P, _P, _P, _P, _P, _P]),
+        "moe_mx_workspace_size": (ctypes.c_int, [_SP, ctypes.POINTER(ctypes.c_size_t)]),
+        "moe_mx_forward": (ctypes.c_int, [_SP, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P,
+                                          ctypes.c_size_t, _P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -739,7 +747,7 @@ def moe_mx_scale_size(rows: int, cols: int) -> int:
     return b.value
 
 
-def _fp4_matrix(rows: int, cols: int, dtype: str):
+def _mx_matrix(rows: int, cols: int, dtype: str):
     """(torch dtype, moe_dtype, bytes of the values, bytes of the scales) of a packed matrix; sizes
     that the library refuses need no buffer here."""
     if dtype not in ("bf16", "f32"):
@@ -751,7 +759,7 @@ def _fp4_matrix(rows: int, cols: int, dtype: str):
 
 def moe_quantize_mx(rows: int, cols: int, dtype: str, x, q, scale, stream=None) -> None:
     """x ("bf16" or "f32") as a packed 4-bit matrix: q and scale uint8."""
-    dt, code, nq, ns = _fp4_matrix(rows, cols, dtype)
+    dt, code, nq, ns = _mx_matrix(rows, cols, dtype)
     index, ptrs = _pointers((x, dt, rows * cols, "x"), (q, torch.uint8, nq, "q"),
                             (scale, torch.uint8, ns, "scale"))
     _call("moe_quantize_mx", index, stream, rows, cols, code, *ptrs)
@@ -759,7 +767,7 @@ def moe_quantize_mx(rows: int, cols: int, dtype: str, x, q, scale, stream=None) 
 
 def moe_pack_mx(rows: int, cols: int, q_rows, scale_rows, q, scale, stream=None) -> None:
     """A matrix already in 4 bits, row by row, as a packed one."""
-    _, _, nq, ns = _fp4_matrix(rows, cols, "bf16")
+    _, _, nq, ns = _mx_matrix(rows, cols, "bf16")
     u8 = torch.uint8
     index, ptrs = _pointers((q_rows, u8, nq, "q_rows"),
                             (scale_rows, u8, rows * cols // 32, "scale_rows"), (q, u8, nq, "q"),
@@ -769,7 +777,60 @@ def moe_pack_mx(rows: int, cols: int, q_rows, scale_rows, q, scale, stream=None)
 
 def moe_dequantize_mx(rows: int, cols: int, dtype: str, q, scale, x, stream=None) -> None:
     """The values of a packed 4-bit matrix as x ("bf16" or "f32")."""
-    dt, code, nq, ns = _fp4_matrix(rows, cols, dtype)
+    dt, code, nq, ns = _mx_matrix(rows, cols, dtype)
     index, ptrs = _pointers((q, torch.uint8, nq, "q"), (scale, torch.uint8, ns, "scale"),
                             (x, dt, rows * cols, "x"))
     _call("moe_dequantize_mx", index, stream, rows, cols, code, *ptrs)
+
+
+# ---------------------------------------------------------------- 4-bit experts
+def moe_mx_gate_up_gather_pair(shape: moe_shape, chunk: int, hidden_states, src_row, offsets,
+                               w_gate_up_q, w_gate_up_scale, act, stream=None) -> None:
+    rows = sum(_rows_of_pair(shape, chunk))
+    dt, i32, u8 = shape.torch_dtype, torch.int32, torch.uint8
+    T, H, E, I = shape.num_tokens, shape.hidden, shape.num_experts, shape.intermediate  # noqa: E741
+    index, ptrs = _pointers(
+        (hidden_states, dt, T * H, "hidden_states"), (src_row, i32, T * shape.top_k, "src_row"),
+        (offsets, i32, shape.N * (E + 1), "offsets"), (w_gate_up_q, u8, E * I * H, "w_gate_up_q"),
+        (w_gate_up_scale, u8, E * 16 * I * -(-H // 256), "w_gate_up_scale"),
+        (act, dt, rows * I, "act"))
+    _call("moe_mx_gate_up_gather_pair", index, stream, ctypes.byref(shape), chunk, *ptrs)
+
+
+def moe_mx_down_pair(shape: moe_shape, chunk: int, act, offsets, w_down_q, w_down_scale, y0, y1,
+                     stream=None) -> None:
+    rows0, rows1 = _rows_of_pair(shape, chunk)
+    dt, u8 = shape.torch_dtype, torch.uint8
+    H, E, I = shape.hidden, shape.num_experts, shape.intermediate  # noqa: E741
+    index, ptrs = _pointers(
+        (act, dt, (rows0 + rows1) * I, "act"), (offsets, torch.int32, shape.N * (E + 1), "offsets"),
+        (w_down_q, u8, E * H * I // 2, "w_down_q"),
+        (w_down_scale, u8, E * 8 * H * -(-I // 256), "w_down_scale"), (y0, dt, rows0 * H, "y0"),
+        (y1, dt, rows1 * H, "y1"))
+    _call("moe_mx_down_pair", index, stream, ctypes.byref(shape), chunk, *ptrs)
+
+
+def moe_mx_workspace_size(shape: moe_shape) -> int:
+    b = ctypes.c_size_t()
+    _check("moe_mx_workspace_size",
+           load_library().moe_mx_workspace_size(ctypes.byref(shape), ctypes.byref(b)))
+    return b.value
+
+
+def moe_mx_forward(shape: moe_shape, hidden_states, top_k_index, top_k_weights, w_gate_up_q,
+                   w_gate_up_scale, w_down_q, w_down_scale, out, ws, dev_error=None,
+                   stream=None) -> None:
+    """The layer with packed 4-bit expert weights (moe_quantize_mx or moe_pack_mx); bf16 rows."""
+    dt, i32, u8 = shape.torch_dtype, torch.int32, torch.uint8
+    T, H, E, I = shape.num_tokens, shape.hidden, shape.num_experts, shape.intermediate  # noqa: E741
+    A = T * shape.top_k
+    # (the library compares the workspace's size with what it needs)
+    index, ptrs = _pointers(
+        (hidden_states, dt, T * H, "hidden_states"), (top_k_index, i32, A, "top_k_index"),
+        (top_k_weights, torch.float32, A, "top_k_weights"),
+        (w_gate_up_q, u8, E * I * H, "w_gate_up_q"),
+        (w_gate_up_scale, u8, E * 16 * I * -(-H // 256), "w_gate_up_scale"),
+        (w_down_q, u8, E * H * I // 2, "w_down_q"),
+        (w_down_scale, u8, E * 8 * H * -(-I // 256), "w_down_scale"), (out, dt, T * H, "out"),
+        (dev_error, i32, 1, "dev_error", True), (ws, u8, 1, "ws"))
+    _call("moe_mx_forward", index, stream, ctypes.byref(shape), *ptrs, ws.numel())

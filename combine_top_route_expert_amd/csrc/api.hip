@@ -1333,4 +1333,177 @@ moe_status moe_dequantize_mx(int64_t rows, int64_t cols, int32_t dtype, const ui
   return hip_status(launch_dequantize_fp4(rows, cols, dtype == MOE_BF16, q, scale, x, stream));
 }
 
+namespace moe {
+namespace {
+
+// Layout of the moe_mx_forward workspace: the forward's metadata, a [rows][H] y buffer
+// per slot and the pair's joint act rows.
+struct MxPlan {
+  size_t counts, offsets, splits, src_row, dst_row, dev_err, meta_ws;
+  size_t y[2], act;
+  size_t bytes;
+};
+
+MxPlan mx_plan(const Shape& s) {
+  MxPlan p{};
+  size_t o = 0;
+  auto take = [&](size_t n) {
+    size_t at = o;
+    o += align256(n);
+    return at;
+  };
+  p.counts = take((size_t)s.N * s.E * 4);
+  p.offsets = take((size_t)s.N * (s.E + 1) * 4);
+  p.splits = take((size_t)s.N * s.G * 4);
+  p.src_row = take((size_t)s.A * 4);
+  p.dst_row = take((size_t)s.A * 4);
+  p.dev_err = take(4);
+  p.meta_ws = take(meta_plan(s).bytes);
+  const size_t rows = (size_t)s.Tc * s.k;
+  const int nslots = s.N >= 2 ? 2 : 1;
+  for (int i = 0; i < nslots; ++i) p.y[i] = take(rows * s.H * s.elem);
+  p.act = take(nslots * rows * s.I * s.elem);
+  p.bytes = o;
+  return p;
+}
+
+// Checks shared by the 4-bit pair entry points.
+moe_status mx_pair_args(const moe_shape* shape, int32_t chunk, Shape* s, const int32_t* offsets,
+                        const int32_t** off0, const int32_t** off1, int64_t* rows0,
+                        int64_t* rows1) {
+  const moe_status st = resolve_shape(shape, s);
+  if (st != MOE_OK) return st;
+  if (s->dtype != MOE_BF16) return MOE_ERR_UNSUPPORTED;
+  return pair_args(shape, chunk, s, offsets, off0, off1, rows0, rows1);
+}
+
+hipError_t mx_gate_up(const Shape& s, int chunk, const void* hidden, const int32_t* src_row,
+                      const int32_t* off0, const int32_t* off1, int64_t rows, const uint8_t* w,
+                      const uint8_t* w_scale, void* act, hipStream_t st) {
+  int t0, t1, u0 = 0, u1 = 0;
+  chunk_tokens(s, chunk, &t0, &t1);
+  if (chunk + 1 < s.N) chunk_tokens(s, chunk + 1, &u0, &u1);
+  GroupedIO io{};
+  io.off[0] = off0;
+  io.off[1] = off1;
+  io.rows_bound = rows;
+  io.a[0] = hidden;
+  io.gather[0] = src_row + (size_t)t0 * s.k;
+  io.gather[1] = src_row + (size_t)u0 * s.k;
+  io.gather_k = s.k;
+  io.c[0] = act;
+  return launch_gate_up_fp4(s, io, w, w_scale, st);
+}
+
+hipError_t mx_down(const Shape& s, const void* act, const int32_t* off0, const int32_t* off1,
+                   int64_t rows, const uint8_t* w, const uint8_t* w_scale, void* y0, void* y1,
+                   hipStream_t st) {
+  GroupedIO io{};
+  io.off[0] = off0;
+  io.off[1] = off1;
+  io.rows_bound = rows;
+  io.a[0] = act;
+  io.c[0] = y0;
+  io.c[1] = y1;
+  io.c_split = true;
+  return launch_down_fp4(s, io, w, w_scale, st);
+}
+
+}  // namespace
+}  // namespace moe
+
+moe_status moe_mx_gate_up_gather_pair(const moe_shape* shape, int32_t chunk,
+                                      const void* hidden_states, const int32_t* src_row,
+                                      const int32_t* offsets, const uint8_t* w_gate_up_q,
+                                      const uint8_t* w_gate_up_scale, void* act,
+                                      hipStream_t stream) {
+  Shape s;
+  const int32_t *off0 = nullptr, *off1 = nullptr;
+  int64_t rows0 = 0, rows1 = 0;
+  const moe_status st = mx_pair_args(shape, chunk, &s, offsets, &off0, &off1, &rows0, &rows1);
+  if (st != MOE_OK || rows0 + rows1 == 0) return st;
+  if (!buf_ok(hidden_states, 1) || !src_row || !aligned(src_row, 4) || !buf_ok(w_gate_up_q, 1) ||
+      !buf_ok(w_gate_up_scale, 1) || !buf_ok(act, 1))
+    return MOE_ERR_INVALID_ARG;
+  return hip_status(mx_gate_up(s, chunk, hidden_states, src_row, off0, off1, rows0 + rows1,
+                               w_gate_up_q, w_gate_up_scale, act, stream));
+}
+
+moe_status moe_mx_down_pair(const moe_shape* shape, int32_t chunk, const void* act,
+                            const int32_t* offsets, const uint8_t* w_down_q,
+                            const uint8_t* w_down_scale, void* y0, void* y1, hipStream_t stream) {
+  Shape s;
+  const int32_t *off0 = nullptr, *off1 = nullptr;
+  int64_t rows0 = 0, rows1 = 0;
+  const moe_status st = mx_pair_args(shape, chunk, &s, offsets, &off0, &off1, &rows0, &rows1);
+  if (st != MOE_OK || rows0 + rows1 == 0) return st;
+  if (!buf_ok(act, 1) || !buf_ok(w_down_q, 1) || !buf_ok(w_down_scale, 1) || !buf_ok(y0, rows0) ||
+      !buf_ok(y1, rows1))
+    return MOE_ERR_INVALID_ARG;
+  return hip_status(
+      mx_down(s, act, off0, off1, rows0 + rows1, w_down_q, w_down_scale, y0, y1, stream));
+}
+
+moe_status moe_mx_workspace_size(const moe_shape* shape, size_t* bytes) {
+  Shape s;
+  const moe_status st = resolve_shape(shape, &s);
+  if (st != MOE_OK) return st;
+  if (s.dtype != MOE_BF16) return MOE_ERR_UNSUPPORTED;
+  if (!bytes) return MOE_ERR_INVALID_ARG;
+  *bytes = mx_plan(s).bytes;
+  return MOE_OK;
+}
+
+moe_status moe_mx_forward(const moe_shape* shape, const void* hidden_states,
+                          const int32_t* top_k_index, const float* top_k_weights,
+                          const uint8_t* w_gate_up_q, const uint8_t* w_gate_up_scale,
+                          const uint8_t* w_down_q, const uint8_t* w_down_scale, void* out,
+                          int32_t* dev_error, void* ws, size_t ws_bytes, hipStream_t stream) {
+  Shape s;
+  const moe_status st = resolve_shape(shape, &s);
+  if (st != MOE_OK) return st;
+  if (s.dtype != MOE_BF16) return MOE_ERR_UNSUPPORTED;
+  if (!ws || !aligned(ws, 256) || !aligned(dev_error, 4)) return MOE_ERR_INVALID_ARG;
+  const MxPlan p = mx_plan(s);
+  if (ws_bytes < p.bytes) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  if (s.T > 0) {
+    const void* bufs[] = {hidden_states, w_gate_up_q, w_gate_up_scale, w_down_q, w_down_scale, out};
+    for (const void* b : bufs)
+      if (!buf_ok(b, 1)) return MOE_ERR_INVALID_ARG;
+    if (!top_k_index || !top_k_weights || !aligned(top_k_index, 4) || !aligned(top_k_weights, 4))
+      return MOE_ERR_INVALID_ARG;
+  }
+  char* w = (char*)ws;
+  int32_t* offsets = (int32_t*)(w + p.offsets);
+  int32_t* src_row = (int32_t*)(w + p.src_row);
+  int32_t* dst_row = (int32_t*)(w + p.dst_row);
+  int32_t* err = dev_error ? dev_error : (int32_t*)(w + p.dev_err);
+  void* act = w + p.act;
+  hipError_t he = launch_route_meta(s, top_k_index, (int32_t*)(w + p.counts), offsets,
+                                    (int32_t*)(w + p.splits), src_row, dst_row, err,
+                                    w + p.meta_ws, stream);
+  // pairs of chunks as in the pair-fused forward: each expert's weights are
+  // streamed once per pair
+  for (int c = 0; he == hipSuccess && c < s.N; c += 2) {
+    int t0, t1, u0 = 0, u1 = 0;
+    chunk_tokens(s, c, &t0, &t1);
+    if (c + 1 < s.N) chunk_tokens(s, c + 1, &u0, &u1);
+    const int64_t rows0 = (int64_t)(t1 - t0) * s.k, rows1 = (int64_t)(u1 - u0) * s.k;
+    const int64_t rows = rows0 + rows1;
+    if (rows == 0) continue;  // empty tail pair
+    const int32_t* off0 = offsets + (size_t)c * (s.E + 1);
+    const int32_t* off1 = rows1 > 0 ? off0 + (s.E + 1) : nullptr;
+    void *y0 = w + p.y[0], *y1 = rows1 > 0 ? w + p.y[1] : nullptr;
+    he = mx_gate_up(s, c, hidden_states, src_row, off0, off1, rows, w_gate_up_q, w_gate_up_scale,
+                    act, stream);
+    if (he == hipSuccess)
+      he = mx_down(s, act, off0, off1, rows, w_down_q, w_down_scale, y0, y1, stream);
+    if (he == hipSuccess)
+      he = rows1 > 0 ? launch_combine_pair(s, t0, u0, u1, y0, y1, dst_row, top_k_weights, out,
+                                           stream)
+                     : launch_combine(s, t0, t1, y0, dst_row, top_k_weights, out, stream);
+  }
+  return hip_status(he);
+}
+
 }  // extern "C"

@@ -1,4 +1,5 @@
-// Tile machinery of the grouped expert GEMMs (gemm_bf16.hip, gemm_i8.hip): the
+// Tile machinery of the grouped expert GEMMs (gemm_bf16.hip, gemm_i8.hip; gemm_fp4.hip
+// has its own loop and shares the rows, the waits and the bf16 epilogue): the
 // copies of A and B stages into LDS and the K loops around the matrix
 // instruction.  Both kernels move K in stages of 128 bytes of a row (64 bf16 or
 // 128 int8 values) and feed 16 bytes of a row per lane to a 32 x 32 matrix
@@ -559,6 +560,104 @@ __device__ __forceinline__ void k_loop_small(typename Loader::Mma::acc (&acc)[FM
     stage_mma<F, SB, Loader>(acc, sa + row0 * ROWB,
                              sa + Loader::template small_a<SROWS>() + wn * WN * ROWB, lane);
     __builtin_amdgcn_s_waitcnt(kWaitLgkm0);
+  }
+}
+
+// Arguments and epilogue of the products with bf16 output.
+struct GemmArgs : TileArgs {
+  uint16_t* C[2];             // [rows][ncols] bf16 (C[1]: chunk-1 rows when c_split)
+  uint16_t* gu;               // gate_up, optional: g and u of each row, joint [rows][2I]
+};
+
+__device__ __forceinline__ uint16_t to_bf16_bits(float f) {
+  return __builtin_bit_cast(uint16_t, (__bf16)f);
+}
+
+// Epilogue through LDS.  The K loops pass the weight fragment as the MFMA's
+// first operand and the row fragment as its second, so each 32x32 block holds
+// C transposed: lane l holds row l % 32 of columns 8*(q/4) + 4*(l/32) + q%4,
+// q = 0..15 (the products and their order over K are those of the other
+// operand order: same bits).  A lane's four consecutive columns of a row go to
+// LDS as one 8-byte write (with the rows in each lane's columns, one 2-byte
+// write per element had taken four times the LDS writes and twice the
+// conversions: down GEMM 2-2.5% slower).  Every wave writes its nblk 32-row
+// blocks from row row0 (after SwiGLU for gate_up) as bf16 into a row-major C
+// tile in the freed stage buffers, then the workgroup stores the tile 16 bytes
+// per lane, one row segment at a time.  PLANES = 3 (gate_up in the backward's
+// recompute) also saves g and u into the joint [rows][2I] copy: one plane per
+// pass.
+template <bool kGateUp, int PLANES, int FM, int FN, int BM, int BN, int WM, int WN, int NT>
+__device__ __forceinline__ void store_tile_lds(const GemmArgs& a, const f32x16 (&acc)[FM][FN],
+                                               const TileRows& tr, int nt, int row0, int nblk,
+                                               int wn, int lane, char* smem) {
+  constexpr int CT = kGateUp ? BN / 2 : BN;  // tile columns of C
+  constexpr int CPR = CT / 8;                // 16-byte chunks per tile row
+  static_assert(CPR >= 8, "chunk swizzle needs 8 chunks per row");
+  static_assert(PLANES == 1 || kGateUp, "g and u exist for gate_up only");
+  // chunk ch of row r at slot ch ^ (r mod CPR): the 32 rows of one 8-byte
+  // write (a row per lane, lanes l and l + 32 the two halves of one chunk)
+  // fall in distinct slots
+  auto lds_at = [](int r, int c) {
+    return r * (CT * 2) + (((c >> 3) ^ (r & (CPR - 1))) << 4) + (c & 7) * 2;
+  };
+  typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+  const int rl = row0 + (lane & 31), cq = 4 * (lane >> 5);
+  const int col0 = nt * CT;
+  const uint16_t* const cbase[2] = {a.C[0], a.C[1]};
+#pragma unroll
+  for (int plane = 0; plane < PLANES; ++plane) {
+    if (plane > 0) __syncthreads();  // the previous plane's reads are done
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+      // blocks past the wave's band or the tile's rows: never stored
+      if (i >= nblk || row0 + i * 32 >= tr.rows) break;
+      const int r = rl + i * 32;
+#pragma unroll
+      for (int g4 = 0; g4 < 4; ++g4) {
+        if constexpr (kGateUp) {
+#pragma unroll
+          for (int j = 0; j < FN / 2; ++j) {
+            const int c = wn * (WN / 2) + j * 32 + 8 * g4 + cq;
+            float v[4];
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+              const float g = acc[i][j][4 * g4 + t], u = acc[i][j + FN / 2][4 * g4 + t];
+              v[t] = plane == 0 ? swiglu<true>(g, u) : plane == 1 ? g : u;
+            }
+            *(bf16x4*)(smem + lds_at(r, c)) =
+                bf16x4{(__bf16)v[0], (__bf16)v[1], (__bf16)v[2], (__bf16)v[3]};
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < FN; ++j) {
+            const int c = wn * WN + j * 32 + 8 * g4 + cq;
+            const f32x16& x = acc[i][j];
+            *(bf16x4*)(smem + lds_at(r, c)) =
+                bf16x4{(__bf16)x[4 * g4], (__bf16)x[4 * g4 + 1], (__bf16)x[4 * g4 + 2],
+                       (__bf16)x[4 * g4 + 3]};
+          }
+        }
+      }
+    }
+    __syncthreads();
+    for (int ch = threadIdx.x; ch < BM * CPR; ch += NT) {
+      const int r = ch / CPR, c = (ch % CPR) * 8;
+      if (r >= tr.rows || col0 + c >= a.ncols) continue;
+      typedef uint32_t u32x4v __attribute__((ext_vector_type(4)));
+      const u32x4v v = *(const u32x4v*)(smem + lds_at(r, c));
+      uint16_t* dst;
+      if (plane == 0)
+        dst = (uint16_t*)row_ptr(cbase, a.c_split, tr, tr.v0 + r, a.ncols);
+      else  // g (plane 1) or u (plane 2) of the joint [rows][2I] copy
+        dst = a.gu + (int64_t)tr.joint_row(tr.v0 + r) * (2 * a.I) + (plane - 1) * a.I;
+      // each output row is written once and read by the next launch: streamed
+      // non-temporally in the forward (act, y); the backward's recompute keeps
+      // plain stores for the g and u planes it reads back
+      if constexpr (PLANES == 1)
+        __builtin_nontemporal_store(v, (u32x4v*)(dst + col0 + c));
+      else
+        *(u32x4v*)(dst + col0 + c) = v;
+    }
   }
 }
 

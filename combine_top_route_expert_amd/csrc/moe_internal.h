@@ -46,11 +46,17 @@ __device__ __forceinline__ void buffer_load_lds16_nt(rsrc_t r, char* dst, uint32
   __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)dst, 16,
                                            off, soff, 0, 2);
 }
+// 4 bytes a lane, at dst + 4 l.
+__device__ __forceinline__ void buffer_load_lds4(rsrc_t r, char* dst, uint32_t off, int soff) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)dst, 4,
+                                           off, soff, 0, 0);
+}
 #else
 struct rsrc_t {};
 __device__ __forceinline__ rsrc_t raw_rsrc(const void*) { return {}; }
 __device__ __forceinline__ void buffer_load_lds16(rsrc_t, char*, uint32_t, int) {}
 __device__ __forceinline__ void buffer_load_lds16_nt(rsrc_t, char*, uint32_t, int) {}
+__device__ __forceinline__ void buffer_load_lds4(rsrc_t, char*, uint32_t, int) {}
 #endif
 
 // Host: whether rows of ld 2-byte elements in the buffers at p0 and p1 (at
@@ -239,6 +245,13 @@ hipError_t launch_gate_up_i8(const Shape& s, const GroupedIO& io, const float* a
                              const void* w_gate_up, const float* w_scale, hipStream_t st);
 hipError_t launch_down_i8(const Shape& s, const GroupedIO& io, const float* a_scale,
                           const void* w_down, const float* w_scale, hipStream_t st);
+
+// Products with packed 4-bit weights (gemm_fp4.hip): bf16 rows and results; gate_up gathers
+// its rows, down reads joint ones.
+hipError_t launch_gate_up_fp4(const Shape& s, const GroupedIO& io, const uint8_t* w_gate_up,
+                              const uint8_t* w_scale, hipStream_t st);
+hipError_t launch_down_fp4(const Shape& s, const GroupedIO& io, const uint8_t* w_down,
+                           const uint8_t* w_scale, hipStream_t st);
 
 // The whole 8-bit layer for a few assignments (few_rows_i8.hip): nothing is sorted,
 // act [T*k][I] holds row f for assignment f; also counts the dropped ids.

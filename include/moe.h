@@ -21,7 +21,8 @@
  * and its quantising form) and, for inference, the layer with 8-bit integer
  * experts (moe_quantize_rows, moe_quant_*); the router that makes its ids and weights
  * (moe_router_top_k and its backward), dropout behind it (moe_dropout_add), and 4-bit
- * expert weights (moe_quantize_mx, moe_pack_mx, moe_dequantize_mx).
+ * expert weights (moe_quantize_mx, moe_pack_mx, moe_dequantize_mx) with the layer that
+ * multiplies with them (moe_mx_*).
  *
  * Conventions shared by every entry point
  * ---------------------------------------
@@ -682,6 +683,48 @@ moe_status moe_pack_mx(int64_t rows, int64_t cols, const uint8_t* q_rows,
  * moe_quantize_mx. */
 moe_status moe_dequantize_mx(int64_t rows, int64_t cols, int32_t dtype, const uint8_t* q,
                               const uint8_t* scale, void* x, hipStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * The layer with 4-bit experts (inference; there is no backward).
+ *
+ * Rows, act, y and out are bf16 (MOE_F32 is MOE_ERR_UNSUPPORTED), weights packed
+ * matrices as above, expert after expert: w_gate_up_q and its scales E matrices of
+ * [2I][H], w_down_q and its scales E of [H][I].  Products are those of the bf16 layer with
+ * the weights written out in bf16: fp32 sums; act, y and out rounded once each.  Rows,
+ * offsets, src_row, pairs and dropped ids are those of the calls above, and results do not depend
+ * on N.  moe_mx_forward gives the bits of its steps, except for a few assignments (T * k <= 64),
+ * which it sums in another order (the same within rounding).
+ * Limits: H % 64 == 0 and I % 64 == 0.
+ * --------------------------------------------------------------------------- */
+
+/* First expert product with the SwiGLU epilogue: moe_expert_gate_up_gather_pair with
+ * packed 4-bit weights. */
+moe_status moe_mx_gate_up_gather_pair(const moe_shape* shape, int32_t chunk,
+                                      const void* hidden_states, const int32_t* src_row,
+                                      const int32_t* offsets, const uint8_t* w_gate_up_q,
+                                      const uint8_t* w_gate_up_scale, void* act,
+                                      hipStream_t stream);
+
+/* Second expert product: moe_expert_down_pair with packed 4-bit weights. */
+moe_status moe_mx_down_pair(const moe_shape* shape, int32_t chunk, const void* act,
+                            const int32_t* offsets, const uint8_t* w_down_q,
+                            const uint8_t* w_down_scale, void* y0, void* y1, hipStream_t stream);
+
+/* Bytes of workspace moe_mx_forward needs: the metadata plus min(N,2) slots of
+ * ceil(T/N)*k rows of (H + I) elements.  Host-only. */
+moe_status moe_mx_workspace_size(const moe_shape* shape, size_t* bytes);
+
+/*
+ * The whole layer: metadata once, then per chunk pair gate_up, down and the weighted
+ * combine, all on `stream`; capturable in a HIP graph.  dev_error as for moe_chunked_forward
+ * (nullable); ws must hold moe_mx_workspace_size bytes and not be shared by calls, or by
+ * graphs that hold them, that may overlap.
+ */
+moe_status moe_mx_forward(const moe_shape* shape, const void* hidden_states,
+                          const int32_t* top_k_index, const float* top_k_weights,
+                          const uint8_t* w_gate_up_q, const uint8_t* w_gate_up_scale,
+                          const uint8_t* w_down_q, const uint8_t* w_down_scale, void* out,
+                          int32_t* dev_error, void* ws, size_t ws_bytes, hipStream_t stream);
 
 #ifdef __cplusplus
 }
