@@ -32,7 +32,7 @@ __all__ = [
     "moe_quant_gate_up_gather_pair", "moe_quant_act_pair", "moe_quant_down_pair",
     "moe_quant_workspace_size", "moe_quant_forward", "moe_router_top_k", "moe_router_top_k_backward",
     "moe_dropout_add", "moe_mx_scale_size", "moe_quantize_mx", "moe_pack_mx", "moe_dequantize_mx",
-    "moe_mx_gate_up_gather_pair", "moe_mx_down_pair", "moe_mx_workspace_size", "moe_mx_forward",
+    "moe_mx_workspace_size", "moe_mx_forward",
 ]
 
 MOE_F32, MOE_BF16 = 0, 1
@@ -53,8 +53,8 @@ EXPORTED_SYMBOLS = (
     "moe_layer_norm_backward", "moe_quantize_rows", "moe_quant_gate_up_gather_pair",
     "moe_quant_act_pair", "moe_quant_down_pair", "moe_quant_workspace_size", "moe_quant_forward",
     "moe_router_top_k", "moe_router_top_k_backward", "moe_dropout_add", "moe_mx_scale_size",
-    "moe_quantize_mx", "moe_pack_mx", "moe_dequantize_mx", "moe_mx_gate_up_gather_pair",
-    "moe_mx_down_pair", "moe_mx_workspace_size", "moe_mx_forward",
+    "moe_quantize_mx", "moe_pack_mx", "moe_dequantize_mx", "moe_mx_workspace_size",
+    "moe_mx_forward",
 )
 
 
@@ -187,9 +187,6 @@ def load_library() -> ctypes.CDLL:
         "moe_pack_mx": (ctypes.c_int, [ctypes.c_int64, ctypes.c_int64, _P, _P, _P, _P, _P]),
         "moe_dequantize_mx": (ctypes.c_int, [ctypes.c_int64, ctypes.c_int64, ctypes.c_int32, _P,
                                              _P, _P, _P]),
-        "moe_mx_gate_up_gather_pair": (ctypes.c_int, [_SP, ctypes.c_int32, _P, _P, _P, _P, _P, _P,
-                                                      _P]),
-        "moe_mx_down_pair": (ctypes.c_int, [_SP, ctypes.c_int32, _P, _P, _P, _P, _P, _P, _P]),
         "moe_mx_workspace_size": (ctypes.c_int, [_SP, ctypes.POINTER(ctypes.c_size_t)]),
         "moe_mx_forward": (ctypes.c_int, [_SP, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P,
                                           ctypes.c_size_t, _P]),
@@ -784,32 +781,6 @@ def moe_dequantize_mx(rows: int, cols: int, dtype: str, q, scale, x, stream=None
 
 
 # ---------------------------------------------------------------- 4-bit experts
-def moe_mx_gate_up_gather_pair(shape: moe_shape, chunk: int, hidden_states, src_row, offsets,
-                               w_gate_up_q, w_gate_up_scale, act, stream=None) -> None:
-    rows = sum(_rows_of_pair(shape, chunk))
-    dt, i32, u8 = shape.torch_dtype, torch.int32, torch.uint8
-    T, H, E, I = shape.num_tokens, shape.hidden, shape.num_experts, shape.intermediate  # noqa: E741
-    index, ptrs = _pointers(
-        (hidden_states, dt, T * H, "hidden_states"), (src_row, i32, T * shape.top_k, "src_row"),
-        (offsets, i32, shape.N * (E + 1), "offsets"), (w_gate_up_q, u8, E * I * H, "w_gate_up_q"),
-        (w_gate_up_scale, u8, E * 16 * I * -(-H // 256), "w_gate_up_scale"),
-        (act, dt, rows * I, "act"))
-    _call("moe_mx_gate_up_gather_pair", index, stream, ctypes.byref(shape), chunk, *ptrs)
-
-
-def moe_mx_down_pair(shape: moe_shape, chunk: int, act, offsets, w_down_q, w_down_scale, y0, y1,
-                     stream=None) -> None:
-    rows0, rows1 = _rows_of_pair(shape, chunk)
-    dt, u8 = shape.torch_dtype, torch.uint8
-    H, E, I = shape.hidden, shape.num_experts, shape.intermediate  # noqa: E741
-    index, ptrs = _pointers(
-        (act, dt, (rows0 + rows1) * I, "act"), (offsets, torch.int32, shape.N * (E + 1), "offsets"),
-        (w_down_q, u8, E * H * I // 2, "w_down_q"),
-        (w_down_scale, u8, E * 8 * H * -(-I // 256), "w_down_scale"), (y0, dt, rows0 * H, "y0"),
-        (y1, dt, rows1 * H, "y1"))
-    _call("moe_mx_down_pair", index, stream, ctypes.byref(shape), chunk, *ptrs)
-
-
 def moe_mx_workspace_size(shape: moe_shape) -> int:
     b = ctypes.c_size_t()
     _check("moe_mx_workspace_size",

@@ -7,6 +7,7 @@
 
 #include "fp4_layout.h"
 #include "moe_internal.h"
+#include "mx_rows.h"
 
 namespace moe {
 
@@ -1336,11 +1337,12 @@ moe_status moe_dequantize_mx(int64_t rows, int64_t cols, int32_t dtype, const ui
 namespace moe {
 namespace {
 
-// Layout of the moe_mx_forward workspace: the forward's metadata, a [rows][H] y buffer
-// per slot and the pair's joint act rows.
+// Layout of the moe_mx_forward workspace: the forward's metadata, the pair's input and act
+// rows, sorted by expert, in two 6-bit parts and the output rows of each slot in scaled
+// fp16.
 struct MxPlan {
   size_t counts, offsets, splits, src_row, dst_row, dev_err, meta_ws;
-  size_t y[2], act;
+  size_t x, x_scale, act, act_scale, y[2], y_scale[2];
   size_t bytes;
 };
 
@@ -1361,88 +1363,21 @@ MxPlan mx_plan(const Shape& s) {
   p.meta_ws = take(meta_plan(s).bytes);
   const size_t rows = (size_t)s.Tc * s.k;
   const int nslots = s.N >= 2 ? 2 : 1;
-  for (int i = 0; i < nslots; ++i) p.y[i] = take(rows * s.H * s.elem);
-  p.act = take(nslots * rows * s.I * s.elem);
+  const int64_t blocks = mx_row_blocks(nslots * (int64_t)rows, s.E);
+  p.x = take(mx_value_bytes(blocks, s.H));
+  p.x_scale = take(mx_scale_bytes(blocks, s.H));
+  p.act = take(mx_value_bytes(blocks, s.I));
+  p.act_scale = take(mx_scale_bytes(blocks, s.I));
+  for (int i = 0; i < nslots; ++i) {
+    p.y[i] = take(rows * s.H * 2);
+    p.y_scale[i] = take(rows * mx_out_scales(s.H));
+  }
   p.bytes = o;
   return p;
 }
 
-// Checks shared by the 4-bit pair entry points.
-moe_status mx_pair_args(const moe_shape* shape, int32_t chunk, Shape* s, const int32_t* offsets,
-                        const int32_t** off0, const int32_t** off1, int64_t* rows0,
-                        int64_t* rows1) {
-  const moe_status st = resolve_shape(shape, s);
-  if (st != MOE_OK) return st;
-  if (s->dtype != MOE_BF16) return MOE_ERR_UNSUPPORTED;
-  return pair_args(shape, chunk, s, offsets, off0, off1, rows0, rows1);
-}
-
-hipError_t mx_gate_up(const Shape& s, int chunk, const void* hidden, const int32_t* src_row,
-                      const int32_t* off0, const int32_t* off1, int64_t rows, const uint8_t* w,
-                      const uint8_t* w_scale, void* act, hipStream_t st) {
-  int t0, t1, u0 = 0, u1 = 0;
-  chunk_tokens(s, chunk, &t0, &t1);
-  if (chunk + 1 < s.N) chunk_tokens(s, chunk + 1, &u0, &u1);
-  GroupedIO io{};
-  io.off[0] = off0;
-  io.off[1] = off1;
-  io.rows_bound = rows;
-  io.a[0] = hidden;
-  io.gather[0] = src_row + (size_t)t0 * s.k;
-  io.gather[1] = src_row + (size_t)u0 * s.k;
-  io.gather_k = s.k;
-  io.c[0] = act;
-  return launch_gate_up_fp4(s, io, w, w_scale, st);
-}
-
-hipError_t mx_down(const Shape& s, const void* act, const int32_t* off0, const int32_t* off1,
-                   int64_t rows, const uint8_t* w, const uint8_t* w_scale, void* y0, void* y1,
-                   hipStream_t st) {
-  GroupedIO io{};
-  io.off[0] = off0;
-  io.off[1] = off1;
-  io.rows_bound = rows;
-  io.a[0] = act;
-  io.c[0] = y0;
-  io.c[1] = y1;
-  io.c_split = true;
-  return launch_down_fp4(s, io, w, w_scale, st);
-}
-
 }  // namespace
 }  // namespace moe
-
-moe_status moe_mx_gate_up_gather_pair(const moe_shape* shape, int32_t chunk,
-                                      const void* hidden_states, const int32_t* src_row,
-                                      const int32_t* offsets, const uint8_t* w_gate_up_q,
-                                      const uint8_t* w_gate_up_scale, void* act,
-                                      hipStream_t stream) {
-  Shape s;
-  const int32_t *off0 = nullptr, *off1 = nullptr;
-  int64_t rows0 = 0, rows1 = 0;
-  const moe_status st = mx_pair_args(shape, chunk, &s, offsets, &off0, &off1, &rows0, &rows1);
-  if (st != MOE_OK || rows0 + rows1 == 0) return st;
-  if (!buf_ok(hidden_states, 1) || !src_row || !aligned(src_row, 4) || !buf_ok(w_gate_up_q, 1) ||
-      !buf_ok(w_gate_up_scale, 1) || !buf_ok(act, 1))
-    return MOE_ERR_INVALID_ARG;
-  return hip_status(mx_gate_up(s, chunk, hidden_states, src_row, off0, off1, rows0 + rows1,
-                               w_gate_up_q, w_gate_up_scale, act, stream));
-}
-
-moe_status moe_mx_down_pair(const moe_shape* shape, int32_t chunk, const void* act,
-                            const int32_t* offsets, const uint8_t* w_down_q,
-                            const uint8_t* w_down_scale, void* y0, void* y1, hipStream_t stream) {
-  Shape s;
-  const int32_t *off0 = nullptr, *off1 = nullptr;
-  int64_t rows0 = 0, rows1 = 0;
-  const moe_status st = mx_pair_args(shape, chunk, &s, offsets, &off0, &off1, &rows0, &rows1);
-  if (st != MOE_OK || rows0 + rows1 == 0) return st;
-  if (!buf_ok(act, 1) || !buf_ok(w_down_q, 1) || !buf_ok(w_down_scale, 1) || !buf_ok(y0, rows0) ||
-      !buf_ok(y1, rows1))
-    return MOE_ERR_INVALID_ARG;
-  return hip_status(
-      mx_down(s, act, off0, off1, rows0 + rows1, w_down_q, w_down_scale, y0, y1, stream));
-}
 
 moe_status moe_mx_workspace_size(const moe_shape* shape, size_t* bytes) {
   Shape s;
@@ -1478,7 +1413,8 @@ moe_status moe_mx_forward(const moe_shape* shape, const void* hidden_states,
   int32_t* src_row = (int32_t*)(w + p.src_row);
   int32_t* dst_row = (int32_t*)(w + p.dst_row);
   int32_t* err = dev_error ? dev_error : (int32_t*)(w + p.dev_err);
-  void* act = w + p.act;
+  const MxRows x{w + p.x, w + p.x_scale}, act{w + p.act, w + p.act_scale};
+  const MxRows y[2] = {{w + p.y[0], w + p.y_scale[0]}, {w + p.y[1], w + p.y_scale[1]}};
   hipError_t he = launch_route_meta(s, top_k_index, (int32_t*)(w + p.counts), offsets,
                                     (int32_t*)(w + p.splits), src_row, dst_row, err,
                                     w + p.meta_ws, stream);
@@ -1489,19 +1425,24 @@ moe_status moe_mx_forward(const moe_shape* shape, const void* hidden_states,
     chunk_tokens(s, c, &t0, &t1);
     if (c + 1 < s.N) chunk_tokens(s, c + 1, &u0, &u1);
     const int64_t rows0 = (int64_t)(t1 - t0) * s.k, rows1 = (int64_t)(u1 - u0) * s.k;
-    const int64_t rows = rows0 + rows1;
-    if (rows == 0) continue;  // empty tail pair
-    const int32_t* off0 = offsets + (size_t)c * (s.E + 1);
-    const int32_t* off1 = rows1 > 0 ? off0 + (s.E + 1) : nullptr;
-    void *y0 = w + p.y[0], *y1 = rows1 > 0 ? w + p.y[1] : nullptr;
-    he = mx_gate_up(s, c, hidden_states, src_row, off0, off1, rows, w_gate_up_q, w_gate_up_scale,
-                    act, stream);
+    if (rows0 + rows1 == 0) continue;  // empty tail pair
+    MxIO io{};
+    io.off[0] = offsets + (size_t)c * (s.E + 1);
+    io.off[1] = rows1 > 0 ? io.off[0] + (s.E + 1) : nullptr;
+    io.rows_bound = rows0 + rows1;
+    io.gather[0] = src_row + (size_t)t0 * s.k;
+    io.gather[1] = src_row + (size_t)u0 * s.k;
+    he = launch_split_rows(s, io, hidden_states, x, stream);
+    io.w = w_gate_up_q;
+    io.w_scale = w_gate_up_scale;
+    if (he == hipSuccess) he = launch_gate_up_mx(s, io, x, act, stream);
+    io.w = w_down_q;
+    io.w_scale = w_down_scale;
+    if (he == hipSuccess) he = launch_down_mx(s, io, act, y, stream);
     if (he == hipSuccess)
-      he = mx_down(s, act, off0, off1, rows, w_down_q, w_down_scale, y0, y1, stream);
-    if (he == hipSuccess)
-      he = rows1 > 0 ? launch_combine_pair(s, t0, u0, u1, y0, y1, dst_row, top_k_weights, out,
-                                           stream)
-                     : launch_combine(s, t0, t1, y0, dst_row, top_k_weights, out, stream);
+      he = rows1 > 0
+               ? launch_combine_scaled(s, t0, u0, u1, y, dst_row, top_k_weights, out, stream)
+               : launch_combine_scaled(s, t0, t1, t1, y, dst_row, top_k_weights, out, stream);
   }
   return hip_status(he);
 }

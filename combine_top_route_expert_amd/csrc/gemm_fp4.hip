@@ -1,355 +1,565 @@
-// Grouped expert GEMMs with bf16 rows and packed 4-bit weights (fp4_layout.h):
-//   gate_up: act[r][i] = silu(g) u,  g, u = x_r . W[e][i], x_r . W[e][I + i]
-//   down   : y[r][n]   = act_r . W[e][n]
-// A weight is an E2M1 number times a power of two, which bf16 holds exactly, so the
-// products are those of the bf16 GEMMs with the weights written out: bf16 matrix
-// instructions, fp32 sums over K in ascending order whatever the tile (the same bits
-// from every variant), one rounding of the result.
+// Grouped expert products with packed 4-bit weights (fp4_layout.h) and rows in two 6-bit
+// parts (mx_rows.h):
+//   gate_up: act[r] = silu(g) u in two parts,  g, u = x_r . W[e][i], x_r . W[e][I + i]
+//   down   : y[r][n] = act_r . W[e][n] in scaled fp16
 //
-// The weights stay in 4 bits until they are operands: a stage of 64 columns is copied
-// to LDS as it lies in memory, a kilobyte for 32 weight rows, and a wave reads 16 bytes a
-// lane of it and converts them (v_cvt_scalef32_pk_bf16_fp4: two values and their power
-// of two in one instruction) right before the four matrix instructions that they feed.
-// Lane 32 h + r holds columns 32 h .. 32 h + 31 of row r, so instruction kk multiplies
-// columns 8 kk .. 8 kk + 7 of both halves; the fragments of the activations are read to
-// match.  The powers of two of four stages lie in a dword a lane, copied to LDS with
-// every fourth stage.
+// v_mfma_scale_f32_32x32x64_f8f6f4 multiplies 32 x 64 E2M1 weights by 32 x 64 E2M3 values
+// with a power of two for each 32 of either side, in the 32 cycles in which the bf16
+// instruction multiplies a quarter of that; the two parts of the rows make it half the
+// matrix time of bf16.  Weights go from memory to the instruction as they lie: lane
+// 32 h + r holds the 16 bytes of columns 32 h .. of row r and a dword with its scales of
+// four blocks, of which the instruction picks a byte.  (Converted to bf16 in registers
+// instead, with bf16 rows and instructions: 2.05 ms for gate_up of 4096 tokens on 256
+// experts, H = 7168, I = 2048; 64 tokens 0.65 ms, 0.1 of it the conversions.)  Sums are
+// fp32, over K in ascending order, part h before part l in each 64 columns, whatever the
+// tile: every variant gives the same bits.
 #include <algorithm>
 #include <type_traits>
 
 #include "fp4_layout.h"
 #include "gemm_tile.h"
+#include "mx_rows.h"
 
 namespace moe {
 
 namespace {
 
-struct Fp4Args : GemmArgs {
-  const char* scale;            // packed scales of B
-  int64_t scale_expert_bytes;   // per expert
-  int blocks;                   // 64-column blocks of a row: K / 64
-  int quads;                    // scale dwords of a row
+typedef int i32x12 __attribute__((ext_vector_type(12)));
+
+struct MxArgs {
+  MxRows a;                   // rows of A
+  const int32_t *off0, *off1; // E + 1 offsets of the chunk(s); off1 may be null
+  const char *b, *bs;         // packed weights and scales, expert after expert
+  int64_t b_expert, bs_expert;
+  int E, ncols, n_tiles;      // columns of C, column tiles
+  int blocks, quads;          // 64-column blocks of K, scale dwords of a weight row
+  int up;                     // gate_up: row blocks from a gate row to its up row
+  MxRows c;                   // gate_up: act
+  MxRows y[2];                // down: the two chunks' rows
+  int c_split;
 };
 
-constexpr int kScaleUnits = 4;   // dwords of scales kept in LDS for a weight row
-constexpr int kMaxStages = 12;   // stages that span at most that many units
+// One product of 64 columns: weights w (16 bytes a lane) and a part of the rows (the first
+// or the last 24 of a lane's 48 bytes), each with a scale byte of a dword.
+template <int kPart>
+__device__ __forceinline__ f32x16 mx_mma(const i32x4& w, uint32_t ws, const i32x12& a, uint32_t as,
+                                         const f32x16& c) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  typedef int i32x8 __attribute__((ext_vector_type(8)));
+  const i32x8 wv = __builtin_shufflevector(w, w, 0, 1, 2, 3, -1, -1, -1, -1);
+  i32x8 av;
+  if constexpr (kPart == 0)
+    av = __builtin_shufflevector(a, a, 0, 1, 2, 3, 4, 5, -1, -1);
+  else
+    av = __builtin_shufflevector(a, a, 6, 7, 8, 9, 10, 11, -1, -1);
+  // (4: E2M1, 2: E2M3; byte 0 of the weights' scales, byte kPart of the rows')
+  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(wv, av, c, 4, 2, 0, (int)ws, kPart,
+                                                         (int)as);
+#else
+  return c;
+#endif
+}
 
 template <bool kBuf>
-struct Source {  // rows or blocks to copy from: a descriptor with offsets, or addresses
+struct Source {  // what to copy from: a descriptor with offsets, or addresses
   rsrc_t desc;
   const char* base;
   __device__ __forceinline__ void init(const char* p) {
     base = p;
     if constexpr (kBuf) desc = raw_rsrc(p);
   }
+  typedef std::conditional_t<kBuf, uint32_t, int64_t> offset;
   template <bool kNt>
-  __device__ __forceinline__ void load16(char* dst, int64_t off, int koff) const {
+  __device__ __forceinline__ void load16(char* dst, offset off, int koff) const {
     if constexpr (kBuf) {
       if constexpr (kNt)
-        buffer_load_lds16_nt(desc, dst, (uint32_t)off, koff);
+        buffer_load_lds16_nt(desc, dst, off, koff);
       else
-        buffer_load_lds16(desc, dst, (uint32_t)off, koff);
+        buffer_load_lds16(desc, dst, off, koff);
     } else {
       __builtin_amdgcn_global_load_lds((const void*)(base + off + koff), (lds_void*)dst, 16, 0,
                                        kNt ? 2 : 0);
     }
   }
-  __device__ __forceinline__ void load4(char* dst, int64_t off, int koff) const {
+  __device__ __forceinline__ void load4(char* dst, offset off, int koff) const {
     if constexpr (kBuf)
-      buffer_load_lds4(desc, dst, (uint32_t)off, koff);
+      buffer_load_lds4(desc, dst, off, koff);
     else
       __builtin_amdgcn_global_load_lds((const void*)(base + off + koff), (lds_void*)dst, 4, 0, 0);
   }
 };
 
-// The copies of one workgroup's stages: its rows of A in blocks of 8 (1 KB), dealt to the
-// waves in turn, then NB blocks of B.
-template <bool kGateUp, int BM, int NB, int FN, int NW, bool kBuf>
-struct Fp4Loader {
-  using G = StageGeom<128>;
-  static constexpr int LA = BM / 8 / NW, LB = NB / NW;
-  static_assert(LA * 8 * NW == BM && LB * NW == NB, "whole blocks for every wave");
-  Source<kBuf> a, b, sc;
-  int64_t a_off[LA], b_off[LB], s_off[LB];
-  int wave, live_a;    // blocks of A that this wave copies
-  int a_bytes, stage_bytes, stages;
+// Row block of the packed weights behind block j of a tile's NB (FN to a wave): gate_up, a
+// wave's first half gate and the matching up rows after; clamped, since what lies past C
+// is never stored.
+template <bool kGateUp, int FN>
+__device__ __forceinline__ int weight_block(const MxArgs& g, int nt, int nb, int j) {
+  const int last = g.ncols / kFp4BlockRows - 1;
+  if constexpr (kGateUp) {
+    const int q = j % FN / (FN / 2);
+    const int rb = nt * (nb / 2) + j / FN * (FN / 2) + j % (FN / 2);
+    return (rb < last ? rb : last) + q * g.up;
+  } else {
+    const int rb = nt * nb + j;
+    return rb < last ? rb : last;
+  }
+}
+
+// ---------------------------------------------------------------- many rows an expert
+// A workgroup of four waves, one for each SIMD with all its 512 registers, computes 64 F rows
+// by 256 columns, a wave half of either (F x 4 blocks of 32 x 32).  Wave tiles that large
+// read the least from LDS, which with a product at four times the bf16 rate is as scarce as
+// the matrix pipe: at F = 4 a stage's 32 matrix instructions of a wave take 1024 cycles, the
+// four waves' reads 512 and the copies' writes 264.
+constexpr int kWideSmem = 160 * 1024;
+constexpr int kWaves = 4, kWideFN = 4, kWideNB = 8;  // waves; column blocks of a wave, of a tile
+constexpr int kScaleUnits = 4;  // dwords of a weight row's scales in LDS (each of four stages)
+
+template <int F>
+struct WideStage {
+  static constexpr int kBlocks = 2 * F;  // row blocks
+  static constexpr int kAtScales = kBlocks * kMxBlockBytes;          // of the rows
+  static constexpr int kAtB = kAtScales + kBlocks * kMxScaleBytes;   // weight blocks
+  static constexpr int kBytes = kAtB + kWideNB * kFp4BlockBytes;
+  static constexpr int kRoom = kWideSmem - kScaleUnits * kWideNB * kFp4ScaleBytes;
+  // stages in LDS: as many as fit, and no more than the scale units serve
+  static constexpr int kCount = kRoom / kBytes < 8 ? kRoom / kBytes : 8;
+  static constexpr int kCopies = (kBlocks * 3 + kWaves - 1) / kWaves;  // of A's values, a wave
+  static constexpr int kScales = (kBlocks + kWaves - 1) / kWaves;      // of their scales
+  static constexpr int kB = kWideNB / kWaves;
+  static constexpr int kPerStage = kCopies + kScales + kB;
+};
+
+// The copies of a workgroup's stages.  Every wave issues the same number: those past the
+// last repeat it, and row blocks past the expert's last repeat that one.  The rows' scales
+// (two stages' in a dword) are copied with every stage, so that all are alike.
+template <bool kGateUp, int F, bool kBuf>
+struct WideLoader {
+  using S = WideStage<F>;
+  typedef typename Source<kBuf>::offset offset;
+  Source<kBuf> a, as, b, bs;
+  offset a_off[S::kCopies], as_off[S::kScales], b_off[S::kB], bs_off[S::kB];
+  int wave;
   char *smem, *scales;
 
-  __device__ __forceinline__ void init(const Fp4Args& g, const TileRows& tr, int nt, int lane,
-                                       int wave_, char* smem_, int smem_bytes) {
+  __device__ __forceinline__ int copy_of(int t) const {
+    const int i = t * kWaves + wave, last = S::kBlocks * 3 - 1;
+    return i < last ? i : last;
+  }
+  __device__ __forceinline__ int scale_of(int t) const {
+    const int i = t * kWaves + wave, last = S::kBlocks - 1;
+    return i < last ? i : last;
+  }
+  __device__ __forceinline__ void init(const MxArgs& g, const TileRows& tr, int nt, int lane,
+                                       int wave_, char* smem_) {
     wave = wave_;
     scales = smem_;
-    smem = smem_ + kScaleUnits * NB * kFp4ScaleBytes;
-    const int nb = (tr.rows + 31) / 32;
-    a_bytes = nb * 32 * G::ROW_BYTES;
-    stage_bytes = a_bytes + NB * kFp4BlockBytes;
-    stages = (smem_bytes - kScaleUnits * NB * kFp4ScaleBytes) / stage_bytes;
-    stages = stages < kMaxStages ? stages : kMaxStages;
+    smem = smem_ + kScaleUnits * kWideNB * kFp4ScaleBytes;
     const int e = __builtin_amdgcn_readfirstlane(tr.e);
-    a.init(kBuf ? g.a_base : g.A[0]);
-    b.init(g.B + (int64_t)e * g.b_expert_bytes);
-    sc.init(g.scale + (int64_t)e * g.scale_expert_bytes);
-    live_a = 0;
-    int row[LA];
+    const int64_t rb = mx_row_block(tr, tr.v0);
+    const int pairs = (g.blocks + 1) / 2, last = (tr.rows - 1) / 32;
+    a.init(g.a.values + rb * g.blocks * kMxBlockBytes);
+    as.init(g.a.scales + rb * pairs * kMxScaleBytes);
+    b.init(g.b + (int64_t)e * g.b_expert);
+    bs.init(g.bs + (int64_t)e * g.bs_expert);
 #pragma unroll
-    for (int t = 0; t < LA; ++t) {
-      row[t] = (t * NW + wave) * 8 + lane / G::CH;
-      live_a += (t * NW + wave) * 8 < tr.rows ? 1 : 0;
-    }
-    int src[LA];
-#pragma unroll
-    for (int t = 0; t < LA; ++t) {
-      const int v = tr.v0 + (row[t] < tr.rows ? row[t] : tr.rows - 1);
-      if (g.gather[0]) {
-        int part;
-        const int cr = tr.split_row(v, &part);
-        src[t] = (part ? g.gather[1] : g.gather[0])[cr];
-      } else {
-        src[t] = tr.joint_row(v);
-      }
+    for (int t = 0; t < S::kCopies; ++t) {
+      const int block = copy_of(t) / 3, third = copy_of(t) % 3;
+      a_off[t] = (offset)((int64_t)(block < last ? block : last) * g.blocks * kMxBlockBytes +
+                          third * 1024 + lane * 16);
     }
 #pragma unroll
-    for (int t = 0; t < LA; ++t) {
-      const int64_t r = g.gather[0] ? src[t] / g.gather_k : src[t];
-      a_off[t] = r * g.row_bytes + ((lane % G::CH) ^ G::swz(row[t])) * 16;
+    for (int t = 0; t < S::kScales; ++t) {
+      const int block = scale_of(t);
+      as_off[t] = (offset)((int64_t)(block < last ? block : last) * pairs * kMxScaleBytes + lane * 4);
     }
 #pragma unroll
-    for (int t = 0; t < LB; ++t) {
-      const int j = t * NW + wave;  // tile block: 32 columns of the tile
-      const int last = g.ncols / kFp4BlockRows - 1;
-      int rb;
-      if constexpr (kGateUp) {
-        // a wave's FN blocks: gate for the first half, the matching up rows after
-        const int q = j % FN / (FN / 2);
-        rb = nt * (NB / 2) + j / FN * (FN / 2) + j % (FN / 2);
-        rb = (rb < last ? rb : last) + q * (g.I / kFp4BlockRows);
-      } else {
-        rb = nt * NB + j;
-        rb = rb < last ? rb : last;  // columns past C are never stored
-      }
-      b_off[t] = (int64_t)rb * g.blocks * kFp4BlockBytes + lane * 16;
-      s_off[t] = (int64_t)rb * g.quads * kFp4ScaleBytes + lane * 4;
+    for (int t = 0; t < S::kB; ++t) {
+      const int rb = weight_block<kGateUp, kWideFN>(g, nt, kWideNB, t * kWaves + wave);
+      b_off[t] = (offset)((int64_t)rb * g.blocks * kFp4BlockBytes + lane * 16);
+      bs_off[t] = (offset)((int64_t)rb * g.quads * kFp4ScaleBytes + lane * 4);
     }
   }
-
-  // Stage kt into ring slot `slot`; every fourth with its unit of scales.
+  // Copy q of stage st into ring slot `slot`.
   template <bool kNt>
-  __device__ __forceinline__ void issue(int kt, int slot) const {
-    char* base = smem + slot * stage_bytes;
-    if ((kt & 3) == 0) {
-      char* s = scales + ((kt >> 2) & (kScaleUnits - 1)) * NB * kFp4ScaleBytes;
+  __device__ __forceinline__ void issue(int st, int slot, int q) const {
+    char* base = smem + slot * S::kBytes;
+    if (q < S::kB)
+      b.template load16<kNt>(base + S::kAtB + (q * kWaves + wave) * kFp4BlockBytes, b_off[q],
+                             st * kFp4BlockBytes);
+    else if (q < S::kB + S::kScales)
+      as.load4(base + S::kAtScales + scale_of(q - S::kB) * kMxScaleBytes, as_off[q - S::kB],
+               (st >> 1) * kMxScaleBytes);
+    else
+      a.template load16<false>(base + copy_of(q - S::kB - S::kScales) * 1024,
+                               a_off[q - S::kB - S::kScales], st * kMxBlockBytes);
+  }
+  // The weights' scales of stages 4 u .. 4 u + 3.
+  __device__ __forceinline__ void issue_scales(int u) const {
 #pragma unroll
-      for (int t = 0; t < LB; ++t)
-        sc.load4(s + (t * NW + wave) * kFp4ScaleBytes, s_off[t], (kt >> 2) * kFp4ScaleBytes);
-    }
-#pragma unroll
-    for (int t = 0; t < LB; ++t)
-      b.template load16<kNt>(base + a_bytes + (t * NW + wave) * kFp4BlockBytes, b_off[t],
-                             kt * kFp4BlockBytes);
-#pragma unroll
-    for (int t = 0; t < LA; ++t)
-      if (t < live_a)
-        a.template load16<false>(base + (t * NW + wave) * 1024, a_off[t], kt * G::ROW_BYTES);
+    for (int t = 0; t < S::kB; ++t)
+      bs.load4(scales + ((u & (kScaleUnits - 1)) * kWideNB + t * kWaves + wave) * kFp4ScaleBytes,
+               bs_off[t], u * kFp4ScaleBytes);
   }
 };
 
-// Eight values of a lane as a bf16 fragment.
-__device__ __forceinline__ bf16x8 unpack_fp4(uint32_t v, float power) {
-#if defined(__HIP_DEVICE_COMPILE__)
-  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-  const bf16x2 p0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(v, power, 0);
-  const bf16x2 p1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(v, power, 1);
-  const bf16x2 p2 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(v, power, 2);
-  const bf16x2 p3 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(v, power, 3);
-  return bf16x8{p0[0], p0[1], p1[0], p1[1], p2[0], p2[1], p3[0], p3[1]};
-#else
-  return bf16x8{};
-#endif
-}
-
-// The K loop of a wave that holds F 32-row blocks of the tile from row0 on (F = 0: it only
-// copies and joins the barriers).
-template <int F, int FM, int FN, int NB, bool kNt, class Loader>
-__device__ __forceinline__ void fp4_k_loop(f32x16 (&acc)[FM][FN], const Loader& ld, int KT,
-                                           int lane, int wn, int row0) {
-  using G = StageGeom<128>;
-  static_assert(F <= FM, "band blocks");
-  const int r = lane & 31, half = lane >> 5;
-  const int per_stage = ld.live_a + Loader::LB, stages = ld.stages;
-  for (int s = 0; s < stages - 1; ++s)
-    if (s < KT) ld.template issue<kNt>(s, s);
-  __builtin_amdgcn_s_waitcnt(kWaitLgkm0);
-  int slot = 0, next = stages - 1;  // of stage kt, and of stage kt + stages - 1
-  for (int kt = 0; kt < KT; ++kt) {
-    // stage kt has landed once only the newer stages' loads are pending
-    const int newer = KT - 1 - kt < stages - 2 ? KT - 1 - kt : stages - 2;
-    const int pending = newer * per_stage + (((kt + newer) >> 2) - (kt >> 2)) * Loader::LB;
-    wait_loads(pending < 24 ? pending : 24);
-    __builtin_amdgcn_s_barrier();
-    const char* sa = ld.smem + slot * ld.stage_bytes + row0 * G::ROW_BYTES;
-    if constexpr (F > 0) {
-      const char* sb = ld.smem + slot * ld.stage_bytes + ld.a_bytes + wn * FN * kFp4BlockBytes;
-      const char* ss = ld.scales + (((kt >> 2) & (kScaleUnits - 1)) * NB + wn * FN) * kFp4ScaleBytes;
-      bf16x8 af[2][F], bf[2][FN];
-      uint4 raw[FN];
-      float power[FN];
-      auto rows = [&](int kk, int b) __attribute__((always_inline)) {
-        const int fo = r * G::ROW_BYTES + (((4 * half + kk) ^ G::swz(r)) << 4);
-#pragma unroll
-        for (int i = 0; i < F; ++i) af[b][i] = *(const bf16x8*)(sa + i * 32 * G::ROW_BYTES + fo);
-      };
-      auto cols = [&](int kk, int b) __attribute__((always_inline)) {
-#pragma unroll
-        for (int j = 0; j < FN; ++j) {
-          const uint32_t v = kk == 0 ? raw[j].x : kk == 1 ? raw[j].y : kk == 2 ? raw[j].z : raw[j].w;
-          bf[b][j] = unpack_fp4(v, power[j]);
-        }
-      };
-#pragma unroll
-      for (int j = 0; j < FN; ++j) {
-        raw[j] = *(const uint4*)(sb + j * kFp4BlockBytes + lane * 16);
-        const uint32_t s = *(const uint32_t*)(ss + j * kFp4ScaleBytes + lane * 4);
-        power[j] = __uint_as_float((s >> (8 * (kt & 3)) & 0xffu) << 23);
-      }
-      rows(0, 0);
-      if (kt + stages - 1 < KT) ld.template issue<kNt>(kt + stages - 1, next);
-      cols(0, 0);
-#pragma unroll
-      for (int kk = 0; kk < 4; ++kk) {
-        if (kk + 1 < 4) rows(kk + 1, (kk + 1) & 1);
-        __builtin_amdgcn_sched_barrier(0);
-        if (kk + 1 < 4) cols(kk + 1, (kk + 1) & 1);
-#pragma unroll
-        for (int i = 0; i < F; ++i)
-#pragma unroll
-          for (int j = 0; j < FN; ++j)
-            acc[i][j] = MmaBf16::mma(bf[kk & 1][j], af[kk & 1][i], acc[i][j]);
-        __builtin_amdgcn_sched_barrier(0);
+// The K loop of a wave.  A step multiplies a stage whose operands are in registers, while it
+// reads those of the next from LDS and copies a later one into the slot that the barrier at
+// its start has freed (every wave's reads of it are complete); a copy, which holds its wave for
+// some sixteen cycles, after each few matrix instructions.
+template <int F, bool kNt, class Loader>
+__device__ __forceinline__ void wide_k_loop(f32x16 (&acc)[F][kWideFN], const Loader& ld, int ST,
+                                            int lane, int wm, int wn) {
+  using S = WideStage<F>;
+  constexpr int FN = kWideFN, N = S::kCount;
+  struct Operands {
+    i32x4 a[F][3];
+    i32x4 b[FN];
+    uint32_t as[F], bs[FN];
+  };
+  Operands op[2];
+  // read q of stage st's operands
+  constexpr int kReads = 4 * F + 2 * FN;
+  auto read = [&](Operands& o, int st, int slot, int q) __attribute__((always_inline)) {
+    const char* base = ld.smem + slot * S::kBytes;
+    if (q < 2 * FN) {
+      const int j = q >> 1;
+      if (q & 1) {
+        const char* sc = ld.scales + ((st >> 2) & (kScaleUnits - 1)) * kWideNB * kFp4ScaleBytes;
+        o.bs[j] = *(const uint32_t*)(sc + (wn * FN + j) * kFp4ScaleBytes + lane * 4);
+      } else {
+        o.b[j] = *(const i32x4*)(base + S::kAtB + (wn * FN + j) * kFp4BlockBytes + lane * 16);
       }
     } else {
-      if (kt + stages - 1 < KT) ld.template issue<kNt>(kt + stages - 1, next);
+      const int i = (q - 2 * FN) >> 2, third = (q - 2 * FN) & 3;
+      if (third == 3)
+        o.as[i] = *(const uint32_t*)(base + S::kAtScales + (wm * F + i) * kMxScaleBytes + lane * 4);
+      else
+        o.a[i][third] =
+            *(const i32x4*)(base + (wm * F + i) * kMxBlockBytes + third * 1024 + lane * 16);
     }
-    slot = slot + 1 == stages ? 0 : slot + 1;
-    next = next + 1 == stages ? 0 : next + 1;
-    __builtin_amdgcn_s_waitcnt(kWaitLgkm0);  // this stage's reads are complete
+  };
+  // the prologue's scales first: a unit lands before the first stage that needs it
+#pragma unroll
+  for (int s = 0; s < N; ++s) {
+    if (s >= ST) break;
+    if ((s & 3) == 0) ld.issue_scales(s >> 2);
+#pragma unroll
+    for (int q = 0; q < S::kPerStage; ++q) ld.template issue<kNt>(s, s, q);
+  }
+  // (of N stages' copies; fewer stages wait for all)
+  if (ST >= N)
+    __builtin_amdgcn_s_waitcnt(wait_vm((N - 1) * S::kPerStage));
+  else
+    __builtin_amdgcn_s_waitcnt(wait_vm(0));
+  __builtin_amdgcn_s_waitcnt(kWaitLgkm0);
+  __builtin_amdgcn_s_barrier();
+#pragma unroll
+  for (int q = 0; q < kReads; ++q) read(op[0], 0, 0, q);
+  int slot = 0;
+  auto step = [&](int st, const Operands& o, Operands& next) __attribute__((always_inline)) {
+    const int after = slot + 1 == N ? 0 : slot + 1;
+    const bool again = st + 1 < ST, more = st + N < ST;
+    if (again) {
+      // stage st + 1 has landed once only the copies of the N - 2 after it may be pending
+      // (scales not counted: a few copies more than necessary have landed)
+      if (st + N - 1 < ST)
+        __builtin_amdgcn_s_waitcnt(wait_vm((N - 2) * S::kPerStage));
+      else
+        __builtin_amdgcn_s_waitcnt(wait_vm(0));
+      __builtin_amdgcn_s_waitcnt(kWaitLgkm0);
+      __builtin_amdgcn_s_barrier();
+    }
+    // the bytes of the scales that this stage uses, to the lowest place
+    uint32_t as[F], bs[FN];
+#pragma unroll
+    for (int i = 0; i < F; ++i) as[i] = o.as[i] >> (16 * (st & 1));
+#pragma unroll
+    for (int j = 0; j < FN; ++j) bs[j] = o.bs[j] >> (8 * (st & 3));
+    __builtin_amdgcn_sched_barrier(0);
+    // reads and copies in turn, spread over the stage's matrix instructions
+    constexpr int kMma = 2 * F * FN, kOps = kReads + S::kPerStage;
+#pragma unroll
+    for (int m = 0; m < kMma; ++m) {
+      const int i = m / (2 * FN), j = m % FN;
+      const i32x12 rows = __builtin_shufflevector(
+          __builtin_shufflevector(o.a[i][0], o.a[i][1], 0, 1, 2, 3, 4, 5, 6, 7),
+          __builtin_shufflevector(o.a[i][2], o.a[i][2], 0, 1, 2, 3, -1, -1, -1, -1), 0, 1, 2, 3, 4,
+          5, 6, 7, 8, 9, 10, 11);
+      acc[i][j] = m / FN & 1 ? mx_mma<1>(o.b[j], bs[j], rows, as[i], acc[i][j])
+                             : mx_mma<0>(o.b[j], bs[j], rows, as[i], acc[i][j]);
+      // (the compiler moves matrix instructions down past branches, and so past the copies
+      // and the barrier that they are to cover, unless their results are named before)
+      asm volatile("" : "+a"(acc[i][j]));
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int t = m * kOps / kMma; t < (m + 1) * kOps / kMma; ++t) {
+        const int copies = t * S::kPerStage / kOps, after_t = (t + 1) * S::kPerStage / kOps;
+        if (after_t > copies) {
+          if (more) ld.template issue<kNt>(st + N, slot, copies);
+        } else if (again) {
+          read(next, st + 1, after, t - copies);
+        }
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    if (more && ((st + N) & 3) == 0) ld.issue_scales((st + N) >> 2);
+    slot = after;
+  };
+  int st = 0;
+  for (; st + 1 < ST; st += 2) {
+    step(st, op[0], op[1]);
+    step(st + 1, op[1], op[0]);
+  }
+  if (st < ST) step(st, op[0], op[1]);
+}
+
+// act of 32 rows by 32 columns of two row blocks, from the accumulators of gate and up
+// columns: lane l holds row l % 32 of a block and its columns 8 (q / 4) + 4 (l / 32) + q % 4.
+// Swapping the upper half of one block's registers with the lower half of the other's
+// leaves lane l all 32 columns of one row, in the first block (l < 32) or the second.
+__device__ __forceinline__ TwoParts act_parts(const f32x16& g0, const f32x16& u0, const f32x16& g1,
+                                              const f32x16& u1) {
+  f32x16v even, odd;
+#pragma unroll
+  for (int q = 0; q < 16; ++q) {
+    const float a = swiglu<true>(g0[q], u0[q]), b = swiglu<true>(g1[q], u1[q]);
+    float lo = a, hi = b;  // columns 8 (q / 4) + q % 4 and 4 more of the lane's row
+#if defined(__HIP_DEVICE_COMPILE__)
+    const auto s = __builtin_amdgcn_permlane32_swap(__float_as_uint(a), __float_as_uint(b), false,
+                                                    false);
+    lo = __uint_as_float(s[0]);
+    hi = __uint_as_float(s[1]);
+#endif
+    const int c = 4 * (q / 4) + q % 4 / 2;  // half of the first's column
+    if (q % 2 == 0) {
+      even[c] = lo;
+      even[c + 2] = hi;
+    } else {
+      odd[c] = lo;
+      odd[c + 2] = hi;
+    }
+  }
+  return split32(even, odd);
+}
+
+// Stores the act rows of a wave's F row blocks from row0 on; `col` is the first of its
+// 32-column blocks of C, FC of them.
+template <int FM, int FN>
+__device__ __forceinline__ void store_act(const MxArgs& a, const f32x16 (&acc)[FM][FN],
+                                          const TileRows& tr, int row0, int f, int block0,
+                                          int lane) {
+  constexpr int FC = FN / 2;
+  const int r = lane & 31, half = lane >> 5;
+  const int nk = a.ncols / 64;
+#pragma unroll
+  for (int i = 0; i < FM; i += 2) {
+    if (i >= f) break;
+    constexpr int kLast = FM - 1;
+    const int i1 = i < kLast ? i + 1 : i;
+    const int row = row0 + 32 * (i + half) + r;
+    const bool live = row < tr.rows && (half == 0 || i + 1 < f);
+    const int64_t rb = mx_row_block(tr, tr.v0 + row0 + 32 * (i + half));
+#pragma unroll
+    for (int j = 0; j < FC; ++j) {
+      const int block = block0 + j;
+      if (block * 32 >= a.ncols) break;
+      const TwoParts p = act_parts(acc[i][j], acc[i][j + FC], acc[i1][j], acc[i1][j + FC]);
+      if (live) store_parts(p, a.c, nk, rb, r, block);
+      __builtin_amdgcn_sched_barrier(0);  // one block at a time: a split holds a hundred registers
+    }
   }
 }
 
-template <bool kGateUp, int BM, int BN, int WAVES_M, int WAVES_N, int kSmem, bool kBuf>
-__global__ void __launch_bounds__(64 * WAVES_M * WAVES_N) grouped_gemm_fp4(Fp4Args a) {
-  constexpr int NW = WAVES_M * WAVES_N, NB = BN / 32;
-  constexpr int WM = BM / WAVES_M, WN = BN / WAVES_N, FM = WM / 32, FN = WN / 32;
-  using Loader = Fp4Loader<kGateUp, BM, NB, FN, NW, kBuf>;
-  static_assert(!kGateUp || FN % 2 == 0, "gate/up halves");
-  static_assert(BM * (kGateUp ? BN / 2 : BN) * 2 <= kSmem, "C tile fits the stage buffers");
-  __shared__ __attribute__((aligned(1024))) char smem[kSmem];
+// Scaled fp16 of 64 columns of a row (two blocks' accumulators): the byte of the power of two
+// that brings the largest finite magnitude into [2^14, 2^15).
+__device__ __forceinline__ uint32_t out_scale(const f32x16& a, const f32x16& b) {
+  uint32_t big = 0;
+#pragma unroll
+  for (int q = 0; q < 16; ++q) {
+    const uint32_t x = __float_as_uint(a[q]) & 0x7fffffffu, y = __float_as_uint(b[q]) & 0x7fffffffu;
+    big = x > big && x < 0x7f800000u ? x : big;
+    big = y > big && y < 0x7f800000u ? y : big;
+  }
+  const uint32_t other = (uint32_t)__shfl_xor((int)big, 32);  // the row's other columns
+  big = other > big ? other : big;
+  const int byte = (int)(big >> 23) - 14;
+  return byte > 14 ? (uint32_t)byte : 14u;  // (its reciprocal has to be a number)
+}
+__device__ __forceinline__ float out_factor(uint32_t byte) {
+  return __uint_as_float((254u - byte) << 23);
+}
+
+// kDown epilogue of a wide tile: fp16 rows through the freed stage buffers, row-major, with
+// the four scale bytes of a row behind them, out in 16-byte pieces.
+template <int FM, int FN, int BM, int BN, int NT>
+__device__ __forceinline__ void store_out(const MxArgs& a, const f32x16 (&acc)[FM][FN],
+                                          const TileRows& tr, int nt, int row0, int f, int wn,
+                                          int lane, char* smem) {
+  typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
+  constexpr int CPR = BN / 8;  // 16-byte chunks of a tile row
+  auto at = [](int r, int c) {
+    return r * (BN * 2) + (((c >> 3) ^ (r & (CPR - 1))) << 4) + (c & 7) * 2;
+  };
+  uint8_t* scales = (uint8_t*)smem + BM * BN * 2;
+  const int r0 = row0 + (lane & 31), cq = 4 * (lane >> 5);
+#pragma unroll
+  for (int i = 0; i < FM; ++i) {
+    if (i >= f) break;
+    const int r = r0 + i * 32;
+#pragma unroll
+    for (int j = 0; j < FN; j += 2) {
+      const uint32_t byte = out_scale(acc[i][j], acc[i][j + 1]);
+      const float p = out_factor(byte);
+      if (lane < 32) scales[r * (BN / 64) + (wn * FN + j) / 2] = (uint8_t)byte;
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const f32x16& x = acc[i][j + h];
+          *(f16x4*)(smem + at(r, (wn * FN + j + h) * 32 + 8 * g + cq)) =
+              f16x4{(_Float16)(x[4 * g] * p), (_Float16)(x[4 * g + 1] * p),
+                    (_Float16)(x[4 * g + 2] * p), (_Float16)(x[4 * g + 3] * p)};
+        }
+    }
+  }
+  __syncthreads();
+  const int col0 = nt * BN;
+  for (int ch = threadIdx.x; ch < BM * CPR; ch += NT) {
+    const int r = ch / CPR, c = (ch % CPR) * 8;
+    if (r >= tr.rows || col0 + c >= a.ncols) continue;
+    int part = 0, row = tr.joint_row(tr.v0 + r);
+    if (a.c_split) row = tr.split_row(tr.v0 + r, &part);
+    char *y0 = a.y[0].values, *y1 = a.y[1].values;
+    __builtin_nontemporal_store(*(const u32x4*)(smem + at(r, c)),
+                                (u32x4*)((part ? y1 : y0) + ((int64_t)row * a.ncols + col0 + c) * 2));
+  }
+  const int64_t row_scales = mx_out_scales(a.ncols);
+  static_assert(BN == 256, "a dword of scales a row");
+  for (int r = threadIdx.x; r < tr.rows; r += NT) {
+    int part = 0, row = tr.joint_row(tr.v0 + r);
+    if (a.c_split) row = tr.split_row(tr.v0 + r, &part);
+    char *s0 = a.y[0].scales, *s1 = a.y[1].scales;
+    *(uint32_t*)((part ? s1 : s0) + row * row_scales + nt * 4) = *(const uint32_t*)(scales + r * 4);
+  }
+}
+
+template <bool kGateUp, bool kBuf>
+__global__ void __launch_bounds__(64 * kWaves, 1) grouped_gemm_mx(MxArgs a) {
+  constexpr int BM = 256, BN = 256, FN = kWideFN;
+  static_assert(BM * BN * 2 + BM * (BN / 64) <= kWideSmem, "C tile fits the stage buffers");
+  __shared__ __attribute__((aligned(1024))) char smem[kWideSmem];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int wm = wave / WAVES_N, wn = wave % WAVES_N;
+  const int wm = wave >> 1, wn = wave & 1;
   MTileMap tm;
-  tm.build(a.off0, a.off1, a.E, BM, BM >= 128 ? BM : 1);
+  tm.build(a.off0, a.off1, a.E, BM, BM);
   int mt, nt;
   if (!xcd_tile_at(tm, a.n_tiles, blockIdx.x & 7, blockIdx.x >> 3,
                    (32 + a.n_tiles - 1) / a.n_tiles, &mt, &nt))
     return;
   const TileRows tr = tm.locate(a.off0, a.off1, BM, mt);
-  f32x16 acc[FM][FN];
+  auto run = [&](auto f_tag, auto nt_tag) __attribute__((always_inline)) {
+    constexpr int F = decltype(f_tag)::value;
+    f32x16 acc[F][FN];
 #pragma unroll
-  for (int i = 0; i < FM; ++i)
+    for (int i = 0; i < F; ++i)
 #pragma unroll
-    for (int j = 0; j < FN; ++j) acc[i][j] = f32x16{};
-  // the tile's 32-row blocks are shared out evenly between the wave rows
-  const int nb = (tr.rows + 31) / 32;
-  const int f0 = WAVES_M == 1 ? nb : (nb + 1) / 2;
-  const int f = wm == 0 ? f0 : nb - f0, row0 = wm == 0 ? 0 : f0 * 32;
-  Loader ld;
-  ld.init(a, tr, nt, lane, wave, smem, kSmem);
-  auto run = [&](auto nt_tag) __attribute__((always_inline)) {
-    constexpr bool kNt = decltype(nt_tag)::value;
-    if (FM >= 4 && f == 4) {
-      if constexpr (FM >= 4) fp4_k_loop<4, FM, FN, NB, kNt>(acc, ld, a.blocks, lane, wn, row0);
-    } else if (FM >= 3 && f == 3) {
-      if constexpr (FM >= 3) fp4_k_loop<3, FM, FN, NB, kNt>(acc, ld, a.blocks, lane, wn, row0);
-    } else if (FM >= 2 && f == 2) {
-      if constexpr (FM >= 2) fp4_k_loop<2, FM, FN, NB, kNt>(acc, ld, a.blocks, lane, wn, row0);
-    } else if (f == 1) {
-      fp4_k_loop<1, FM, FN, NB, kNt>(acc, ld, a.blocks, lane, wn, row0);
+      for (int j = 0; j < FN; ++j) acc[i][j] = f32x16{};
+    WideLoader<kGateUp, F, kBuf> ld;
+    ld.init(a, tr, nt, lane, wave, smem);
+    wide_k_loop<F, decltype(nt_tag)::value>(acc, ld, a.blocks, lane, wm, wn);
+    if constexpr (kGateUp) {
+      store_act<F, FN>(a, acc, tr, wm * F * 32, F, nt * (kWideNB / 2) + wn * (FN / 2), lane);
     } else {
-      fp4_k_loop<0, FM, FN, NB, kNt>(acc, ld, a.blocks, lane, wn, row0);
+      __syncthreads();  // every wave is done with the stage buffers
+      store_out<F, FN, 64 * F, BN, 64 * kWaves>(a, acc, tr, nt, wm * F * 32, F, wn, lane, smem);
     }
   };
+  const std::integral_constant<int, 1> f1{};
+  const std::integral_constant<int, 2> f2{};
+  const std::integral_constant<int, 3> f3{};
+  const std::integral_constant<int, 4> f4{};
   // the weights of a tile that holds all of its expert's rows are read by no other tile
-  if (tr.single)
-    run(std::true_type{});
-  else
-    run(std::false_type{});
-  __syncthreads();  // every wave is done with the stage buffers
-  store_tile_lds<kGateUp, 1, FM, FN, BM, BN, WM, WN, 64 * NW>(a, acc, tr, nt, row0, f, wn, lane,
-                                                             smem);
-}
-
-template <bool kGateUp, int BM, int BN, int WAVES_M, int WAVES_N, int kSmem, bool kBuf>
-hipError_t launch_instance(Fp4Args a, const Shape& s, int64_t rows_bound, hipStream_t st) {
-  constexpr int threads = 64 * WAVES_M * WAVES_N, cols = kGateUp ? BN / 2 : BN;
-  a.n_tiles = (a.ncols + cols - 1) / cols;
-  const int64_t grid = xcd_grid(m_tiles_bound(rows_bound, s.E, BM), a.n_tiles);
-  if (grid <= 0) return hipSuccess;
-  if (grid > 0x7fffffff / threads) return hipErrorInvalidConfiguration;
-  hipLaunchKernelGGL((grouped_gemm_fp4<kGateUp, BM, BN, WAVES_M, WAVES_N, kSmem, kBuf>),
-                     dim3((unsigned)grid), dim3(threads), 0, st, a);
-  return hipGetLastError();
+  const std::true_type once{};
+  const std::false_type shared{};
+  if (tr.single) {
+    if (tr.rows <= 64)
+      run(f1, once);
+    else if (tr.rows <= 128)
+      run(f2, once);
+    else if (tr.rows <= 192)
+      run(f3, once);
+    else
+      run(f4, once);
+  } else {
+    if (tr.rows <= 64)
+      run(f1, shared);
+    else if (tr.rows <= 128)
+      run(f2, shared);
+    else if (tr.rows <= 192)
+      run(f3, shared);
+    else
+      run(f4, shared);
+  }
 }
 
 template <bool kGateUp, bool kBuf>
-hipError_t launch_kind(const Fp4Args& a, const Shape& s, int64_t rows_bound, hipStream_t st) {
-  if (rows_bound >= 4096)
-    return launch_instance<kGateUp, 256, 256, 2, 4, 160 * 1024, kBuf>(a, s, rows_bound, st);
-  return launch_instance<kGateUp, 32, 256, 1, 4, 80 * 1024, kBuf>(a, s, rows_bound, st);
+hipError_t launch_wide(MxArgs a, int64_t rows_bound, hipStream_t st) {
+  constexpr int cols = kGateUp ? 128 : 256;
+  a.n_tiles = (a.ncols + cols - 1) / cols;
+  const int64_t grid = xcd_grid(m_tiles_bound(rows_bound, a.E, 256), a.n_tiles);
+  if (grid <= 0) return hipSuccess;
+  if (grid > 0x7fffffff / (64 * kWaves)) return hipErrorInvalidConfiguration;
+  hipLaunchKernelGGL((grouped_gemm_mx<kGateUp, kBuf>), dim3((unsigned)grid), dim3(64 * kWaves), 0,
+                     st, a);
+  return hipGetLastError();
 }
 
 template <bool kGateUp>
-hipError_t launch(const Shape& s, const GroupedIO& io, const uint8_t* B, const uint8_t* scale,
-                  hipStream_t st) {
-  if (io.rows_bound <= 0) return hipSuccess;
-  const int K = kGateUp ? s.H : s.I, rows = kGateUp ? 2 * s.I : s.H;  // of an expert's matrix
-  Fp4Args a{};
-  a.A[0] = a.A[1] = (const char*)io.a[0];
-  a.C[0] = (uint16_t*)io.c[0];
-  a.C[1] = (uint16_t*)(io.c_split ? io.c[1] : io.c[0]);
+hipError_t launch(const MxArgs& a, int64_t rows_bound, hipStream_t st) {
+  if (rows_bound <= 0) return hipSuccess;
+  // descriptor loads take 32-bit offsets from a tile's first row block and an expert's weights
+  const uint64_t lim = (uint64_t)1 << 32;
+  const bool buf = (uint64_t)8 * a.blocks * kMxBlockBytes < lim && (uint64_t)a.b_expert < lim;
+  return buf ? launch_wide<kGateUp, true>(a, rows_bound, st)
+             : launch_wide<kGateUp, false>(a, rows_bound, st);
+}
+
+// K columns; `rows` rows of an expert's weights.
+MxArgs mx_args(const Shape& s, const MxIO& io, const MxRows& rows_of_a, int K, int rows) {
+  MxArgs a{};
+  a.a = rows_of_a;
   a.off0 = io.off[0];
   a.off1 = io.off[1];
-  a.c_split = io.c_split && io.off[1];
-  a.gather[0] = io.gather[0];
-  a.gather[1] = io.off[1] ? io.gather[1] : io.gather[0];
-  a.gather_k = io.gather_k;
-  a.B = (const char*)B;
-  a.scale = (const char*)scale;
+  a.b = (const char*)io.w;
+  a.bs = (const char*)io.w_scale;
+  a.b_expert = (int64_t)rows * K / 2;
+  a.bs_expert = fp4_scale_bytes(rows, K);
   a.E = s.E;
-  a.I = s.I;
-  a.row_bytes = (int64_t)K * 2;
-  a.ncols = kGateUp ? s.I : s.H;
   a.blocks = K / kFp4BlockCols;
   a.quads = (int)fp4_scale_quads(K);
-  a.b_expert_bytes = (int64_t)rows * K / 2;
-  a.scale_expert_bytes = fp4_scale_bytes(rows, K);
-  a.a_base = a.A[0];
-  // descriptor loads take 32-bit offsets: the rows of A, and an expert's weights, each
-  // have to lie within 4 GiB
-  const bool buf = rows_fit_4g(a.A[0], a.A[0], kGateUp ? s.T : io.rows_bound, K) &&
-                   (uint64_t)a.b_expert_bytes < ((uint64_t)1 << 32);
-  return buf ? launch_kind<kGateUp, true>(a, s, io.rows_bound, st)
-             : launch_kind<kGateUp, false>(a, s, io.rows_bound, st);
+  return a;
 }
 
 }  // namespace
 
-hipError_t launch_gate_up_fp4(const Shape& s, const GroupedIO& io, const uint8_t* w_gate_up,
-                              const uint8_t* w_scale, hipStream_t st) {
-  return launch<true>(s, io, w_gate_up, w_scale, st);
+hipError_t launch_gate_up_mx(const Shape& s, const MxIO& io, const MxRows& x, const MxRows& act,
+                             hipStream_t st) {
+  MxArgs a = mx_args(s, io, x, s.H, 2 * s.I);
+  a.ncols = s.I;
+  a.up = s.I / kFp4BlockRows;
+  a.c = act;
+  return launch<true>(a, io.rows_bound, st);
 }
 
-hipError_t launch_down_fp4(const Shape& s, const GroupedIO& io, const uint8_t* w_down,
-                           const uint8_t* w_scale, hipStream_t st) {
-  return launch<false>(s, io, w_down, w_scale, st);
+hipError_t launch_down_mx(const Shape& s, const MxIO& io, const MxRows& act, const MxRows (&y)[2],
+                          hipStream_t st) {
+  MxArgs a = mx_args(s, io, act, s.I, s.H);
+  a.ncols = s.H;
+  a.y[0] = y[0];
+  a.y[1] = io.off[1] ? y[1] : y[0];
+  a.c_split = io.off[1] != nullptr;
+  return launch<false>(a, io.rows_bound, st);
 }
 
 }  // namespace moe

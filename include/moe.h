@@ -687,31 +687,22 @@ moe_status moe_dequantize_mx(int64_t rows, int64_t cols, int32_t dtype, const ui
 /* ---------------------------------------------------------------------------
  * The layer with 4-bit experts (inference; there is no backward).
  *
- * Rows, act, y and out are bf16 (MOE_F32 is MOE_ERR_UNSUPPORTED), weights packed
+ * hidden_states and out are bf16 (MOE_F32 is MOE_ERR_UNSUPPORTED), weights packed
  * matrices as above, expert after expert: w_gate_up_q and its scales E matrices of
- * [2I][H], w_down_q and its scales E of [H][I].  Products are those of the bf16 layer with
- * the weights written out in bf16: fp32 sums; act, y and out rounded once each.  Rows,
- * offsets, src_row, pairs and dropped ids are those of the calls above, and results do not depend
- * on N.  moe_mx_forward gives the bits of its steps, except for a few assignments (T * k <= 64),
- * which it sums in another order (the same within rounding).
+ * [2I][H], w_down_q and its scales E of [H][I].
+ * The products take their activations (hidden_states and act) as the sum of two 6-bit
+ * floating point numbers (E2M3), each with a power of two for 32 consecutive values:
+ * off by at most 2^-8.9 of the largest of the 32, and over them closer than a rounding to
+ * bf16.  Sums are fp32; y is kept to 2^-12, out rounded to bf16 once.
+ * A token that holds an infinity, a NaN or a magnitude above 1.875 * 2^127 gives NaN in its
+ * own output row only.  Dropped ids as in the calls above; results do not depend on N.
  * Limits: H % 64 == 0 and I % 64 == 0.
  * --------------------------------------------------------------------------- */
 
-/* First expert product with the SwiGLU epilogue: moe_expert_gate_up_gather_pair with
- * packed 4-bit weights. */
-moe_status moe_mx_gate_up_gather_pair(const moe_shape* shape, int32_t chunk,
-                                      const void* hidden_states, const int32_t* src_row,
-                                      const int32_t* offsets, const uint8_t* w_gate_up_q,
-                                      const uint8_t* w_gate_up_scale, void* act,
-                                      hipStream_t stream);
-
-/* Second expert product: moe_expert_down_pair with packed 4-bit weights. */
-moe_status moe_mx_down_pair(const moe_shape* shape, int32_t chunk, const void* act,
-                            const int32_t* offsets, const uint8_t* w_down_q,
-                            const uint8_t* w_down_scale, void* y0, void* y1, hipStream_t stream);
-
-/* Bytes of workspace moe_mx_forward needs: the metadata plus min(N,2) slots of
- * ceil(T/N)*k rows of (H + I) elements.  Host-only. */
+/* Bytes of workspace moe_mx_forward needs: the metadata and, for the min(N,2) * ceil(T/N) * k
+ * rows of a pair, 25/16 bytes for each of H + I values, in blocks of 32 rows of which
+ * every expert may leave one in part empty (up to 50 E (H + I) bytes more), and 2H bytes of y
+ * with one for each 64 of H.  Host-only. */
 moe_status moe_mx_workspace_size(const moe_shape* shape, size_t* bytes);
 
 /*
