@@ -40,8 +40,9 @@ struct MxArgs {
 };
 
 // One product of 64 columns: weights w (16 bytes a lane) and a part of the rows (the first
-// or the last 24 of a lane's 48 bytes), each with a scale byte of a dword.
-template <int kPart>
+// or the last 24 of a lane's 48 bytes), with byte kWs of the weights' scales and byte kAs + kPart
+// of the rows'.
+template <int kPart, int kWs, int kAs>
 __device__ __forceinline__ f32x16 mx_mma(const i32x4& w, uint32_t ws, const i32x12& a, uint32_t as,
                                          const f32x16& c) {
 #if defined(__HIP_DEVICE_COMPILE__)
@@ -52,12 +53,20 @@ __device__ __forceinline__ f32x16 mx_mma(const i32x4& w, uint32_t ws, const i32x
     av = __builtin_shufflevector(a, a, 0, 1, 2, 3, 4, 5, -1, -1);
   else
     av = __builtin_shufflevector(a, a, 6, 7, 8, 9, 10, 11, -1, -1);
-  // (4: E2M1, 2: E2M3; byte 0 of the weights' scales, byte kPart of the rows')
-  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(wv, av, c, 4, 2, 0, (int)ws, kPart,
+  // (4: E2M1, 2: E2M3)
+  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(wv, av, c, 4, 2, kWs, (int)ws, kAs + kPart,
                                                          (int)as);
 #else
   return c;
 #endif
+}
+
+// A lane's 48 bytes of a row block, from its thirds.
+__device__ __forceinline__ i32x12 both_parts(const i32x4 (&a)[3]) {
+  return __builtin_shufflevector(
+      __builtin_shufflevector(a[0], a[1], 0, 1, 2, 3, 4, 5, 6, 7),
+      __builtin_shufflevector(a[2], a[2], 0, 1, 2, 3, -1, -1, -1, -1), 0, 1, 2, 3, 4, 5, 6, 7, 8, 9,
+      10, 11);
 }
 
 template <bool kBuf>
@@ -282,12 +291,9 @@ __device__ __forceinline__ void wide_k_loop(f32x16 (&acc)[F][kWideFN], const Loa
 #pragma unroll
     for (int m = 0; m < kMma; ++m) {
       const int i = m / (2 * FN), j = m % FN;
-      const i32x12 rows = __builtin_shufflevector(
-          __builtin_shufflevector(o.a[i][0], o.a[i][1], 0, 1, 2, 3, 4, 5, 6, 7),
-          __builtin_shufflevector(o.a[i][2], o.a[i][2], 0, 1, 2, 3, -1, -1, -1, -1), 0, 1, 2, 3, 4,
-          5, 6, 7, 8, 9, 10, 11);
-      acc[i][j] = m / FN & 1 ? mx_mma<1>(o.b[j], bs[j], rows, as[i], acc[i][j])
-                             : mx_mma<0>(o.b[j], bs[j], rows, as[i], acc[i][j]);
+      const i32x12 rows = both_parts(o.a[i]);
+      acc[i][j] = m / FN & 1 ? mx_mma<1, 0, 0>(o.b[j], bs[j], rows, as[i], acc[i][j])
+                             : mx_mma<0, 0, 0>(o.b[j], bs[j], rows, as[i], acc[i][j]);
       // (the compiler moves matrix instructions down past branches, and so past the copies
       // and the barrier that they are to cover, unless their results are named before)
       asm volatile("" : "+a"(acc[i][j]));
@@ -343,22 +349,19 @@ __device__ __forceinline__ TwoParts act_parts(const f32x16& g0, const f32x16& u0
   return split32(even, odd);
 }
 
-// Stores the act rows of a wave's F row blocks from row0 on; `col` is the first of its
-// 32-column blocks of C, FC of them.
+// Stores the act rows of a wave's FM row blocks from row0 on, 32-column blocks block0 on.
 template <int FM, int FN>
 __device__ __forceinline__ void store_act(const MxArgs& a, const f32x16 (&acc)[FM][FN],
-                                          const TileRows& tr, int row0, int f, int block0,
-                                          int lane) {
+                                          const TileRows& tr, int row0, int block0, int lane) {
   constexpr int FC = FN / 2;
   const int r = lane & 31, half = lane >> 5;
   const int nk = a.ncols / 64;
 #pragma unroll
   for (int i = 0; i < FM; i += 2) {
-    if (i >= f) break;
     constexpr int kLast = FM - 1;
     const int i1 = i < kLast ? i + 1 : i;
     const int row = row0 + 32 * (i + half) + r;
-    const bool live = row < tr.rows && (half == 0 || i + 1 < f);
+    const bool live = row < tr.rows && (half == 0 || i + 1 < FM);
     const int64_t rb = mx_row_block(tr, tr.v0 + row0 + 32 * (i + half));
 #pragma unroll
     for (int j = 0; j < FC; ++j) {
@@ -394,8 +397,8 @@ __device__ __forceinline__ float out_factor(uint32_t byte) {
 // the four scale bytes of a row behind them, out in 16-byte pieces.
 template <int FM, int FN, int BM, int BN, int NT>
 __device__ __forceinline__ void store_out(const MxArgs& a, const f32x16 (&acc)[FM][FN],
-                                          const TileRows& tr, int nt, int row0, int f, int wn,
-                                          int lane, char* smem) {
+                                          const TileRows& tr, int nt, int row0, int wn, int lane,
+                                          char* smem) {
   typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
   constexpr int CPR = BN / 8;  // 16-byte chunks of a tile row
   auto at = [](int r, int c) {
@@ -405,7 +408,6 @@ __device__ __forceinline__ void store_out(const MxArgs& a, const f32x16 (&acc)[F
   const int r0 = row0 + (lane & 31), cq = 4 * (lane >> 5);
 #pragma unroll
   for (int i = 0; i < FM; ++i) {
-    if (i >= f) break;
     const int r = r0 + i * 32;
 #pragma unroll
     for (int j = 0; j < FN; j += 2) {
@@ -444,6 +446,32 @@ __device__ __forceinline__ void store_out(const MxArgs& a, const f32x16 (&acc)[F
   }
 }
 
+// Scaled fp16 of 32 rows of the 64 columns from col0 on, straight from the accumulators: lane
+// l holds row l % 32 and columns 8 (q / 4) + 4 (l / 32) + q % 4 of each block.
+__device__ __forceinline__ void store_out_rows(const MxArgs& a, const f32x16 (&acc)[2],
+                                               const TileRows& tr, int col0, int lane) {
+  typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
+  const uint32_t byte = out_scale(acc[0], acc[1]);
+  const float p = out_factor(byte);
+  const int r = lane & 31, half = lane >> 5;
+  if (r >= tr.rows || col0 >= a.ncols) return;
+  int part = 0, row = tr.joint_row(tr.v0 + r);
+  if (a.c_split) row = tr.split_row(tr.v0 + r, &part);
+  char* to = (part ? a.y[1].values : a.y[0].values) + ((int64_t)row * a.ncols + col0) * 2;
+  if (half == 0)
+    ((uint8_t*)(part ? a.y[1].scales : a.y[0].scales))[row * mx_out_scales(a.ncols) + col0 / 64] =
+        (uint8_t)byte;
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const f32x16& x = acc[j];
+#pragma unroll
+    for (int g = 0; g < 4; ++g)
+      *(f16x4*)(to + (32 * j + 8 * g + 4 * half) * 2) =
+          f16x4{(_Float16)(x[4 * g] * p), (_Float16)(x[4 * g + 1] * p),
+                (_Float16)(x[4 * g + 2] * p), (_Float16)(x[4 * g + 3] * p)};
+  }
+}
+
 template <bool kGateUp, bool kBuf>
 __global__ void __launch_bounds__(64 * kWaves, 1) grouped_gemm_mx(MxArgs a) {
   constexpr int BM = 256, BN = 256, FN = kWideFN;
@@ -469,10 +497,10 @@ __global__ void __launch_bounds__(64 * kWaves, 1) grouped_gemm_mx(MxArgs a) {
     ld.init(a, tr, nt, lane, wave, smem);
     wide_k_loop<F, decltype(nt_tag)::value>(acc, ld, a.blocks, lane, wm, wn);
     if constexpr (kGateUp) {
-      store_act<F, FN>(a, acc, tr, wm * F * 32, F, nt * (kWideNB / 2) + wn * (FN / 2), lane);
+      store_act<F, FN>(a, acc, tr, wm * F * 32, nt * (kWideNB / 2) + wn * (FN / 2), lane);
     } else {
       __syncthreads();  // every wave is done with the stage buffers
-      store_out<F, FN, 64 * F, BN, 64 * kWaves>(a, acc, tr, nt, wm * F * 32, F, wn, lane, smem);
+      store_out<F, FN, 64 * F, BN, 64 * kWaves>(a, acc, tr, nt, wm * F * 32, wn, lane, smem);
     }
   };
   const std::integral_constant<int, 1> f1{};
@@ -515,9 +543,170 @@ hipError_t launch_wide(MxArgs a, int64_t rows_bound, hipStream_t st) {
   return hipGetLastError();
 }
 
+// ---------------------------------------------------------------- few rows an expert
+// Products with up to 32 rows a tile, bound by streaming the weights: every wave reads its own
+// 64 weight rows (gate_up: 32 gate rows and their up rows) straight into registers, a unit of
+// four stages ahead, and no other wave reads them; only the rows of A, which the waves of a
+// workgroup share, go through LDS, a unit at a time in two buffers with one barrier for it.
+// Of an H = 7168, I = 2048 layer with 64 tokens on 8 of 256 experts (2 rows each) gate_up
+// reads 3.4 GB in 590 us and down 1.7 in 285, 5.9 and 6.1 TB/s (a plain read of such weights:
+// 6.8).  Loads that leave the weights in the caches cost 6% more; two or six waves a
+// workgroup 0 and 19%.
+constexpr int kStreamWaves = 4, kUnit = 4;
+// Rows an expert, on average, up to which these products are taken.  The layer, these and the
+// wide ones: 2 rows 0.89 and 1.21 ms, 8 rows 1.07 and 1.42, 16 rows 1.13 and 1.52, 32 rows
+// 1.63 and 1.55; of a layer with H = 2048, I = 1024, 64 experts 32 rows 0.085 and 0.097.
+constexpr int kStreamRows = 24;
+
+template <bool kGateUp>
+__global__ void __launch_bounds__(64 * kStreamWaves) stream_mx(MxArgs a) {
+  constexpr int BM = 32, FN = 2;
+  constexpr int kUnitBytes = kUnit * kMxBlockBytes + kUnit / 2 * kMxScaleBytes;
+  __shared__ __attribute__((aligned(1024))) char smem[2 * kUnitBytes];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  MTileMap tm;
+  tm.build(a.off0, a.off1, a.E, BM, BM);
+  int mt, nt;
+  if (!xcd_tile_at(tm, a.n_tiles, blockIdx.x & 7, blockIdx.x >> 3,
+                   (32 + a.n_tiles - 1) / a.n_tiles, &mt, &nt))
+    return;
+  const TileRows tr = tm.locate(a.off0, a.off1, BM, mt);
+  const int e = __builtin_amdgcn_readfirstlane(tr.e);
+  const int units = a.quads, KB = a.blocks, pairs = (KB + 1) / 2;
+  const int r = lane & 31;
+
+  // Unit u of A: twelve kilobytes of values, three to a wave, and two dwords a row of scales.
+  // Blocks past the last of K repeat that; the entries of rows past the tile's are not copied.
+  const int64_t rb0 = mx_row_block(tr, tr.v0);
+  const char* av = a.a.values + rb0 * KB * kMxBlockBytes + lane * 16;
+  const char* as = a.a.scales + rb0 * pairs * kMxScaleBytes + lane * 4;
+  auto copy = [&](int u) __attribute__((always_inline)) {
+    if (r >= tr.rows) return;
+    char* base = smem + (u & 1) * kUnitBytes;
+#pragma unroll
+    for (int t = 0; t < kUnit * 3 / kStreamWaves; ++t) {
+      const int q = t * kStreamWaves + wave, k = kUnit * u + q / 3;
+      __builtin_amdgcn_global_load_lds(
+          (const void*)(av + (int64_t)(k < KB ? k : KB - 1) * kMxBlockBytes + q % 3 * 1024),
+          (lds_void*)(base + q * 1024), 16, 0, 0);
+    }
+    const int d = wave & 1, pair = 2 * u + d;
+    __builtin_amdgcn_global_load_lds(
+        (const void*)(as + (int64_t)(pair < pairs ? pair : pairs - 1) * kMxScaleBytes),
+        (lds_void*)(base + kUnit * kMxBlockBytes + d * kMxScaleBytes), 4, 0, 0);
+  };
+  const i32x4* b[FN];
+  const uint32_t* bs[FN];
+#pragma unroll
+  for (int j = 0; j < FN; ++j) {
+    const int rb = weight_block<kGateUp, FN>(a, nt, kStreamWaves * FN, wave * FN + j);
+    b[j] = (const i32x4*)(a.b + e * a.b_expert + (int64_t)rb * KB * kFp4BlockBytes) + lane;
+    bs[j] = (const uint32_t*)(a.bs + e * a.bs_expert + (int64_t)rb * units * kFp4ScaleBytes) + lane;
+  }
+  f32x16 acc[1][FN];
+#pragma unroll
+  for (int j = 0; j < FN; ++j) acc[0][j] = f32x16{};
+
+  i32x4 w[kUnit][FN];
+  uint32_t sc[FN], sn[FN];
+  auto load = [&](int k, i32x4 (&to)[FN]) __attribute__((always_inline)) {
+#pragma unroll
+    for (int j = 0; j < FN; ++j)
+      to[j] = __builtin_nontemporal_load(b[j] + (int64_t)k * (kFp4BlockBytes / 16));
+  };
+  copy(0);
+  __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+  for (int j = 0; j < FN; ++j) sn[j] = sc[j] = bs[j][0];
+#pragma unroll
+  for (int k = 0; k < kUnit; ++k)
+    if (k < KB) load(k, w[k]);
+  auto stage = [&](const char* sa, auto k_tag, const i32x4 (&x)[FN]) __attribute__((always_inline)) {
+    constexpr int k = decltype(k_tag)::value;
+    i32x4 thirds[3];
+#pragma unroll
+    for (int t = 0; t < 3; ++t)
+      thirds[t] = *(const i32x4*)(sa + k * kMxBlockBytes + t * 1024 + lane * 16);
+    const uint32_t s =
+        *(const uint32_t*)(sa + kUnit * kMxBlockBytes + k / 2 * kMxScaleBytes + lane * 4);
+    const i32x12 row = both_parts(thirds);
+#pragma unroll
+    for (int j = 0; j < FN; ++j)
+      acc[0][j] = mx_mma<0, k, 2 * (k & 1)>(x[j], sc[j], row, s, acc[0][j]);
+#pragma unroll
+    for (int j = 0; j < FN; ++j)
+      acc[0][j] = mx_mma<1, k, 2 * (k & 1)>(x[j], sc[j], row, s, acc[0][j]);
+  };
+  const std::integral_constant<int, 0> k0{};
+  const std::integral_constant<int, 1> k1{};
+  const std::integral_constant<int, 2> k2{};
+  const std::integral_constant<int, 3> k3{};
+  const int full = KB / kUnit;  // whole units
+  for (int u = 0; u < units; ++u) {
+    __builtin_amdgcn_sched_barrier(0);
+    // this unit's rows have landed once only the loads of a whole unit's stages, which were
+    // issued after them, are pending
+    if (u < full)
+      __builtin_amdgcn_s_waitcnt(wait_vm(kUnit * FN));
+    else
+      __builtin_amdgcn_s_waitcnt(wait_vm(0));
+    __builtin_amdgcn_s_waitcnt(kWaitLgkm0);  // and this wave's reads of the other buffer are done
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    const char* sa = smem + (u & 1) * kUnitBytes;
+    if (u + 1 < units) copy(u + 1);
+    __builtin_amdgcn_sched_barrier(0);  // (that count: no load moves up past the copies)
+    if (u + 1 < units) {
+#pragma unroll
+      for (int j = 0; j < FN; ++j) sn[j] = bs[j][(u + 1) * (kFp4ScaleBytes / 4)];
+    }
+    if (u + 1 < full) {
+      stage(sa, k0, w[0]);
+      load(kUnit * (u + 1), w[0]);
+      stage(sa, k1, w[1]);
+      load(kUnit * (u + 1) + 1, w[1]);
+      stage(sa, k2, w[2]);
+      load(kUnit * (u + 1) + 2, w[2]);
+      stage(sa, k3, w[3]);
+      load(kUnit * (u + 1) + 3, w[3]);
+    } else {
+      auto part = [&](auto k_tag) __attribute__((always_inline)) {
+        constexpr int k = decltype(k_tag)::value;
+        if (kUnit * u + k < KB) stage(sa, k_tag, w[k]);
+        if (kUnit * (u + 1) + k < KB) load(kUnit * (u + 1) + k, w[k]);
+      };
+      part(k0);
+      part(k1);
+      part(k2);
+      part(k3);
+    }
+#pragma unroll
+    for (int j = 0; j < FN; ++j) sc[j] = sn[j];
+  }
+
+  if constexpr (kGateUp) {
+    store_act<1, FN>(a, acc, tr, 0, nt * kStreamWaves + wave, lane);
+  } else {
+    store_out_rows(a, acc[0], tr, (nt * kStreamWaves + wave) * 64, lane);
+  }
+}
+
+template <bool kGateUp>
+hipError_t launch_stream(MxArgs a, int64_t rows_bound, hipStream_t st) {
+  constexpr int cols = kStreamWaves * (kGateUp ? 32 : 64);
+  a.n_tiles = (a.ncols + cols - 1) / cols;
+  const int64_t grid = xcd_grid(m_tiles_bound(rows_bound, a.E, 32), a.n_tiles);
+  if (grid <= 0) return hipSuccess;
+  if (grid > 0x7fffffff / (64 * kStreamWaves)) return hipErrorInvalidConfiguration;
+  hipLaunchKernelGGL((stream_mx<kGateUp>), dim3((unsigned)grid), dim3(64 * kStreamWaves), 0, st,
+                     a);
+  return hipGetLastError();
+}
+
 template <bool kGateUp>
 hipError_t launch(const MxArgs& a, int64_t rows_bound, hipStream_t st) {
   if (rows_bound <= 0) return hipSuccess;
+  if (rows_bound <= (int64_t)kStreamRows * a.E) return launch_stream<kGateUp>(a, rows_bound, st);
   // descriptor loads take 32-bit offsets from a tile's first row block and an expert's weights
   const uint64_t lim = (uint64_t)1 << 32;
   const bool buf = (uint64_t)8 * a.blocks * kMxBlockBytes < lim && (uint64_t)a.b_expert < lim;
