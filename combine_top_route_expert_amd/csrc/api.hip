@@ -1366,7 +1366,7 @@ MxPlan mx_plan(const Shape& s) {
   const int64_t blocks = mx_row_blocks(nslots * (int64_t)rows, s.E);
   p.x = take(mx_value_bytes(blocks, s.H));
   p.x_scale = take(mx_scale_bytes(blocks, s.H));
-  p.act = take(mx_value_bytes(blocks, s.I));
+  p.act = take(std::max<size_t>(mx_value_bytes(blocks, s.I), few_rows_mx(s) ? (size_t)s.A * s.I * 4 : 0));
   p.act_scale = take(mx_scale_bytes(blocks, s.I));
   for (int i = 0; i < nslots; ++i) {
     p.y[i] = take(rows * s.H * 2);
@@ -1413,6 +1413,9 @@ moe_status moe_mx_forward(const moe_shape* shape, const void* hidden_states,
   int32_t* src_row = (int32_t*)(w + p.src_row);
   int32_t* dst_row = (int32_t*)(w + p.dst_row);
   int32_t* err = dev_error ? dev_error : (int32_t*)(w + p.dev_err);
+  if (few_rows_mx(s))
+    return hip_status(launch_few_mx(s, hidden_states, top_k_index, top_k_weights, w_gate_up_q,
+                                    w_gate_up_scale, w_down_q, w_down_scale, w + p.act, out, err, stream));
   const MxRows x{w + p.x, w + p.x_scale}, act{w + p.act, w + p.act_scale};
   const MxRows y[2] = {{w + p.y[0], w + p.y_scale[0]}, {w + p.y[1], w + p.y_scale[1]}};
   hipError_t he = launch_route_meta(s, top_k_index, (int32_t*)(w + p.counts), offsets,

@@ -270,6 +270,14 @@ hipError_t launch_down_mx(const Shape& s, const MxIO& io, const MxRows& act, con
 hipError_t launch_combine_scaled(const Shape& s, int t0, int t_mid, int t1, const MxRows (&y)[2],
                                  const int32_t* dst_row, const float* w, void* out,
                                  hipStream_t st);
+// The whole layer with 4-bit experts for a few assignments (few_rows_mx.hip): nothing is
+// sorted, act holds row f for assignment f, four bytes a value; also counts the dropped ids.
+bool few_rows_mx(const Shape& s);
+hipError_t launch_few_mx(const Shape& s, const void* hidden_states, const int32_t* top_k_index,
+                         const float* top_k_weights, const uint8_t* w_gate_up_q,
+                         const uint8_t* w_gate_up_scale, const uint8_t* w_down_q,
+                         const uint8_t* w_down_scale, void* act, void* out, int32_t* dev_error,
+                         hipStream_t st);
 
 // The whole 8-bit layer for a few assignments (few_rows_i8.hip): nothing is sorted,
 // act [T*k][I] holds row f for assignment f; also counts the dropped ids.

@@ -170,8 +170,38 @@ def two_parts(x, delta=None):
     return v.view_as(x), off.view_as(x)
 
 
+def few(s):
+    """Whether a layer takes the form for a few assignments: x as it is, act in two bf16 numbers, y in float32."""
+    return s.T * s.k <= 32 and (s.T == 1 or s.T * s.k <= s.E)
+
+
+def few_reference(c: Case, x=None):
+    """Float32 sums of exact products: at most K / 2 additions in a row, each off by at most 2 U of the magnitudes so far, then
+    at most 32 of partial sums.  act comes as two bf16 numbers, off by 2^-16, and takes twice as many; the slots' weights and
+    sums add k + 1 more."""
+    s = c.shape
+    x = (c.x if x is None else x).double()
+    ref = torch.zeros(s.T, s.H, dtype=torch.float64, device="cuda")
+    err = torch.zeros_like(ref)
+    for t in range(s.T):
+        for j in range(s.k):
+            e = int(c.idx[t, j])
+            if not 0 <= e < s.E:
+                continue
+            gu = c.vgu[e].double()
+            p = gu @ x[t]
+            act, ea = swiglu_bound(*p.chunk(2), *((gu.abs() @ x[t].abs()) * (s.H + 64) * U).chunk(2))
+            ea = ea + 2.0 ** -16 * act.abs()
+            v, w = c.vd[e].double(), float(c.w[t, j])
+            ref[t] += v @ act * w
+            err[t] += (v.abs() @ ea + v.abs() @ (act.abs() + ea) * (2 * s.I + 66 + s.k) * U) * abs(w)
+    return ref, err + HALF * (ref.abs() + err)
+
+
 def layer_reference(c: Case, x=None):
     s = c.shape
+    if few(s):
+        return few_reference(c, x)
     x2 = two_parts(c.x if x is None else x)
     ref = torch.zeros(s.T, s.H, dtype=torch.float64, device="cuda")
     err = torch.zeros_like(ref)
@@ -209,6 +239,31 @@ def test_against_float64(T, H, E, k, I, N):  # noqa: E741
     c = Case(T, H, E, k, I, N, seed=T)
     within(c.forward(), *layer_reference(c), "out")
     assert int(c.err.item()) == 0
+
+
+# one token and a handful: one expert, as many assignments as experts, 32 of them and one more; K of less than a unit of
+# columns, of a part of one, of more units than waves
+FEW = [(1, 64, 1, 1, 64), (1, 64, 2, 8, 64), (1, 2048, 16, 4, 1024), (2, 320, 8, 3, 448), (8, 192, 32, 4, 576),
+       (11, 192, 40, 3, 64), (4, 4096 + 320, 9, 2, 2240), (4, 64, 64, 8, 128), (1, 128, 3, 32, 192),
+       (11, 128, 70, 3, 192)]
+
+
+@pytest.mark.parametrize("T,H,E,k,I", FEW)
+def test_few_assignments(T, H, E, k, I):  # noqa: E741
+    say(f"4-bit experts T={T} H={H} E={E} k={k} I={I}")
+    c = Case(T, H, E, k, I, seed=T + k)
+    want = c.forward()
+    within(want, *layer_reference(c), "out")
+    assert int(c.err.item()) == 0
+    for n in (2, 5):
+        if not few(c.shape):
+            break
+        assert torch.equal(c.forward(moe.make_shape(T, H, E, k, I, 1, n, "bf16")), want), n
+    c.idx[0, 0], c.idx[T - 1, k - 1] = -3, E
+    if T == 1 and k == 1:
+        assert bool((c.forward() == 0).all())
+    within(c.forward(), *layer_reference(c), "out")
+    assert int(c.err.item()) == (1 if T * k == 1 else 2)
 
 
 # row counts on both sides of every tile limit, an expert without rows, slots that are dropped
