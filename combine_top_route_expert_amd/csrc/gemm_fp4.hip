@@ -69,35 +69,6 @@ __device__ __forceinline__ i32x12 both_parts(const i32x4 (&a)[3]) {
       10, 11);
 }
 
-template <bool kBuf>
-struct Source {  // what to copy from: a descriptor with offsets, or addresses
-  rsrc_t desc;
-  const char* base;
-  __device__ __forceinline__ void init(const char* p) {
-    base = p;
-    if constexpr (kBuf) desc = raw_rsrc(p);
-  }
-  typedef std::conditional_t<kBuf, uint32_t, int64_t> offset;
-  template <bool kNt>
-  __device__ __forceinline__ void load16(char* dst, offset off, int koff) const {
-    if constexpr (kBuf) {
-      if constexpr (kNt)
-        buffer_load_lds16_nt(desc, dst, off, koff);
-      else
-        buffer_load_lds16(desc, dst, off, koff);
-    } else {
-      __builtin_amdgcn_global_load_lds((const void*)(base + off + koff), (lds_void*)dst, 16, 0,
-                                       kNt ? 2 : 0);
-    }
-  }
-  __device__ __forceinline__ void load4(char* dst, offset off, int koff) const {
-    if constexpr (kBuf)
-      buffer_load_lds4(desc, dst, off, koff);
-    else
-      __builtin_amdgcn_global_load_lds((const void*)(base + off + koff), (lds_void*)dst, 4, 0, 0);
-  }
-};
-
 // Row block of the packed weights behind block j of a tile's NB (FN to a wave): gate_up, a
 // wave's first half gate and the matching up rows after; clamped, since what lies past C
 // is never stored.
@@ -115,209 +86,182 @@ __device__ __forceinline__ int weight_block(const MxArgs& g, int nt, int nb, int
 }
 
 // ---------------------------------------------------------------- many rows an expert
-// A workgroup of four waves, one for each SIMD with all its 512 registers, computes 64 F rows
-// by 256 columns, a wave half of either (F x 4 blocks of 32 x 32).  Wave tiles that large
-// read the least from LDS, which with a product at four times the bf16 rate is as scarce as
-// the matrix pipe: at F = 4 a stage's 32 matrix instructions of a wave take 1024 cycles, the
-// four waves' reads 512 and the copies' writes 264.
-constexpr int kWideSmem = 160 * 1024;
-constexpr int kWaves = 4, kWideFN = 4, kWideNB = 8;  // waves; column blocks of a wave, of a tile
-constexpr int kScaleUnits = 4;  // dwords of a weight row's scales in LDS (each of four stages)
+// A workgroup of four waves, one for each SIMD with all its 512 registers, computes up to 128
+// rows by 512 columns, a wave all the rows of its own 128 columns (R x 4 blocks of 32 x 32).
+// The weights, which no other wave uses, go from memory straight into registers, three stages
+// ahead; the rows go through LDS, a unit of four stages at a time in two buffers.
+constexpr int kWaves = 4, kWideFN = 4, kUnit = 4;  // waves; column blocks of a wave; stages of a unit
+constexpr int kWideRows = 128;
 
-template <int F>
-struct WideStage {
-  static constexpr int kBlocks = 2 * F;  // row blocks
-  static constexpr int kAtScales = kBlocks * kMxBlockBytes;          // of the rows
-  static constexpr int kAtB = kAtScales + kBlocks * kMxScaleBytes;   // weight blocks
-  static constexpr int kBytes = kAtB + kWideNB * kFp4BlockBytes;
-  static constexpr int kRoom = kWideSmem - kScaleUnits * kWideNB * kFp4ScaleBytes;
-  // stages in LDS: as many as fit, and no more than the scale units serve
-  static constexpr int kCount = kRoom / kBytes < 8 ? kRoom / kBytes : 8;
-  static constexpr int kCopies = (kBlocks * 3 + kWaves - 1) / kWaves;  // of A's values, a wave
-  static constexpr int kScales = (kBlocks + kWaves - 1) / kWaves;      // of their scales
-  static constexpr int kB = kWideNB / kWaves;
-  static constexpr int kPerStage = kCopies + kScales + kB;
+template <int R>
+struct WideUnit {
+  static constexpr int kAtScales = R * kUnit * kMxBlockBytes;
+  static constexpr int kBytes = kAtScales + R * kUnit / 2 * kMxScaleBytes;
+  static constexpr int kValues = R * kUnit * 3 / kWaves;               // a wave's copies
+  static constexpr int kScales = (R * kUnit / 2 + kWaves - 1) / kWaves;
+  static constexpr int kCopies = kValues + kScales;
 };
 
-// The copies of a workgroup's stages.  Every wave issues the same number: those past the
-// last repeat it, and row blocks past the expert's last repeat that one.  The rows' scales
-// (two stages' in a dword) are copied with every stage, so that all are alike.
-template <bool kGateUp, int F, bool kBuf>
-struct WideLoader {
-  using S = WideStage<F>;
-  typedef typename Source<kBuf>::offset offset;
-  Source<kBuf> a, as, b, bs;
-  offset a_off[S::kCopies], as_off[S::kScales], b_off[S::kB], bs_off[S::kB];
-  int wave;
-  char *smem, *scales;
-
-  __device__ __forceinline__ int copy_of(int t) const {
-    const int i = t * kWaves + wave, last = S::kBlocks * 3 - 1;
-    return i < last ? i : last;
-  }
-  __device__ __forceinline__ int scale_of(int t) const {
-    const int i = t * kWaves + wave, last = S::kBlocks - 1;
-    return i < last ? i : last;
-  }
-  __device__ __forceinline__ void init(const MxArgs& g, const TileRows& tr, int nt, int lane,
-                                       int wave_, char* smem_) {
-    wave = wave_;
-    scales = smem_;
-    smem = smem_ + kScaleUnits * kWideNB * kFp4ScaleBytes;
-    const int e = __builtin_amdgcn_readfirstlane(tr.e);
-    const int64_t rb = mx_row_block(tr, tr.v0);
-    const int pairs = (g.blocks + 1) / 2, last = (tr.rows - 1) / 32;
-    a.init(g.a.values + rb * g.blocks * kMxBlockBytes);
-    as.init(g.a.scales + rb * pairs * kMxScaleBytes);
-    b.init(g.b + (int64_t)e * g.b_expert);
-    bs.init(g.bs + (int64_t)e * g.bs_expert);
-#pragma unroll
-    for (int t = 0; t < S::kCopies; ++t) {
-      const int block = copy_of(t) / 3, third = copy_of(t) % 3;
-      a_off[t] = (offset)((int64_t)(block < last ? block : last) * g.blocks * kMxBlockBytes +
-                          third * 1024 + lane * 16);
-    }
-#pragma unroll
-    for (int t = 0; t < S::kScales; ++t) {
-      const int block = scale_of(t);
-      as_off[t] = (offset)((int64_t)(block < last ? block : last) * pairs * kMxScaleBytes + lane * 4);
-    }
-#pragma unroll
-    for (int t = 0; t < S::kB; ++t) {
-      const int rb = weight_block<kGateUp, kWideFN>(g, nt, kWideNB, t * kWaves + wave);
-      b_off[t] = (offset)((int64_t)rb * g.blocks * kFp4BlockBytes + lane * 16);
-      bs_off[t] = (offset)((int64_t)rb * g.quads * kFp4ScaleBytes + lane * 4);
-    }
-  }
-  // Copy q of stage st into ring slot `slot`.
-  template <bool kNt>
-  __device__ __forceinline__ void issue(int st, int slot, int q) const {
-    char* base = smem + slot * S::kBytes;
-    if (q < S::kB)
-      b.template load16<kNt>(base + S::kAtB + (q * kWaves + wave) * kFp4BlockBytes, b_off[q],
-                             st * kFp4BlockBytes);
-    else if (q < S::kB + S::kScales)
-      as.load4(base + S::kAtScales + scale_of(q - S::kB) * kMxScaleBytes, as_off[q - S::kB],
-               (st >> 1) * kMxScaleBytes);
-    else
-      a.template load16<false>(base + copy_of(q - S::kB - S::kScales) * 1024,
-                               a_off[q - S::kB - S::kScales], st * kMxBlockBytes);
-  }
-  // The weights' scales of stages 4 u .. 4 u + 3.
-  __device__ __forceinline__ void issue_scales(int u) const {
-#pragma unroll
-    for (int t = 0; t < S::kB; ++t)
-      bs.load4(scales + ((u & (kScaleUnits - 1)) * kWideNB + t * kWaves + wave) * kFp4ScaleBytes,
-               bs_off[t], u * kFp4ScaleBytes);
-  }
-};
-
-// The K loop of a wave.  A step multiplies a stage whose operands are in registers, while it
-// reads those of the next from LDS and copies a later one into the slot that the barrier at
-// its start has freed (every wave's reads of it are complete); a copy, which holds its wave for
-// some sixteen cycles, after each few matrix instructions.
-template <int F, bool kNt, class Loader>
-__device__ __forceinline__ void wide_k_loop(f32x16 (&acc)[F][kWideFN], const Loader& ld, int ST,
-                                            int lane, int wm, int wn) {
-  using S = WideStage<F>;
-  constexpr int FN = kWideFN, N = S::kCount;
-  struct Operands {
-    i32x4 a[F][3];
-    i32x4 b[FN];
-    uint32_t as[F], bs[FN];
-  };
-  Operands op[2];
-  // read q of stage st's operands
-  constexpr int kReads = 4 * F + 2 * FN;
-  auto read = [&](Operands& o, int st, int slot, int q) __attribute__((always_inline)) {
-    const char* base = ld.smem + slot * S::kBytes;
-    if (q < 2 * FN) {
-      const int j = q >> 1;
-      if (q & 1) {
-        const char* sc = ld.scales + ((st >> 2) & (kScaleUnits - 1)) * kWideNB * kFp4ScaleBytes;
-        o.bs[j] = *(const uint32_t*)(sc + (wn * FN + j) * kFp4ScaleBytes + lane * 4);
-      } else {
-        o.b[j] = *(const i32x4*)(base + S::kAtB + (wn * FN + j) * kFp4BlockBytes + lane * 16);
-      }
+// The K loop of a wave.
+template <bool kGateUp, int R, bool kNt>
+__device__ __forceinline__ void wide_k_loop(f32x16 (&acc)[R][kWideFN], const MxArgs& g,
+                                            const TileRows& tr, int nt, int lane, int wave,
+                                            char* smem) {
+  using U = WideUnit<R>;
+  constexpr int FN = kWideFN;
+  const int e = __builtin_amdgcn_readfirstlane(tr.e);
+  const int KB = g.blocks, units = g.quads, pairs = (KB + 1) / 2, full = KB / kUnit;
+  const int64_t rb0 = mx_row_block(tr, tr.v0);
+  const char* av = g.a.values + rb0 * KB * kMxBlockBytes + lane * 16;
+  const char* as = g.a.scales + rb0 * pairs * kMxScaleBytes + lane * 4;
+  // Copy q of unit u: kilobyte q of the values, then 256 bytes of scales; blocks past the last
+  // of K repeat that, and copies past a unit's last repeat it.
+  auto copy = [&](int u, int t) __attribute__((always_inline)) {
+    char* base = smem + (u & 1) * U::kBytes;
+    if (t < U::kValues) {
+      const int q = t * kWaves + wave, i = q / (3 * kUnit), k = kUnit * u + q % (3 * kUnit) / 3;
+      __builtin_amdgcn_global_load_lds(
+          (const void*)(av + ((int64_t)i * KB + (k < KB ? k : KB - 1)) * kMxBlockBytes + q % 3 * 1024),
+          (lds_void*)(base + q * 1024), 16, 0, 0);
     } else {
-      const int i = (q - 2 * FN) >> 2, third = (q - 2 * FN) & 3;
-      if (third == 3)
-        o.as[i] = *(const uint32_t*)(base + S::kAtScales + (wm * F + i) * kMxScaleBytes + lane * 4);
-      else
-        o.a[i][third] =
-            *(const i32x4*)(base + (wm * F + i) * kMxBlockBytes + third * 1024 + lane * 16);
+      int q = (t - U::kValues) * kWaves + wave;
+      q = q < R * kUnit / 2 ? q : R * kUnit / 2 - 1;
+      const int i = q / (kUnit / 2), pair = kUnit / 2 * u + q % (kUnit / 2);
+      __builtin_amdgcn_global_load_lds(
+          (const void*)(as + ((int64_t)i * pairs + (pair < pairs ? pair : pairs - 1)) * kMxScaleBytes),
+          (lds_void*)(base + U::kAtScales + q * kMxScaleBytes), 4, 0, 0);
     }
   };
-  // the prologue's scales first: a unit lands before the first stage that needs it
+  const i32x4* b[FN];
+  const uint32_t* bs[FN];
 #pragma unroll
-  for (int s = 0; s < N; ++s) {
-    if (s >= ST) break;
-    if ((s & 3) == 0) ld.issue_scales(s >> 2);
-#pragma unroll
-    for (int q = 0; q < S::kPerStage; ++q) ld.template issue<kNt>(s, s, q);
+  for (int j = 0; j < FN; ++j) {
+    const int rb = weight_block<kGateUp, FN>(g, nt, kWaves * FN, wave * FN + j);
+    b[j] = (const i32x4*)(g.b + e * g.b_expert + (int64_t)rb * KB * kFp4BlockBytes) + lane;
+    bs[j] = (const uint32_t*)(g.bs + e * g.bs_expert + (int64_t)rb * units * kFp4ScaleBytes) + lane;
   }
-  // (of N stages' copies; fewer stages wait for all)
-  if (ST >= N)
-    __builtin_amdgcn_s_waitcnt(wait_vm((N - 1) * S::kPerStage));
+  i32x4 w[kUnit][FN];
+  uint32_t sc[FN], sn[FN];
+  struct Row {
+    i32x4 thirds[3];
+    uint32_t s;
+  };
+  Row row[2];
+  auto load = [&](int k, int j, i32x4& to) __attribute__((always_inline)) {
+    const i32x4* from = b[j] + (int64_t)k * (kFp4BlockBytes / 16);
+    if constexpr (kNt)
+      to = __builtin_nontemporal_load(from);
+    else
+      to = *from;
+  };
+  auto read = [&](Row& to, int u, int k, int i, int t) __attribute__((always_inline)) {
+    const char* base = smem + (u & 1) * U::kBytes;
+    if (t < 3)
+      to.thirds[t] = *(const i32x4*)(base + (i * kUnit + k) * kMxBlockBytes + t * 1024 + lane * 16);
+    else
+      to.s = *(const uint32_t*)(base + U::kAtScales + (i * (kUnit / 2) + k / 2) * kMxScaleBytes +
+                                lane * 4);
+  };
+#pragma unroll
+  for (int t = 0; t < U::kCopies; ++t) copy(0, t);
+  __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+  for (int j = 0; j < FN; ++j) sn[j] = sc[j] = bs[j][0];
+#pragma unroll
+  for (int k = 0; k < kUnit - 1; ++k)
+    if (k < KB) {
+#pragma unroll
+      for (int j = 0; j < FN; ++j) load(k, j, w[k][j]);
+    }
+  __builtin_amdgcn_sched_barrier(0);
+  // (the copies have landed: at most what came after them is pending)
+  if (KB >= kUnit - 1)
+    __builtin_amdgcn_s_waitcnt(wait_vm((kUnit - 1) * FN));
   else
     __builtin_amdgcn_s_waitcnt(wait_vm(0));
-  __builtin_amdgcn_s_waitcnt(kWaitLgkm0);
   __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
 #pragma unroll
-  for (int q = 0; q < kReads; ++q) read(op[0], 0, 0, q);
-  int slot = 0;
-  auto step = [&](int st, const Operands& o, Operands& next) __attribute__((always_inline)) {
-    const int after = slot + 1 == N ? 0 : slot + 1;
-    const bool again = st + 1 < ST, more = st + N < ST;
-    if (again) {
-      // stage st + 1 has landed once only the copies of the N - 2 after it may be pending
-      // (scales not counted: a few copies more than necessary have landed)
-      if (st + N - 1 < ST)
-        __builtin_amdgcn_s_waitcnt(wait_vm((N - 2) * S::kPerStage));
-      else
-        __builtin_amdgcn_s_waitcnt(wait_vm(0));
-      __builtin_amdgcn_s_waitcnt(kWaitLgkm0);
-      __builtin_amdgcn_s_barrier();
+  for (int t = 0; t < 4; ++t) read(row[0], 0, 0, 0, t);
+
+  // Stage k of unit u.  kFull: unit u + 1 is a whole one.
+  auto stage = [&](int u, auto k_tag, auto full_tag) __attribute__((always_inline)) {
+    constexpr int k = decltype(k_tag)::value;
+    constexpr bool kFull = decltype(full_tag)::value;
+    const bool next = kFull || u + 1 < units;              // there is a unit u + 1
+    const bool ahead = kFull || kUnit * u + k + kUnit - 1 < KB;  // the stage to load
+    if (k == 0 && next) {
+#pragma unroll
+      for (int j = 0; j < FN; ++j) sn[j] = bs[j][(u + 1) * (kFp4ScaleBytes / 4)];
     }
-    // the bytes of the scales that this stage uses, to the lowest place
-    uint32_t as[F], bs[FN];
 #pragma unroll
-    for (int i = 0; i < F; ++i) as[i] = o.as[i] >> (16 * (st & 1));
-#pragma unroll
-    for (int j = 0; j < FN; ++j) bs[j] = o.bs[j] >> (8 * (st & 3));
-    __builtin_amdgcn_sched_barrier(0);
-    // reads and copies in turn, spread over the stage's matrix instructions
-    constexpr int kMma = 2 * F * FN, kOps = kReads + S::kPerStage;
-#pragma unroll
-    for (int m = 0; m < kMma; ++m) {
-      const int i = m / (2 * FN), j = m % FN;
-      const i32x12 rows = both_parts(o.a[i]);
-      acc[i][j] = m / FN & 1 ? mx_mma<1, 0, 0>(o.b[j], bs[j], rows, as[i], acc[i][j])
-                             : mx_mma<0, 0, 0>(o.b[j], bs[j], rows, as[i], acc[i][j]);
-      // (the compiler moves matrix instructions down past branches, and so past the copies
-      // and the barrier that they are to cover, unless their results are named before)
-      asm volatile("" : "+a"(acc[i][j]));
-      __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-      for (int t = m * kOps / kMma; t < (m + 1) * kOps / kMma; ++t) {
-        const int copies = t * S::kPerStage / kOps, after_t = (t + 1) * S::kPerStage / kOps;
-        if (after_t > copies) {
-          if (more) ld.template issue<kNt>(st + N, slot, copies);
-        } else if (again) {
-          read(next, st + 1, after, t - copies);
-        }
+    for (int i = 0; i < R; ++i) {
+      const bool last = k == kUnit - 1 && i == R - 1;
+      if (last && next) {
+        // every wave has read this unit; the copies of the next, issued in the first stage, have
+        // landed once at most the loads issued after that stage are pending
+        constexpr int kLoads = (R > 1 ? kUnit - 1 : kUnit - 2) * FN;
+        __builtin_amdgcn_s_waitcnt(kFull ? wait_vm(kLoads) : wait_vm(0));
+        __builtin_amdgcn_s_waitcnt(kWaitLgkm0);
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
       }
+      const Row& now = row[(k * R + i) & 1];
+      Row& then = row[(k * R + i + 1) & 1];
+      const i32x12 rows = both_parts(now.thirds);
       __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int m = 0; m < 2 * FN; ++m) {
+        const int j = m % FN;
+        acc[i][j] = m < FN ? mx_mma<0, k, 2 * (k & 1)>(w[k][j], sc[j], rows, now.s, acc[i][j])
+                           : mx_mma<1, k, 2 * (k & 1)>(w[k][j], sc[j], rows, now.s, acc[i][j]);
+        // (the compiler moves matrix instructions down past branches, and so past the copies
+        // and the barrier that they are to cover, unless their results are named before)
+        asm volatile("" : "+a"(acc[i][j]));
+        __builtin_amdgcn_sched_barrier(0);
+        if (m < 4) {
+          if (i < R - 1)
+            read(then, u, k, i + 1, m);
+          else if (k < kUnit - 1)
+            read(then, u, k + 1, 0, m);  // (of a stage past the last, unused)
+          else if (next)
+            read(then, u + 1, 0, 0, m);
+        }
+        if (i == 0 && m >= 2 * FN - FN && ahead)
+          load(kUnit * u + k + kUnit - 1, m - FN, w[(k + kUnit - 1) % kUnit][m - FN]);
+        if (k == 0 && next) {
+          constexpr int kMma = 2 * FN * R;
+          const int at = i * 2 * FN + m;
+#pragma unroll
+          for (int t = at * U::kCopies / kMma; t < (at + 1) * U::kCopies / kMma; ++t) copy(u + 1, t);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
     }
-    if (more && ((st + N) & 3) == 0) ld.issue_scales((st + N) >> 2);
-    slot = after;
   };
-  int st = 0;
-  for (; st + 1 < ST; st += 2) {
-    step(st, op[0], op[1]);
-    step(st + 1, op[1], op[0]);
+  const std::integral_constant<int, 0> k0{};
+  const std::integral_constant<int, 1> k1{};
+  const std::integral_constant<int, 2> k2{};
+  const std::integral_constant<int, 3> k3{};
+  const std::true_type whole{};
+  const std::false_type part{};
+  int u = 0;
+  for (; u + 1 < full; ++u) {
+    stage(u, k0, whole);
+    stage(u, k1, whole);
+    stage(u, k2, whole);
+    stage(u, k3, whole);
+#pragma unroll
+    for (int j = 0; j < FN; ++j) sc[j] = sn[j];
   }
-  if (st < ST) step(st, op[0], op[1]);
+  for (; u < units; ++u) {
+    stage(u, k0, part);
+    if (kUnit * u + 1 < KB) stage(u, k1, part);
+    if (kUnit * u + 2 < KB) stage(u, k2, part);
+    if (kUnit * u + 3 < KB) stage(u, k3, part);
+#pragma unroll
+    for (int j = 0; j < FN; ++j) sc[j] = sn[j];
+  }
 }
 
 // act of 32 rows by 32 columns of two row blocks, from the accumulators of gate and up
@@ -436,13 +380,15 @@ __device__ __forceinline__ void store_out(const MxArgs& a, const f32x16 (&acc)[F
     __builtin_nontemporal_store(*(const u32x4*)(smem + at(r, c)),
                                 (u32x4*)((part ? y1 : y0) + ((int64_t)row * a.ncols + col0 + c) * 2));
   }
+  constexpr int kDwords = BN / 256;  // of a tile row's scales
   const int64_t row_scales = mx_out_scales(a.ncols);
-  static_assert(BN == 256, "a dword of scales a row");
-  for (int r = threadIdx.x; r < tr.rows; r += NT) {
+  for (int i = threadIdx.x; i < tr.rows * kDwords; i += NT) {
+    const int r = i / kDwords, d = nt * kDwords + i % kDwords;
+    if (d * 256 >= a.ncols) continue;
     int part = 0, row = tr.joint_row(tr.v0 + r);
     if (a.c_split) row = tr.split_row(tr.v0 + r, &part);
     char *s0 = a.y[0].scales, *s1 = a.y[1].scales;
-    *(uint32_t*)((part ? s1 : s0) + row * row_scales + nt * 4) = *(const uint32_t*)(scales + r * 4);
+    *(uint32_t*)((part ? s1 : s0) + row * row_scales + d * 4) = *(const uint32_t*)(scales + i * 4);
   }
 }
 
@@ -472,74 +418,70 @@ __device__ __forceinline__ void store_out_rows(const MxArgs& a, const f32x16 (&a
   }
 }
 
-template <bool kGateUp, bool kBuf>
+template <bool kGateUp>
 __global__ void __launch_bounds__(64 * kWaves, 1) grouped_gemm_mx(MxArgs a) {
-  constexpr int BM = 256, BN = 256, FN = kWideFN;
-  static_assert(BM * BN * 2 + BM * (BN / 64) <= kWideSmem, "C tile fits the stage buffers");
-  __shared__ __attribute__((aligned(1024))) char smem[kWideSmem];
+  constexpr int FN = kWideFN, BN = 32 * FN * kWaves, NT = 64 * kWaves;
+  constexpr int kTile = kGateUp ? 0 : kWideRows * (BN * 2 + BN / 64), kUnits = 2 * WideUnit<4>::kBytes;
+  __shared__ __attribute__((aligned(1024))) char smem[kUnits > kTile ? kUnits : kTile];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int wm = wave >> 1, wn = wave & 1;
   MTileMap tm;
-  tm.build(a.off0, a.off1, a.E, BM, BM);
+  tm.build(a.off0, a.off1, a.E, kWideRows, kWideRows);
   int mt, nt;
   if (!xcd_tile_at(tm, a.n_tiles, blockIdx.x & 7, blockIdx.x >> 3,
                    (32 + a.n_tiles - 1) / a.n_tiles, &mt, &nt))
     return;
-  const TileRows tr = tm.locate(a.off0, a.off1, BM, mt);
-  auto run = [&](auto f_tag, auto nt_tag) __attribute__((always_inline)) {
-    constexpr int F = decltype(f_tag)::value;
-    f32x16 acc[F][FN];
+  const TileRows tr = tm.locate(a.off0, a.off1, kWideRows, mt);
+  auto run = [&](auto r_tag, auto once_tag) __attribute__((always_inline)) {
+    constexpr int R = decltype(r_tag)::value;
+    f32x16 acc[R][FN];
 #pragma unroll
-    for (int i = 0; i < F; ++i)
+    for (int i = 0; i < R; ++i)
 #pragma unroll
       for (int j = 0; j < FN; ++j) acc[i][j] = f32x16{};
-    WideLoader<kGateUp, F, kBuf> ld;
-    ld.init(a, tr, nt, lane, wave, smem);
-    wide_k_loop<F, decltype(nt_tag)::value>(acc, ld, a.blocks, lane, wm, wn);
+    wide_k_loop<kGateUp, R, decltype(once_tag)::value>(acc, a, tr, nt, lane, wave, smem);
     if constexpr (kGateUp) {
-      store_act<F, FN>(a, acc, tr, wm * F * 32, nt * (kWideNB / 2) + wn * (FN / 2), lane);
+      store_act<R, FN>(a, acc, tr, 0, (nt * kWaves + wave) * (FN / 2), lane);
     } else {
-      __syncthreads();  // every wave is done with the stage buffers
-      store_out<F, FN, 64 * F, BN, 64 * kWaves>(a, acc, tr, nt, wm * F * 32, wn, lane, smem);
+      __syncthreads();  // every wave is done with the rows
+      store_out<R, FN, 32 * R, BN, NT>(a, acc, tr, nt, 0, wave, lane, smem);
     }
   };
-  const std::integral_constant<int, 1> f1{};
-  const std::integral_constant<int, 2> f2{};
-  const std::integral_constant<int, 3> f3{};
-  const std::integral_constant<int, 4> f4{};
+  const std::integral_constant<int, 1> r1{};
+  const std::integral_constant<int, 2> r2{};
+  const std::integral_constant<int, 3> r3{};
+  const std::integral_constant<int, 4> r4{};
   // the weights of a tile that holds all of its expert's rows are read by no other tile
   const std::true_type once{};
   const std::false_type shared{};
   if (tr.single) {
-    if (tr.rows <= 64)
-      run(f1, once);
-    else if (tr.rows <= 128)
-      run(f2, once);
-    else if (tr.rows <= 192)
-      run(f3, once);
+    if (tr.rows <= 32)
+      run(r1, once);
+    else if (tr.rows <= 64)
+      run(r2, once);
+    else if (tr.rows <= 96)
+      run(r3, once);
     else
-      run(f4, once);
+      run(r4, once);
   } else {
-    if (tr.rows <= 64)
-      run(f1, shared);
-    else if (tr.rows <= 128)
-      run(f2, shared);
-    else if (tr.rows <= 192)
-      run(f3, shared);
+    if (tr.rows <= 32)
+      run(r1, shared);
+    else if (tr.rows <= 64)
+      run(r2, shared);
+    else if (tr.rows <= 96)
+      run(r3, shared);
     else
-      run(f4, shared);
+      run(r4, shared);
   }
 }
 
-template <bool kGateUp, bool kBuf>
+template <bool kGateUp>
 hipError_t launch_wide(MxArgs a, int64_t rows_bound, hipStream_t st) {
-  constexpr int cols = kGateUp ? 128 : 256;
+  constexpr int cols = kWaves * kWideFN * (kGateUp ? 16 : 32);
   a.n_tiles = (a.ncols + cols - 1) / cols;
-  const int64_t grid = xcd_grid(m_tiles_bound(rows_bound, a.E, 256), a.n_tiles);
+  const int64_t grid = xcd_grid(m_tiles_bound(rows_bound, a.E, kWideRows), a.n_tiles);
   if (grid <= 0) return hipSuccess;
   if (grid > 0x7fffffff / (64 * kWaves)) return hipErrorInvalidConfiguration;
-  hipLaunchKernelGGL((grouped_gemm_mx<kGateUp, kBuf>), dim3((unsigned)grid), dim3(64 * kWaves), 0,
-                     st, a);
+  hipLaunchKernelGGL(grouped_gemm_mx<kGateUp>, dim3((unsigned)grid), dim3(64 * kWaves), 0, st, a);
   return hipGetLastError();
 }
 
@@ -552,7 +494,7 @@ hipError_t launch_wide(MxArgs a, int64_t rows_bound, hipStream_t st) {
 // reads 3.4 GB in 590 us and down 1.7 in 285, 5.9 and 6.1 TB/s (a plain read of such weights:
 // 6.8).  Loads that leave the weights in the caches cost 6% more; two or six waves a
 // workgroup 0 and 19%.
-constexpr int kStreamWaves = 4, kUnit = 4;
+constexpr int kStreamWaves = 4;
 // Rows an expert, on average, up to which these products are taken.  The layer, these and the
 // wide ones: 2 rows 0.89 and 1.21 ms, 8 rows 1.07 and 1.42, 16 rows 1.13 and 1.52, 32 rows
 // 1.63 and 1.55; of a layer with H = 2048, I = 1024, 64 experts 32 rows 0.085 and 0.097.
@@ -707,11 +649,7 @@ template <bool kGateUp>
 hipError_t launch(const MxArgs& a, int64_t rows_bound, hipStream_t st) {
   if (rows_bound <= 0) return hipSuccess;
   if (rows_bound <= (int64_t)kStreamRows * a.E) return launch_stream<kGateUp>(a, rows_bound, st);
-  // descriptor loads take 32-bit offsets from a tile's first row block and an expert's weights
-  const uint64_t lim = (uint64_t)1 << 32;
-  const bool buf = (uint64_t)8 * a.blocks * kMxBlockBytes < lim && (uint64_t)a.b_expert < lim;
-  return buf ? launch_wide<kGateUp, true>(a, rows_bound, st)
-             : launch_wide<kGateUp, false>(a, rows_bound, st);
+  return launch_wide<kGateUp>(a, rows_bound, st);
 }
 
 // K columns; `rows` rows of an expert's weights.
