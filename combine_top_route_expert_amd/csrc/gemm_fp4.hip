@@ -103,7 +103,7 @@ struct WideUnit {
 };
 
 // The K loop of a wave.
-template <bool kGateUp, int R, bool kNt>
+template <bool kGateUp, int R>
 __device__ __forceinline__ void wide_k_loop(f32x16 (&acc)[R][kWideFN], const MxArgs& g,
                                             const TileRows& tr, int nt, int lane, int wave,
                                             char* smem) {
@@ -148,11 +148,7 @@ __device__ __forceinline__ void wide_k_loop(f32x16 (&acc)[R][kWideFN], const MxA
   };
   Row row[2];
   auto load = [&](int k, int j, i32x4& to) __attribute__((always_inline)) {
-    const i32x4* from = b[j] + (int64_t)k * (kFp4BlockBytes / 16);
-    if constexpr (kNt)
-      to = __builtin_nontemporal_load(from);
-    else
-      to = *from;
+    to = b[j][(int64_t)k * (kFp4BlockBytes / 16)];
   };
   auto read = [&](Row& to, int u, int k, int i, int t) __attribute__((always_inline)) {
     const char* base = smem + (u & 1) * U::kBytes;
@@ -431,14 +427,14 @@ __global__ void __launch_bounds__(64 * kWaves, 1) grouped_gemm_mx(MxArgs a) {
                    (32 + a.n_tiles - 1) / a.n_tiles, &mt, &nt))
     return;
   const TileRows tr = tm.locate(a.off0, a.off1, kWideRows, mt);
-  auto run = [&](auto r_tag, auto once_tag) __attribute__((always_inline)) {
+  auto run = [&](auto r_tag) __attribute__((always_inline)) {
     constexpr int R = decltype(r_tag)::value;
     f32x16 acc[R][FN];
 #pragma unroll
     for (int i = 0; i < R; ++i)
 #pragma unroll
       for (int j = 0; j < FN; ++j) acc[i][j] = f32x16{};
-    wide_k_loop<kGateUp, R, decltype(once_tag)::value>(acc, a, tr, nt, lane, wave, smem);
+    wide_k_loop<kGateUp, R>(acc, a, tr, nt, lane, wave, smem);
     if constexpr (kGateUp) {
       store_act<R, FN>(a, acc, tr, 0, (nt * kWaves + wave) * (FN / 2), lane);
     } else {
@@ -446,32 +442,14 @@ __global__ void __launch_bounds__(64 * kWaves, 1) grouped_gemm_mx(MxArgs a) {
       store_out<R, FN, 32 * R, BN, NT>(a, acc, tr, nt, 0, wave, lane, smem);
     }
   };
-  const std::integral_constant<int, 1> r1{};
-  const std::integral_constant<int, 2> r2{};
-  const std::integral_constant<int, 3> r3{};
-  const std::integral_constant<int, 4> r4{};
-  // the weights of a tile that holds all of its expert's rows are read by no other tile
-  const std::true_type once{};
-  const std::false_type shared{};
-  if (tr.single) {
-    if (tr.rows <= 32)
-      run(r1, once);
-    else if (tr.rows <= 64)
-      run(r2, once);
-    else if (tr.rows <= 96)
-      run(r3, once);
-    else
-      run(r4, once);
-  } else {
-    if (tr.rows <= 32)
-      run(r1, shared);
-    else if (tr.rows <= 64)
-      run(r2, shared);
-    else if (tr.rows <= 96)
-      run(r3, shared);
-    else
-      run(r4, shared);
-  }
+  if (tr.rows <= 32)
+    run(std::integral_constant<int, 1>{});
+  else if (tr.rows <= 64)
+    run(std::integral_constant<int, 2>{});
+  else if (tr.rows <= 96)
+    run(std::integral_constant<int, 3>{});
+  else
+    run(std::integral_constant<int, 4>{});
 }
 
 template <bool kGateUp>
