@@ -6,13 +6,12 @@
 // v_mfma_scale_f32_32x32x64_f8f6f4 multiplies 32 x 64 E2M1 weights by 32 x 64 E2M3 values
 // with a power of two for each 32 of either side, in the 32 cycles in which the bf16
 // instruction multiplies a quarter of that; the two parts of the rows make it half the
-// matrix time of bf16.  Weights go from memory to the instruction as they lie: lane
-// 32 h + r holds the 16 bytes of columns 32 h .. of row r and a dword with its scales of
+// matrix time of bf16.  Weights go from memory to the instruction as they lie, in one load:
+// lane 32 h + r holds the 16 bytes of columns 32 h .. of row r and a dword with its scales of
 // four blocks, of which the instruction picks a byte.  (Converted to bf16 in registers
 // instead, with bf16 rows and instructions: 2.05 ms for gate_up of 4096 tokens on 256
-// experts, H = 7168, I = 2048; 64 tokens 0.65 ms, 0.1 of it the conversions.)  Sums are
-// fp32, over K in ascending order, part h before part l in each 64 columns, whatever the
-// tile: every variant gives the same bits.
+// experts, H = 7168, I = 2048, instead of 1.24.)  Sums are fp32, over K in ascending order,
+// part h before part l in each 64 columns, whatever the tile: both forms give the same bits.
 #include <algorithm>
 #include <type_traits>
 
@@ -89,8 +88,27 @@ __device__ __forceinline__ int weight_block(const MxArgs& g, int nt, int nb, int
 // A workgroup of four waves, one for each SIMD with all its 512 registers, computes up to 128
 // rows by 512 columns, a wave all the rows of its own 128 columns (R x 4 blocks of 32 x 32).
 // The weights, which no other wave uses, go from memory straight into registers, three stages
-// ahead; the rows go through LDS, a unit of four stages at a time in two buffers.
-constexpr int kWaves = 4, kWideFN = 4, kUnit = 4;  // waves; column blocks of a wave; stages of a unit
+// (of 64 columns of K) ahead; the rows go through LDS, a unit of four stages at a time in
+// two buffers, and a row block's operands are read while the one before is multiplied.
+//
+// Why this shape: a column of A is 12 bits and one of the weights 4, so that of tiles of 65536
+// sums, all that a CU's registers hold, the one of 128 x 512 copies less than 256 x 256 (28 KB
+// a stage against 32); and with the weights past LDS a stage's 1024 cycles of matrix
+// instructions go with 48 KB of reads and 12 KB of writes there.  256 x 256 with both sides in
+// LDS, two by two waves (64 and 32 KB) took 2000 cycles a stage, about the sum of what its reads
+// and its copies cost: the layer of 4096 tokens with 8 of 256 experts of H = 7168, I = 2048 2.67
+// ms instead of 2.36, of 1024 tokens 1.53 instead of 1.24, of 16384 tokens with 8 of 128 experts
+// of H = 2048, I = 768 1.26 instead of 1.13 to 1.21.
+//
+// The first of these: gate_up 1.21 ms and down 0.80, 1.43 PFLOP/s, 4.9 TB/s of weights.  Neither
+// the matrix pipe (0.64 and 0.32 ms at the 6 PF/s that the instruction reaches, power being what
+// limits it) nor memory (0.59 and 0.29) is full: tiles whose last row block holds a few rows,
+// prologues and epilogues with one workgroup on a CU, and LDS take the rest.  Without effect:
+// seven stages ahead for up to 64 rows (0 to 5% slower); twice the row tiles to a group of an
+// XCD's workgroups; experts in order instead of large ones first (0 to 2% slower); weights that
+// leave no trace in the caches (1% slower, 7% where the layer fits them).
+constexpr int kWaves = 4, kWideFN = 4;  // waves; column blocks of a wave
+constexpr int kUnit = 4;                // stages of a unit
 constexpr int kWideRows = 128;
 
 template <int R>
@@ -473,9 +491,10 @@ hipError_t launch_wide(MxArgs a, int64_t rows_bound, hipStream_t st) {
 // 6.8).  Loads that leave the weights in the caches cost 6% more; two or six waves a
 // workgroup 0 and 19%.
 constexpr int kStreamWaves = 4;
-// Rows an expert, on average, up to which these products are taken.  The layer, these and the
-// wide ones: 2 rows 0.89 and 1.21 ms, 8 rows 1.07 and 1.42, 16 rows 1.13 and 1.52, 32 rows
-// 1.63 and 1.55; of a layer with H = 2048, I = 1024, 64 experts 32 rows 0.085 and 0.097.
+// Rows an expert, on average, up to which these products are taken.  The layer above in ms, these
+// and the wide ones: 1 row (an expert that has any) 0.45 and 0.51, 2 rows 0.89 and 0.97, 8 rows
+// 1.06 and 1.11, 16 rows 1.13 and 1.14, 32 rows 1.63 and 1.24; with H = 2048, I = 1024, 64
+// experts 4 rows 0.066 and 0.066, 32 rows 0.085 and 0.077.
 constexpr int kStreamRows = 24;
 
 template <bool kGateUp>

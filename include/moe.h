@@ -662,8 +662,8 @@ moe_status moe_mx_scale_size(int64_t rows, int64_t cols, size_t* bytes);
 
 /*
  * Quantises x [rows][cols] of dtype (a moe_dtype) into a packed matrix: s is the least
- * integer (at least -127) with max|group| <= 6 * 2^s, every value x / 2^s rounded to the nearest E2M1
- * number, ties to the one with an even code; no value is clipped, but one whose
+ * integer (at least -127) with max|group| <= 6 * 2^s, every value x / 2^s rounded to the
+ * nearest E2M1 number, ties to the one with an even code; no value is clipped, but one whose
  * rounding would reach 2^128 is held at 3 * 2^126.  A group of zeros has scale byte 0; a
  * group that holds an infinity or a NaN has scale byte 255, so that every product with
  * its row is NaN.  Experts' w_gate_up is E*2I rows of H, w_down E*H rows of I, each in
@@ -693,16 +693,20 @@ moe_status moe_dequantize_mx(int64_t rows, int64_t cols, int32_t dtype, const ui
  * The products take their activations (hidden_states and act) as the sum of two 6-bit
  * floating point numbers (E2M3), each with a power of two for 32 consecutive values:
  * off by at most 2^-8.9 of the largest of the 32, and over them closer than a rounding to
- * bf16.  Sums are fp32; y is kept to 2^-12, out rounded to bf16 once.
- * A token that holds an infinity, a NaN or a magnitude above 1.875 * 2^127 gives NaN in its
- * own output row only.  Dropped ids as in the calls above; results do not depend on N.
+ * bf16.  Sums are fp32; y is kept to 2^-12, out rounded to bf16 once.  Up to 32 assignments
+ * (T * k, of one token or not more than there are experts) take a form that rounds neither
+ * hidden_states nor y, and act to 2^-16.
+ * A token that holds an infinity or a NaN gives NaN in its own output row only; so may one
+ * that holds a magnitude above 1.875 * 2^127.  Dropped ids as in the calls above; results do
+ * not depend on N.
  * Limits: H % 64 == 0 and I % 64 == 0.
  * --------------------------------------------------------------------------- */
 
 /* Bytes of workspace moe_mx_forward needs: the metadata and, for the min(N,2) * ceil(T/N) * k
  * rows of a pair, 25/16 bytes for each of H + I values, in blocks of 32 rows of which
  * every expert may leave one in part empty (up to 50 E (H + I) bytes more), and 2H bytes of y
- * with one for each 64 of H.  Host-only. */
+ * with one for each 64 of H; for the form for few assignments also 4 bytes for each of their
+ * I values, where that is more.  Host-only. */
 moe_status moe_mx_workspace_size(const moe_shape* shape, size_t* bytes);
 
 /*
