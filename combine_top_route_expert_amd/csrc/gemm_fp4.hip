@@ -307,10 +307,10 @@ __device__ __forceinline__ TwoParts act_parts(const f32x16& g0, const f32x16& u0
   return split32(even, odd);
 }
 
-// Stores the act rows of a wave's FM row blocks from row0 on, 32-column blocks block0 on.
+// Stores the act rows of a wave's FM row blocks, 32-column blocks block0 on.
 template <int FM, int FN>
 __device__ __forceinline__ void store_act(const MxArgs& a, const f32x16 (&acc)[FM][FN],
-                                          const TileRows& tr, int row0, int block0, int lane) {
+                                          const TileRows& tr, int block0, int lane) {
   constexpr int FC = FN / 2;
   const int r = lane & 31, half = lane >> 5;
   const int nk = a.ncols / 64;
@@ -318,9 +318,9 @@ __device__ __forceinline__ void store_act(const MxArgs& a, const f32x16 (&acc)[F
   for (int i = 0; i < FM; i += 2) {
     constexpr int kLast = FM - 1;
     const int i1 = i < kLast ? i + 1 : i;
-    const int row = row0 + 32 * (i + half) + r;
+    const int row = 32 * (i + half) + r;
     const bool live = row < tr.rows && (half == 0 || i + 1 < FM);
-    const int64_t rb = mx_row_block(tr, tr.v0 + row0 + 32 * (i + half));
+    const int64_t rb = mx_row_block(tr, tr.v0 + 32 * (i + half));
 #pragma unroll
     for (int j = 0; j < FC; ++j) {
       const int block = block0 + j;
@@ -351,19 +351,18 @@ __device__ __forceinline__ float out_factor(uint32_t byte) {
   return __uint_as_float((254u - byte) << 23);
 }
 
-// kDown epilogue of a wide tile: fp16 rows through the freed stage buffers, row-major, with
-// the four scale bytes of a row behind them, out in 16-byte pieces.
+// down's epilogue of a wide tile: fp16 rows through the freed LDS, row-major, with a row's scale
+// bytes behind them, out in 16-byte pieces.
 template <int FM, int FN, int BM, int BN, int NT>
 __device__ __forceinline__ void store_out(const MxArgs& a, const f32x16 (&acc)[FM][FN],
-                                          const TileRows& tr, int nt, int row0, int wn, int lane,
-                                          char* smem) {
+                                          const TileRows& tr, int nt, int wn, int lane, char* smem) {
   typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
   constexpr int CPR = BN / 8;  // 16-byte chunks of a tile row
   auto at = [](int r, int c) {
     return r * (BN * 2) + (((c >> 3) ^ (r & (CPR - 1))) << 4) + (c & 7) * 2;
   };
   uint8_t* scales = (uint8_t*)smem + BM * BN * 2;
-  const int r0 = row0 + (lane & 31), cq = 4 * (lane >> 5);
+  const int r0 = lane & 31, cq = 4 * (lane >> 5);
 #pragma unroll
   for (int i = 0; i < FM; ++i) {
     const int r = r0 + i * 32;
@@ -454,10 +453,10 @@ __global__ void __launch_bounds__(64 * kWaves, 1) grouped_gemm_mx(MxArgs a) {
       for (int j = 0; j < FN; ++j) acc[i][j] = f32x16{};
     wide_k_loop<kGateUp, R>(acc, a, tr, nt, lane, wave, smem);
     if constexpr (kGateUp) {
-      store_act<R, FN>(a, acc, tr, 0, (nt * kWaves + wave) * (FN / 2), lane);
+      store_act<R, FN>(a, acc, tr, (nt * kWaves + wave) * (FN / 2), lane);
     } else {
       __syncthreads();  // every wave is done with the rows
-      store_out<R, FN, 32 * R, BN, NT>(a, acc, tr, nt, 0, wave, lane, smem);
+      store_out<R, FN, 32 * R, BN, NT>(a, acc, tr, nt, wave, lane, smem);
     }
   };
   if (tr.rows <= 32)
@@ -624,7 +623,7 @@ __global__ void __launch_bounds__(64 * kStreamWaves) stream_mx(MxArgs a) {
   }
 
   if constexpr (kGateUp) {
-    store_act<1, FN>(a, acc, tr, 0, nt * kStreamWaves + wave, lane);
+    store_act<1, FN>(a, acc, tr, nt * kStreamWaves + wave, lane);
   } else {
     store_out_rows(a, acc[0], tr, (nt * kStreamWaves + wave) * 64, lane);
   }

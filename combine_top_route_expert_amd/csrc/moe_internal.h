@@ -46,17 +46,11 @@ __device__ __forceinline__ void buffer_load_lds16_nt(rsrc_t r, char* dst, uint32
   __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)dst, 16,
                                            off, soff, 0, 2);
 }
-// 4 bytes a lane, at dst + 4 l.
-__device__ __forceinline__ void buffer_load_lds4(rsrc_t r, char* dst, uint32_t off, int soff) {
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)dst, 4,
-                                           off, soff, 0, 0);
-}
 #else
 struct rsrc_t {};
 __device__ __forceinline__ rsrc_t raw_rsrc(const void*) { return {}; }
 __device__ __forceinline__ void buffer_load_lds16(rsrc_t, char*, uint32_t, int) {}
 __device__ __forceinline__ void buffer_load_lds16_nt(rsrc_t, char*, uint32_t, int) {}
-__device__ __forceinline__ void buffer_load_lds4(rsrc_t, char*, uint32_t, int) {}
 #endif
 
 // Host: whether rows of ld 2-byte elements in the buffers at p0 and p1 (at
@@ -246,7 +240,7 @@ hipError_t launch_gate_up_i8(const Shape& s, const GroupedIO& io, const float* a
 hipError_t launch_down_i8(const Shape& s, const GroupedIO& io, const float* a_scale,
                           const void* w_down, const float* w_scale, hipStream_t st);
 
-// ---- layer with 4-bit experts (mx_rows.hip, gemm_fp4.hip) --------------------------
+// ---- layer with 4-bit experts (mx_rows.hip, gemm_fp4.hip, few_rows_mx.hip) ----------
 // Rows in two 6-bit parts (blocks, mx_rows.h), or output rows in scaled fp16: [rows][cols]
 // values and mx_out_scales(cols) bytes a row, one for each 64 columns.
 struct MxRows {

@@ -345,6 +345,19 @@ def test_a_group_that_is_nan():
     assert torch.equal(got, clean)
 
 
+def test_a_group_that_is_nan_for_few_assignments():
+    c = Case(3, 128, 4, 1, 64, 1, seed=2)
+    c.idx[:, 0] = torch.tensor([0, 1, 0], dtype=torch.int32)
+    clean = c.forward()
+    c.wds[5] = 255                      # row 1, columns 64..95: past K, not read
+    assert torch.equal(c.forward(), clean)
+    c.wds[4] = 255                      # row 1, columns 0..31
+    got = c.forward()
+    assert bool(got[[0, 2], 1].isnan().all())
+    got[[0, 2], 1] = clean[[0, 2], 1]
+    assert torch.equal(got, clean)
+
+
 @pytest.mark.parametrize("T", [2, 70, 2100])
 def test_graph_and_stream(T):
     c = Case(T, 256, 8, 2, 128, 2, seed=T)
