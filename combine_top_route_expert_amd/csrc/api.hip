@@ -1238,7 +1238,8 @@ moe_status router_args(const moe_shape* shape, int32_t dtype, const void* logits
 moe_status fp4_matrix(int64_t rows, int64_t cols, bool* empty) {
   if (rows < 0 || cols < 1) return MOE_ERR_INVALID_ARG;
   if (rows % kFp4BlockRows || cols % kFp4BlockCols) return MOE_ERR_UNSUPPORTED;
-  if (rows > 0 && fp4_scale_quads(cols) > 0x7fffffffLL / (rows / kFp4BlockRows))
+  // (a launch has less than 2^32 threads, 256 for every 32 rows by 256 columns)
+  if (rows > 0 && fp4_scale_quads(cols) > 0xffffffLL / (rows / kFp4BlockRows))
     return MOE_ERR_UNSUPPORTED;
   *empty = rows == 0;
   return MOE_OK;

@@ -668,7 +668,7 @@ moe_status moe_mx_scale_size(int64_t rows, int64_t cols, size_t* bytes);
  * group that holds an infinity or a NaN has scale byte 255, so that every product with
  * its row is NaN.  Experts' w_gate_up is E*2I rows of H, w_down E*H rows of I, each in
  * one call or expert by expert.  MOE_ERR_UNSUPPORTED where rows % 32 or cols % 64 is not
- * 0 or rows / 32 * ceil(cols / 256) passes 2^31 - 1.  q, scale and x must not overlap.
+ * 0 or rows / 32 * ceil(cols / 256) passes 2^24 - 1.  q, scale and x must not overlap.
  */
 moe_status moe_quantize_mx(int64_t rows, int64_t cols, int32_t dtype, const void* x, uint8_t* q,
                             uint8_t* scale, hipStream_t stream);

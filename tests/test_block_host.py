@@ -99,6 +99,14 @@ def test_matrix_limits():
         assert moe.moe_mx_scale_size(rows, cols) == rows * 8 * -(-cols // 256)
 
 
+def test_matrix_limit_of_a_launch():
+    """32 rows by 256 columns are 256 threads of a launch, which holds less than 2^32."""
+    for rows, cols in ((32 << 24, 64), (32 << 12, 256 << 12), (32 << 12, (256 << 12) - 192)):
+        assert matrices(rows, cols) == (UNSUPPORTED,) * 4, (rows, cols)
+    for rows, cols in (((32 << 24) - 32, 64), (32 << 12, (256 << 12) - 256)):
+        assert moe.moe_mx_scale_size(rows, cols) == rows * 8 * -(-cols // 256)
+
+
 def test_binding_refuses():
     s, z = shape(), torch.zeros(1 << 12)
     for call in (lambda: moe.moe_router_top_k(s, z, None, "softmax", 0, True, 1.0, z.int(), z),
