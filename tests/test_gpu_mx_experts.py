@@ -310,6 +310,15 @@ def test_chunks_do_not_change_a_bit(T, k, N):
         assert torch.equal(c.forward(moe.make_shape(T, 320, 9, k, 192, 1, n, "bf16")), want), n
 
 
+def test_both_tilings_give_the_same_bits():
+    """Experts that get nothing lower the average of rows that chooses the tiles: 4 of 64 experts, and the same 4 alone."""
+    T, H, I = 700, 448, 320  # noqa: E741
+    c = Case(T, H, 64, 2, I, 1, counts=[300, 129, 33, 900] + [0] * 60, seed=8)
+    want = c.forward()
+    c.idx[c.idx >= 4] = -1
+    assert torch.equal(c.forward(moe.make_shape(T, H, 4, 2, I, 1, 1, "bf16")), want)
+
+
 def test_one_expert_gets_everything():
     for T, k in ((64, 1), (300, 1), (5000, 1)):
         c = Case(T, 256, 16, k, 128, 1, counts=[0] * 7 + [T] + [0] * 8, seed=T)
