@@ -7,7 +7,6 @@
 
 #include "fp4_layout.h"
 #include "moe_internal.h"
-#include "mx_rows.h"
 
 namespace moe {
 
@@ -1338,12 +1337,11 @@ moe_status moe_dequantize_mx(int64_t rows, int64_t cols, int32_t dtype, const ui
 namespace moe {
 namespace {
 
-// Layout of the moe_mx_forward workspace: the forward's metadata, the pair's input and act
-// rows, sorted by expert, in two 6-bit parts and the output rows of each slot in scaled
-// fp16.
+// Layout of the moe_mx_forward workspace: the forward's metadata, the pair's act rows, sorted by
+// expert, and the output rows of each slot in scaled fp16.
 struct MxPlan {
   size_t counts, offsets, splits, src_row, dst_row, dev_err, meta_ws;
-  size_t x, x_scale, act, act_scale, y[2], y_scale[2];
+  size_t act, y[2], y_scale[2];
   size_t bytes;
 };
 
@@ -1364,11 +1362,7 @@ MxPlan mx_plan(const Shape& s) {
   p.meta_ws = take(meta_plan(s).bytes);
   const size_t rows = (size_t)s.Tc * s.k;
   const int nslots = s.N >= 2 ? 2 : 1;
-  const int64_t blocks = mx_row_blocks(nslots * (int64_t)rows, s.E);
-  p.x = take(mx_value_bytes(blocks, s.H));
-  p.x_scale = take(mx_scale_bytes(blocks, s.H));
-  p.act = take(std::max<size_t>(mx_value_bytes(blocks, s.I), few_rows_mx(s) ? (size_t)s.A * s.I * 4 : 0));
-  p.act_scale = take(mx_scale_bytes(blocks, s.I));
+  p.act = take(std::max<size_t>(nslots * rows * s.I * 2, few_rows_mx(s) ? (size_t)s.A * s.I * 4 : 0));
   for (int i = 0; i < nslots; ++i) {
     p.y[i] = take(rows * s.H * 2);
     p.y_scale[i] = take(rows * mx_out_scales(s.H));
@@ -1417,8 +1411,7 @@ moe_status moe_mx_forward(const moe_shape* shape, const void* hidden_states,
   if (few_rows_mx(s))
     return hip_status(launch_few_mx(s, hidden_states, top_k_index, top_k_weights, w_gate_up_q,
                                     w_gate_up_scale, w_down_q, w_down_scale, w + p.act, out, err, stream));
-  const MxRows x{w + p.x, w + p.x_scale}, act{w + p.act, w + p.act_scale};
-  const MxRows y[2] = {{w + p.y[0], w + p.y_scale[0]}, {w + p.y[1], w + p.y_scale[1]}};
+  const ScaledRows y[2] = {{w + p.y[0], w + p.y_scale[0]}, {w + p.y[1], w + p.y_scale[1]}};
   hipError_t he = launch_route_meta(s, top_k_index, (int32_t*)(w + p.counts), offsets,
                                     (int32_t*)(w + p.splits), src_row, dst_row, err,
                                     w + p.meta_ws, stream);
@@ -1436,13 +1429,12 @@ moe_status moe_mx_forward(const moe_shape* shape, const void* hidden_states,
     io.rows_bound = rows0 + rows1;
     io.gather[0] = src_row + (size_t)t0 * s.k;
     io.gather[1] = src_row + (size_t)u0 * s.k;
-    he = launch_split_rows(s, io, hidden_states, x, stream);
     io.w = w_gate_up_q;
     io.w_scale = w_gate_up_scale;
-    if (he == hipSuccess) he = launch_gate_up_mx(s, io, x, act, stream);
+    he = launch_gate_up_mx(s, io, hidden_states, w + p.act, stream);
     io.w = w_down_q;
     io.w_scale = w_down_scale;
-    if (he == hipSuccess) he = launch_down_mx(s, io, act, y, stream);
+    if (he == hipSuccess) he = launch_down_mx(s, io, w + p.act, y, stream);
     if (he == hipSuccess)
       he = rows1 > 0
                ? launch_combine_scaled(s, t0, u0, u1, y, dst_row, top_k_weights, out, stream)

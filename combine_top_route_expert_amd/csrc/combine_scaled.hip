@@ -1,66 +1,17 @@
-// Row kernels of the layer with 4-bit experts: the input rows, sorted by expert, in two
-// 6-bit parts (mx_rows.h), and the weighted combine of the output rows, which the second
-// product leaves as fp16 numbers with a power of two for each 64 columns of a row.
+// Weighted combine of the layer with 4-bit experts, whose output rows the second product leaves as
+// fp16 numbers with a power of two for each 64 columns of a row.
 //
-// Both are bound by memory.  A workgroup of the first takes a row block, found by the
-// products' own tile map; its waves take 64 columns of the 32 rows at a time, 64 bytes of a
-// row to a lane.  It does the layer's permute as well: k rows are written for every token, and
-// the first product copies contiguous blocks.  16384 tokens of 2048 values with 8 experts:
-// 145 us for 400 MB written and 540 read, most of them from the caches (6.5 TB/s).  Without
-// effect: the next block's loads ahead of a split, eight times the workgroups (2% less time).
-// One split of each token whose parts go to its k places, 16 bytes at a time: 0 to 20% more of
-// the layer's time at every size, the most where rows are many.
-//
-// The combine reads 540 MB and writes 67 there in 100 us, 6 TB/s.  Scaled fp16 keeps y to 2^-12 in
-// the two bytes that bf16 would spend on 2^-9: of the layer's roundings (two parts of x and
-// act, y, out) y's was the largest but one.
+// Bound by memory: 16384 tokens of 2048 values with 8 experts read 540 MB and write 67 in 100 us,
+// 6 TB/s.  Scaled fp16 keeps y to 2^-11 of each value (and to 2^-39 of the largest of the 64, which
+// counts for those 2^28 times smaller) in the two bytes in which bf16 would keep it to 2^-8; fp32
+// would cost twice the bytes here and in the product's epilogue.
 #include <algorithm>
 
-#include "mx_rows.h"
+#include "moe_internal.h"
 
 namespace moe {
 
 namespace {
-
-constexpr int kThreads = 256;
-
-struct SplitArgs {
-  const u32x4* x;             // [T][H] bf16
-  const int32_t *off0, *off1;
-  const int32_t* gather[2];   // src_row slices
-  int E, k, H;
-  MxRows to;
-};
-
-__global__ void __launch_bounds__(kThreads) split_rows(SplitArgs a) {
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  MTileMap tm;
-  tm.build(a.off0, a.off1, a.E, 32, 1);
-  if ((int)blockIdx.x >= tm.total) return;
-  const TileRows tr = tm.locate(a.off0, a.off1, 32, blockIdx.x);
-  const int r = lane & 31, half = lane >> 5;
-  if (r >= tr.rows) return;
-  int part;
-  const int cr = tr.split_row(tr.v0 + r, &part);
-  const int32_t *g0 = a.gather[0], *g1 = a.gather[1];
-  const int64_t token = (part ? g1 : g0)[cr] / a.k;
-  const u32x4* x = a.x + token * (a.H / 8) + half * 4;
-  const int nk = a.H / 64;
-  const int64_t rb = mx_row_block(tr, tr.v0);
-  for (int k = blockIdx.y * (kThreads / 64) + wave; k < nk; k += gridDim.y * (kThreads / 64)) {
-    u32x4 v[4];
-#pragma unroll
-    for (int q = 0; q < 4; ++q) v[q] = x[k * 8 + q];
-    f32x16v even, odd;
-#pragma unroll
-    for (int q = 0; q < 16; ++q) {
-      const uint32_t two = v[q / 4][q % 4];
-      even[q] = __uint_as_float(two << 16);
-      odd[q] = __uint_as_float(two & 0xffff0000u);
-    }
-    store_parts(split32(even, odd), a.to, nk, rb, r, 2 * k + half);
-  }
-}
 
 constexpr int kWaves = 4;        // tokens of a workgroup
 constexpr int kVecPerLane = 4;   // 16-byte vectors a lane keeps in flight per pass
@@ -130,29 +81,7 @@ combine_scaled(const u32x4* __restrict__ y0, const uint8_t* __restrict__ s0,
 
 }  // namespace
 
-hipError_t launch_split_rows(const Shape& s, const MxIO& io, const void* x, const MxRows& to,
-                             hipStream_t st) {
-  if (io.rows_bound <= 0) return hipSuccess;
-  SplitArgs a{};
-  a.x = (const u32x4*)x;
-  a.off0 = io.off[0];
-  a.off1 = io.off[1];
-  a.gather[0] = io.gather[0];
-  a.gather[1] = io.off[1] ? io.gather[1] : io.gather[0];
-  a.E = s.E;
-  a.k = s.k;
-  a.H = s.H;
-  a.to = to;
-  const int64_t blocks = m_tiles_bound(io.rows_bound, s.E, 32);
-  if (blocks > 0x7fffffff / kThreads) return hipErrorInvalidConfiguration;
-  // few row blocks: their columns to several workgroups
-  const int parts = (int)std::max<int64_t>(
-      1, std::min<int64_t>(s.H / 64 / (kThreads / 64), 2048 / std::max<int64_t>(blocks, 1)));
-  hipLaunchKernelGGL(split_rows, dim3((unsigned)blocks, (unsigned)parts), dim3(kThreads), 0, st, a);
-  return hipGetLastError();
-}
-
-hipError_t launch_combine_scaled(const Shape& s, int t0, int t_mid, int t1, const MxRows (&y)[2],
+hipError_t launch_combine_scaled(const Shape& s, int t0, int t_mid, int t1, const ScaledRows (&y)[2],
                                  const int32_t* dst_row, const float* w, void* out,
                                  hipStream_t st) {
   if (t1 <= t0) return hipSuccess;

@@ -1,71 +1,65 @@
-// Grouped expert products with packed 4-bit weights (fp4_layout.h) and rows in two 6-bit
-// parts (mx_rows.h):
-//   gate_up: act[r] = silu(g) u in two parts,  g, u = x_r . W[e][i], x_r . W[e][I + i]
+// Grouped expert products with bf16 rows and packed 4-bit weights (fp4_layout.h):
+//   gate_up: act[r] = rd(silu(g) u),  g, u = x_r . W[e][i], x_r . W[e][I + i]
 //   down   : y[r][n] = act_r . W[e][n] in scaled fp16
 //
-// v_mfma_scale_f32_32x32x64_f8f6f4 multiplies 32 x 64 E2M1 weights by 32 x 64 E2M3 values
-// with a power of two for each 32 of either side, in the 32 cycles in which the bf16
-// instruction multiplies a quarter of that; the two parts of the rows make it half the
-// matrix time of bf16.  Weights go from memory to the instruction as they lie, in one load:
-// lane 32 h + r holds the 16 bytes of columns 32 h .. of row r and a dword with its scales of
-// four blocks, of which the instruction picks a byte.  (Converted to bf16 in registers
-// instead, with bf16 rows and instructions: 2.05 ms for gate_up of 4096 tokens on 256
-// experts, H = 7168, I = 2048, instead of 1.24.)  Sums are fp32, over K in ascending order,
-// part h before part l in each 64 columns, whatever the tile: both forms give the same bits.
+// A weight is an E2M1 number times a power of two, which bf16 holds exactly, and the rows are
+// those that the caller gave, so all products are exact, as those of the bf16 layer with the
+// weights written out.  Weights go from memory straight into registers as they lie: lane 32 h + r
+// of a load holds the 16 bytes of columns 32 h .. + 31 of row r, and of a dword its scales of four
+// blocks; v_cvt_scalef32_pk_bf16_fp4 makes two operands and their power of two in one instruction,
+// right before the matrix instructions that they feed.  Instruction q of a block's four
+// multiplies columns 8 q .. + 7 of both halves; the rows' fragments are read to match.  Sums are
+// fp32, over K in ascending order of the instructions, whatever the tile: both forms give the same
+// bits.
+//
+// Against this, rows in two 6-bit parts on v_mfma_scale_f32_32x32x64_f8f6f4, which multiplies
+// the packed weights at up to four times the rate, halve the matrix time, but keep of a row only
+// 2^-9 of the largest of 32 neighbours: small values beside a large one are lost.
 #include <algorithm>
 #include <type_traits>
 
-#include "fp4_layout.h"
-#include "gemm_tile.h"
-#include "mx_rows.h"
+#include "fp4_operand.h"
 
 namespace moe {
 
 namespace {
 
-typedef int i32x12 __attribute__((ext_vector_type(12)));
-
-struct MxArgs {
-  MxRows a;                   // rows of A
-  const int32_t *off0, *off1; // E + 1 offsets of the chunk(s); off1 may be null
-  const char *b, *bs;         // packed weights and scales, expert after expert
-  int64_t b_expert, bs_expert;
-  int E, ncols, n_tiles;      // columns of C, column tiles
+// A: hidden states or act; B: packed weights; C (gate_up): act.
+struct MxArgs : GemmArgs {
+  const char* bs;             // scales, expert after expert
+  int64_t bs_expert;
   int blocks, quads;          // 64-column blocks of K, scale dwords of a weight row
   int up;                     // gate_up: row blocks from a gate row to its up row
-  MxRows c;                   // gate_up: act
-  MxRows y[2];                // down: the two chunks' rows
-  int c_split;
+  ScaledRows y[2];            // down: the two chunks' rows
 };
 
-// One product of 64 columns: weights w (16 bytes a lane) and a part of the rows (the first
-// or the last 24 of a lane's 48 bytes), with byte kWs of the weights' scales and byte kAs + kPart
-// of the rows'.
-template <int kPart, int kWs, int kAs>
-__device__ __forceinline__ f32x16 mx_mma(const i32x4& w, uint32_t ws, const i32x12& a, uint32_t as,
-                                         const f32x16& c) {
-#if defined(__HIP_DEVICE_COMPILE__)
-  typedef int i32x8 __attribute__((ext_vector_type(8)));
-  const i32x8 wv = __builtin_shufflevector(w, w, 0, 1, 2, 3, -1, -1, -1, -1);
-  i32x8 av;
-  if constexpr (kPart == 0)
-    av = __builtin_shufflevector(a, a, 0, 1, 2, 3, 4, 5, -1, -1);
-  else
-    av = __builtin_shufflevector(a, a, 6, 7, 8, 9, 10, 11, -1, -1);
-  // (4: E2M1, 2: E2M3)
-  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(wv, av, c, 4, 2, kWs, (int)ws, kAs + kPart,
-                                                         (int)as);
-#else
-  return c;
-#endif
+// A stage is 64 columns of K, 128 bytes of a row: 32 rows of one are 4 KB of LDS, chunk c of 16
+// bytes of row r at slot c ^ swz(r), copied a kilobyte (8 rows) at a time.
+using Stage = StageGeom<128>;
+constexpr int kRowBlockBytes = 32 * Stage::ROW_BYTES;
+
+// What this lane copies of row `row` of a tile (one past its last repeats that): the address of
+// its 16 bytes of the row's first stage.
+template <bool kGateUp>
+__device__ __forceinline__ const char* row_piece(const MxArgs& g, const TileRows& tr, int row,
+                                                 int lane) {
+  const int v = tr.v0 + (row < tr.rows ? row : tr.rows - 1);
+  int64_t r;
+  if constexpr (kGateUp) {  // the permute, in the rows' addresses
+    int part;
+    const int cr = tr.split_row(v, &part);
+    const int32_t *g0 = g.gather[0], *g1 = g.gather[1];
+    r = (part ? g1 : g0)[cr] / g.gather_k;
+  } else {
+    r = tr.joint_row(v);
+  }
+  return g.A[0] + r * g.row_bytes + ((lane % Stage::CH) ^ Stage::swz(row)) * 16;
 }
 
-// A lane's 48 bytes of a row block, from its thirds.
-__device__ __forceinline__ i32x12 both_parts(const i32x4 (&a)[3]) {
-  return __builtin_shufflevector(
-      __builtin_shufflevector(a[0], a[1], 0, 1, 2, 3, 4, 5, 6, 7),
-      __builtin_shufflevector(a[2], a[2], 0, 1, 2, 3, -1, -1, -1, -1), 0, 1, 2, 3, 4, 5, 6, 7, 8, 9,
-      10, 11);
+// Offset within a row block of a lane's fragment for instruction q of a stage.
+__device__ __forceinline__ int fragment_at(int lane, int q) {
+  const int r = lane & 31, half = lane >> 5;
+  return r * Stage::ROW_BYTES + (((4 * half + q) ^ Stage::swz(r)) << 4);
 }
 
 // Row block of the packed weights behind block j of a tile's NB (FN to a wave): gate_up, a
@@ -89,95 +83,71 @@ __device__ __forceinline__ int weight_block(const MxArgs& g, int nt, int nb, int
 // rows by 512 columns, a wave all the rows of its own 128 columns (R x 4 blocks of 32 x 32).
 // The weights, which no other wave uses, go from memory straight into registers, three stages
 // (of 64 columns of K) ahead; the rows go through LDS, a unit of four stages at a time in
-// two buffers, and a row block's operands are read while the one before is multiplied.
+// two buffers, their fragments read two steps (of four matrix instructions) ahead.
 //
-// Why this shape: a column of A is 12 bits and one of the weights 4, so that of tiles of 65536
-// sums, all that a CU's registers hold, the one of 128 x 512 copies less than 256 x 256 (28 KB
-// a stage against 32); and with the weights past LDS a stage's 1024 cycles of matrix
-// instructions go with 48 KB of reads and 12 KB of writes there.  256 x 256 with both sides in
-// LDS, two by two waves (64 and 32 KB) took 2000 cycles a stage, about the sum of what its reads
-// and its copies cost: the layer of 4096 tokens with 8 of 256 experts of H = 7168, I = 2048 2.67
-// ms instead of 2.36, of 1024 tokens 1.53 instead of 1.24, of 16384 tokens with 8 of 128 experts
-// of H = 2048, I = 768 1.26 instead of 1.13 to 1.21.
+// Why this shape: of tiles of 65536 sums, all that a CU's registers hold, it copies the least for a
+// stage (16 KB of rows and 17 of weights; 256 x 256: 32 and 8.5), and with the weights past LDS a
+// stage's 2048 cycles of matrix instructions go with 64 KB of reads and 16 KB of writes there.  Converting
+// a wave's weights takes one instruction beside every matrix instruction at four row blocks, four
+// at one.
 //
-// The first of these: gate_up 1.21 ms and down 0.80, 1.43 PFLOP/s, 4.9 TB/s of weights.  Neither
-// the matrix pipe (0.64 and 0.32 ms at the 6 PF/s that the instruction reaches, power being what
-// limits it) nor memory (0.59 and 0.29) is full: tiles whose last row block holds a few rows,
-// prologues and epilogues with one workgroup on a CU, and LDS take the rest.  Without effect:
-// seven stages ahead for up to 64 rows (0 to 5% slower); twice the row tiles to a group of an
-// XCD's workgroups; experts in order instead of large ones first (0 to 2% slower); weights that
-// leave no trace in the caches (1% slower, 7% where the layer fits them).
+// 4096 tokens with 8 of 256 experts of H = 7168, I = 2048: gate_up 1.56 ms, its matrix pipe busy for
+// 71% of them at the 1.85 GHz that the power limit leaves; down 1.00 ms, 54%: 1.13 PFLOP/s together.
+// Tiles whose last row block holds a few rows, and prologues and epilogues with one workgroup on a CU,
+// take the rest.
 constexpr int kWaves = 4, kWideFN = 4;  // waves; column blocks of a wave
 constexpr int kUnit = 4;                // stages of a unit
 constexpr int kWideRows = 128;
-
-template <int R>
-struct WideUnit {
-  static constexpr int kAtScales = R * kUnit * kMxBlockBytes;
-  static constexpr int kBytes = kAtScales + R * kUnit / 2 * kMxScaleBytes;
-  static constexpr int kValues = R * kUnit * 3 / kWaves;               // a wave's copies
-  static constexpr int kScales = (R * kUnit / 2 + kWaves - 1) / kWaves;
-  static constexpr int kCopies = kValues + kScales;
-};
 
 // The K loop of a wave.
 template <bool kGateUp, int R>
 __device__ __forceinline__ void wide_k_loop(f32x16 (&acc)[R][kWideFN], const MxArgs& g,
                                             const TileRows& tr, int nt, int lane, int wave,
                                             char* smem) {
-  using U = WideUnit<R>;
-  constexpr int FN = kWideFN;
+  constexpr int FN = kWideFN, kSteps = 4 * R;  // steps of a stage: instruction q, row block i
+  constexpr int kUnitBytes = R * kUnit * kRowBlockBytes, kCopies = R * kUnit;  // a wave's copies
+  constexpr int kAhead = 2;                    // steps from a fragment's read to its use
   const int e = __builtin_amdgcn_readfirstlane(tr.e);
-  const int KB = g.blocks, units = g.quads, pairs = (KB + 1) / 2, full = KB / kUnit;
-  const int64_t rb0 = mx_row_block(tr, tr.v0);
-  const char* av = g.a.values + rb0 * KB * kMxBlockBytes + lane * 16;
-  const char* as = g.a.scales + rb0 * pairs * kMxScaleBytes + lane * 4;
-  // Copy q of unit u: kilobyte q of the values, then 256 bytes of scales; blocks past the last
-  // of K repeat that, and copies past a unit's last repeat it.
+  const int KB = g.blocks, units = g.quads, full = KB / kUnit;
+  // Of each row block a wave copies eight rows.
+  const char* rows[R];
+#pragma unroll
+  for (int i = 0; i < R; ++i)
+    rows[i] = row_piece<kGateUp>(g, tr, 32 * i + 8 * wave + lane / Stage::CH, lane);
+  // Copy t of unit u; stages past the last of K repeat that.
   auto copy = [&](int u, int t) __attribute__((always_inline)) {
-    char* base = smem + (u & 1) * U::kBytes;
-    if (t < U::kValues) {
-      const int q = t * kWaves + wave, i = q / (3 * kUnit), k = kUnit * u + q % (3 * kUnit) / 3;
-      __builtin_amdgcn_global_load_lds(
-          (const void*)(av + ((int64_t)i * KB + (k < KB ? k : KB - 1)) * kMxBlockBytes + q % 3 * 1024),
-          (lds_void*)(base + q * 1024), 16, 0, 0);
-    } else {
-      int q = (t - U::kValues) * kWaves + wave;
-      q = q < R * kUnit / 2 ? q : R * kUnit / 2 - 1;
-      const int i = q / (kUnit / 2), pair = kUnit / 2 * u + q % (kUnit / 2);
-      __builtin_amdgcn_global_load_lds(
-          (const void*)(as + ((int64_t)i * pairs + (pair < pairs ? pair : pairs - 1)) * kMxScaleBytes),
-          (lds_void*)(base + U::kAtScales + q * kMxScaleBytes), 4, 0, 0);
-    }
+    const int k = kUnit * u + t % kUnit;
+    __builtin_amdgcn_global_load_lds(
+        (const void*)(rows[t / kUnit] + (int64_t)(k < KB ? k : KB - 1) * Stage::ROW_BYTES),
+        (lds_void*)(smem + (u & 1) * kUnitBytes + t * kRowBlockBytes + wave * 1024), 16, 0, 0);
   };
   const i32x4* b[FN];
   const uint32_t* bs[FN];
 #pragma unroll
   for (int j = 0; j < FN; ++j) {
     const int rb = weight_block<kGateUp, FN>(g, nt, kWaves * FN, wave * FN + j);
-    b[j] = (const i32x4*)(g.b + e * g.b_expert + (int64_t)rb * KB * kFp4BlockBytes) + lane;
+    b[j] = (const i32x4*)(g.B + e * g.b_expert_bytes + (int64_t)rb * KB * kFp4BlockBytes) + lane;
     bs[j] = (const uint32_t*)(g.bs + e * g.bs_expert + (int64_t)rb * units * kFp4ScaleBytes) + lane;
   }
-  i32x4 w[kUnit][FN];
-  uint32_t sc[FN], sn[FN];
-  struct Row {
-    i32x4 thirds[3];
-    uint32_t s;
-  };
-  Row row[2];
+  i32x4 w[kUnit][FN] = {};
+  uint32_t sc[FN], sn[FN];           // scales of this unit's stages and of the next's
+  bf16x8 wb[2][FN], frag[4];
   auto load = [&](int k, int j, i32x4& to) __attribute__((always_inline)) {
     to = b[j][(int64_t)k * (kFp4BlockBytes / 16)];
   };
-  auto read = [&](Row& to, int u, int k, int i, int t) __attribute__((always_inline)) {
-    const char* base = smem + (u & 1) * U::kBytes;
-    if (t < 3)
-      to.thirds[t] = *(const i32x4*)(base + (i * kUnit + k) * kMxBlockBytes + t * 1024 + lane * 16);
-    else
-      to.s = *(const uint32_t*)(base + U::kAtScales + (i * (kUnit / 2) + k / 2) * kMxScaleBytes +
-                                lane * 4);
+  const int at = fragment_at(lane, 0);
+  // step n of stage k of unit u
+  auto read = [&](int u, int k, int n) __attribute__((always_inline)) {
+    frag[n & 3] = *(const bf16x8*)(smem + (u & 1) * kUnitBytes + (n % R * kUnit + k) * kRowBlockBytes +
+                                   (at ^ (n / R << 4)));
+  };
+  // operands of instruction q from stage k's weights, whose scales are s
+  auto convert = [&](int k, int q, int j, uint32_t s) __attribute__((always_inline)) {
+    const int v = w[k][j][q];
+    wb[q & 1][j] = unpack_fp4((uint32_t)v, s >> (8 * k) & 0xffu);
   };
 #pragma unroll
-  for (int t = 0; t < U::kCopies; ++t) copy(0, t);
+  for (int t = 0; t < kCopies; ++t) copy(0, t);
   __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
   for (int j = 0; j < FN; ++j) sn[j] = sc[j] = bs[j][0];
@@ -196,7 +166,9 @@ __device__ __forceinline__ void wide_k_loop(f32x16 (&acc)[R][kWideFN], const MxA
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
 #pragma unroll
-  for (int t = 0; t < 4; ++t) read(row[0], 0, 0, 0, t);
+  for (int n = 0; n < kAhead; ++n) read(0, 0, n);
+#pragma unroll
+  for (int j = 0; j < FN; ++j) convert(0, 0, j, sc[j]);
 
   // Stage k of unit u.  kFull: unit u + 1 is a whole one.
   auto stage = [&](int u, auto k_tag, auto full_tag) __attribute__((always_inline)) {
@@ -209,46 +181,43 @@ __device__ __forceinline__ void wide_k_loop(f32x16 (&acc)[R][kWideFN], const MxA
       for (int j = 0; j < FN; ++j) sn[j] = bs[j][(u + 1) * (kFp4ScaleBytes / 4)];
     }
 #pragma unroll
-    for (int i = 0; i < R; ++i) {
-      const bool last = k == kUnit - 1 && i == R - 1;
-      if (last && next) {
+    for (int n = 0; n < kSteps; ++n) {
+      const int q = n / R, i = n % R;
+      const int to = n + kAhead;  // the step whose fragment is read
+      if (k == kUnit - 1 && to == kSteps && next) {
         // every wave has read this unit; the copies of the next, issued in the first stage, have
-        // landed once at most the loads issued after that stage are pending
-        constexpr int kLoads = (R > 1 ? kUnit - 1 : kUnit - 2) * FN;
-        __builtin_amdgcn_s_waitcnt(kFull ? wait_vm(kLoads) : wait_vm(0));
+        // landed once at most the three stages' loads issued after them are pending
+        __builtin_amdgcn_s_waitcnt(kFull ? wait_vm((kUnit - 1) * FN) : wait_vm(0));
         __builtin_amdgcn_s_waitcnt(kWaitLgkm0);
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
       }
-      const Row& now = row[(k * R + i) & 1];
-      Row& then = row[(k * R + i + 1) & 1];
-      const i32x12 rows = both_parts(now.thirds);
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int m = 0; m < 2 * FN; ++m) {
-        const int j = m % FN;
-        acc[i][j] = m < FN ? mx_mma<0, k, 2 * (k & 1)>(w[k][j], sc[j], rows, now.s, acc[i][j])
-                           : mx_mma<1, k, 2 * (k & 1)>(w[k][j], sc[j], rows, now.s, acc[i][j]);
+      for (int m = 0; m < FN; ++m) {
+        acc[i][m] = MmaBf16::mma(wb[q & 1][m], frag[n & 3], acc[i][m]);
         // (the compiler moves matrix instructions down past branches, and so past the copies
         // and the barrier that they are to cover, unless their results are named before)
-        asm volatile("" : "+a"(acc[i][j]));
+        asm volatile("" : "+a"(acc[i][m]));
         __builtin_amdgcn_sched_barrier(0);
-        if (m < 4) {
-          if (i < R - 1)
-            read(then, u, k, i + 1, m);
+        if (m == 0) {
+          if (to < kSteps)
+            read(u, k, to);
           else if (k < kUnit - 1)
-            read(then, u, k + 1, 0, m);  // (of a stage past the last, unused)
+            read(u, k + 1, to - kSteps);  // (of a stage past the last, unused)
           else if (next)
-            read(then, u + 1, 0, 0, m);
+            read(u + 1, 0, to - kSteps);
         }
-        if (i == 0 && m >= 2 * FN - FN && ahead)
-          load(kUnit * u + k + kUnit - 1, m - FN, w[(k + kUnit - 1) % kUnit][m - FN]);
-        if (k == 0 && next) {
-          constexpr int kMma = 2 * FN * R;
-          const int at = i * 2 * FN + m;
-#pragma unroll
-          for (int t = at * U::kCopies / kMma; t < (at + 1) * U::kCopies / kMma; ++t) copy(u + 1, t);
+        // the next instruction's operands, R steps of FN slots for FN of them
+        const int slot = i * FN + m;
+        if (slot % R == 0) {
+          if (q < 3)
+            convert(k, q + 1, slot / R, sc[slot / R]);
+          else
+            convert((k + 1) % kUnit, 0, slot / R, k < kUnit - 1 ? sc[slot / R] : sn[slot / R]);
         }
+        if (n == 0 && ahead) load(kUnit * u + k + kUnit - 1, m, w[(k + kUnit - 1) % kUnit][m]);
+        if (k == 0 && m == FN - 1 && next) copy(u + 1, n);
         __builtin_amdgcn_sched_barrier(0);
       }
     }
@@ -275,60 +244,6 @@ __device__ __forceinline__ void wide_k_loop(f32x16 (&acc)[R][kWideFN], const MxA
     if (kUnit * u + 3 < KB) stage(u, k3, part);
 #pragma unroll
     for (int j = 0; j < FN; ++j) sc[j] = sn[j];
-  }
-}
-
-// act of 32 rows by 32 columns of two row blocks, from the accumulators of gate and up
-// columns: lane l holds row l % 32 of a block and its columns 8 (q / 4) + 4 (l / 32) + q % 4.
-// Swapping the upper half of one block's registers with the lower half of the other's
-// leaves lane l all 32 columns of one row, in the first block (l < 32) or the second.
-__device__ __forceinline__ TwoParts act_parts(const f32x16& g0, const f32x16& u0, const f32x16& g1,
-                                              const f32x16& u1) {
-  f32x16v even, odd;
-#pragma unroll
-  for (int q = 0; q < 16; ++q) {
-    const float a = swiglu<true>(g0[q], u0[q]), b = swiglu<true>(g1[q], u1[q]);
-    float lo = a, hi = b;  // columns 8 (q / 4) + q % 4 and 4 more of the lane's row
-#if defined(__HIP_DEVICE_COMPILE__)
-    const auto s = __builtin_amdgcn_permlane32_swap(__float_as_uint(a), __float_as_uint(b), false,
-                                                    false);
-    lo = __uint_as_float(s[0]);
-    hi = __uint_as_float(s[1]);
-#endif
-    const int c = 4 * (q / 4) + q % 4 / 2;  // half of the first's column
-    if (q % 2 == 0) {
-      even[c] = lo;
-      even[c + 2] = hi;
-    } else {
-      odd[c] = lo;
-      odd[c + 2] = hi;
-    }
-  }
-  return split32(even, odd);
-}
-
-// Stores the act rows of a wave's FM row blocks, 32-column blocks block0 on.
-template <int FM, int FN>
-__device__ __forceinline__ void store_act(const MxArgs& a, const f32x16 (&acc)[FM][FN],
-                                          const TileRows& tr, int block0, int lane) {
-  constexpr int FC = FN / 2;
-  const int r = lane & 31, half = lane >> 5;
-  const int nk = a.ncols / 64;
-#pragma unroll
-  for (int i = 0; i < FM; i += 2) {
-    constexpr int kLast = FM - 1;
-    const int i1 = i < kLast ? i + 1 : i;
-    const int row = 32 * (i + half) + r;
-    const bool live = row < tr.rows && (half == 0 || i + 1 < FM);
-    const int64_t rb = mx_row_block(tr, tr.v0 + 32 * (i + half));
-#pragma unroll
-    for (int j = 0; j < FC; ++j) {
-      const int block = block0 + j;
-      if (block * 32 >= a.ncols) break;
-      const TwoParts p = act_parts(acc[i][j], acc[i][j + FC], acc[i1][j], acc[i1][j + FC]);
-      if (live) store_parts(p, a.c, nk, rb, r, block);
-      __builtin_amdgcn_sched_barrier(0);  // one block at a time: a split holds a hundred registers
-    }
   }
 }
 
@@ -434,7 +349,8 @@ __device__ __forceinline__ void store_out_rows(const MxArgs& a, const f32x16 (&a
 template <bool kGateUp>
 __global__ void __launch_bounds__(64 * kWaves, 1) grouped_gemm_mx(MxArgs a) {
   constexpr int FN = kWideFN, BN = 32 * FN * kWaves, NT = 64 * kWaves;
-  constexpr int kTile = kGateUp ? 0 : kWideRows * (BN * 2 + BN / 64), kUnits = 2 * WideUnit<4>::kBytes;
+  constexpr int kTile = kGateUp ? kWideRows * BN : kWideRows * (BN * 2 + BN / 64);
+  constexpr int kUnits = 2 * (kWideRows / 32) * kUnit * kRowBlockBytes;
   __shared__ __attribute__((aligned(1024))) char smem[kUnits > kTile ? kUnits : kTile];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   MTileMap tm;
@@ -452,12 +368,12 @@ __global__ void __launch_bounds__(64 * kWaves, 1) grouped_gemm_mx(MxArgs a) {
 #pragma unroll
       for (int j = 0; j < FN; ++j) acc[i][j] = f32x16{};
     wide_k_loop<kGateUp, R>(acc, a, tr, nt, lane, wave, smem);
-    if constexpr (kGateUp) {
-      store_act<R, FN>(a, acc, tr, (nt * kWaves + wave) * (FN / 2), lane);
-    } else {
-      __syncthreads();  // every wave is done with the rows
+    __syncthreads();  // every wave is done with the rows
+    if constexpr (kGateUp)
+      store_tile_lds<true, 1, R, FN, 32 * R, BN, 32 * R, 32 * FN, NT>(a, acc, tr, nt, 0, R, wave, lane,
+                                                                     smem);
+    else
       store_out<R, FN, 32 * R, BN, NT>(a, acc, tr, nt, wave, lane, smem);
-    }
   };
   if (tr.rows <= 32)
     run(std::integral_constant<int, 1>{});
@@ -486,20 +402,16 @@ hipError_t launch_wide(MxArgs a, int64_t rows_bound, hipStream_t st) {
 // four stages ahead, and no other wave reads them; only the rows of A, which the waves of a
 // workgroup share, go through LDS, a unit at a time in two buffers with one barrier for it.
 // Of an H = 7168, I = 2048 layer with 64 tokens on 8 of 256 experts (2 rows each) gate_up
-// reads 3.4 GB in 590 us and down 1.7 in 285, 5.9 and 6.1 TB/s (a plain read of such weights:
-// 6.8).  Loads that leave the weights in the caches cost 6% more; two or six waves a
-// workgroup 0 and 19%.
+// reads 3.4 GB in 571 us and down 1.7 in 302, 5.9 and 5.6 TB/s (a plain read of such weights: 6.8).
 constexpr int kStreamWaves = 4;
-// Rows an expert, on average, up to which these products are taken.  The layer above in ms, these
-// and the wide ones: 1 row (an expert that has any) 0.45 and 0.51, 2 rows 0.89 and 0.97, 8 rows
-// 1.06 and 1.11, 16 rows 1.13 and 1.14, 32 rows 1.63 and 1.24; with H = 2048, I = 1024, 64
-// experts 4 rows 0.066 and 0.066, 32 rows 0.085 and 0.077.
+// Rows an expert, on average, up to which these products are taken.
 constexpr int kStreamRows = 24;
 
 template <bool kGateUp>
 __global__ void __launch_bounds__(64 * kStreamWaves) stream_mx(MxArgs a) {
-  constexpr int BM = 32, FN = 2;
-  constexpr int kUnitBytes = kUnit * kMxBlockBytes + kUnit / 2 * kMxScaleBytes;
+  constexpr int BM = 32, FN = 2, BN = 32 * FN * kStreamWaves;
+  constexpr int kUnitBytes = kUnit * kRowBlockBytes;
+  static_assert(2 * kUnitBytes >= BM * BN, "act of a tile fits the rows' buffers");
   __shared__ __attribute__((aligned(1024))) char smem[2 * kUnitBytes];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   MTileMap tm;
@@ -510,35 +422,27 @@ __global__ void __launch_bounds__(64 * kStreamWaves) stream_mx(MxArgs a) {
     return;
   const TileRows tr = tm.locate(a.off0, a.off1, BM, mt);
   const int e = __builtin_amdgcn_readfirstlane(tr.e);
-  const int units = a.quads, KB = a.blocks, pairs = (KB + 1) / 2;
-  const int r = lane & 31;
+  const int units = a.quads, KB = a.blocks;
 
-  // Unit u of A: twelve kilobytes of values, three to a wave, and two dwords a row of scales.
-  // Blocks past the last of K repeat that; the entries of rows past the tile's are not copied.
-  const int64_t rb0 = mx_row_block(tr, tr.v0);
-  const char* av = a.a.values + rb0 * KB * kMxBlockBytes + lane * 16;
-  const char* as = a.a.scales + rb0 * pairs * kMxScaleBytes + lane * 4;
+  // Unit u of A: eight rows to a wave, nothing to one whose rows all lie past the tile's.  Stages
+  // past the last of K repeat that.
+  const char* rows = row_piece<kGateUp>(a, tr, 8 * wave + lane / Stage::CH, lane);
   auto copy = [&](int u) __attribute__((always_inline)) {
-    if (r >= tr.rows) return;
-    char* base = smem + (u & 1) * kUnitBytes;
+    if (8 * wave >= tr.rows) return;
 #pragma unroll
-    for (int t = 0; t < kUnit * 3 / kStreamWaves; ++t) {
-      const int q = t * kStreamWaves + wave, k = kUnit * u + q / 3;
+    for (int t = 0; t < kUnit; ++t) {
+      const int k = kUnit * u + t;
       __builtin_amdgcn_global_load_lds(
-          (const void*)(av + (int64_t)(k < KB ? k : KB - 1) * kMxBlockBytes + q % 3 * 1024),
-          (lds_void*)(base + q * 1024), 16, 0, 0);
+          (const void*)(rows + (int64_t)(k < KB ? k : KB - 1) * Stage::ROW_BYTES),
+          (lds_void*)(smem + (u & 1) * kUnitBytes + t * kRowBlockBytes + wave * 1024), 16, 0, 0);
     }
-    const int d = wave & 1, pair = 2 * u + d;
-    __builtin_amdgcn_global_load_lds(
-        (const void*)(as + (int64_t)(pair < pairs ? pair : pairs - 1) * kMxScaleBytes),
-        (lds_void*)(base + kUnit * kMxBlockBytes + d * kMxScaleBytes), 4, 0, 0);
   };
   const i32x4* b[FN];
   const uint32_t* bs[FN];
 #pragma unroll
   for (int j = 0; j < FN; ++j) {
     const int rb = weight_block<kGateUp, FN>(a, nt, kStreamWaves * FN, wave * FN + j);
-    b[j] = (const i32x4*)(a.b + e * a.b_expert + (int64_t)rb * KB * kFp4BlockBytes) + lane;
+    b[j] = (const i32x4*)(a.B + e * a.b_expert_bytes + (int64_t)rb * KB * kFp4BlockBytes) + lane;
     bs[j] = (const uint32_t*)(a.bs + e * a.bs_expert + (int64_t)rb * units * kFp4ScaleBytes) + lane;
   }
   f32x16 acc[1][FN];
@@ -559,21 +463,21 @@ __global__ void __launch_bounds__(64 * kStreamWaves) stream_mx(MxArgs a) {
 #pragma unroll
   for (int k = 0; k < kUnit; ++k)
     if (k < KB) load(k, w[k]);
+  int at[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) at[q] = fragment_at(lane, q);
   auto stage = [&](const char* sa, auto k_tag, const i32x4 (&x)[FN]) __attribute__((always_inline)) {
     constexpr int k = decltype(k_tag)::value;
-    i32x4 thirds[3];
+    bf16x8 row[4];
 #pragma unroll
-    for (int t = 0; t < 3; ++t)
-      thirds[t] = *(const i32x4*)(sa + k * kMxBlockBytes + t * 1024 + lane * 16);
-    const uint32_t s =
-        *(const uint32_t*)(sa + kUnit * kMxBlockBytes + k / 2 * kMxScaleBytes + lane * 4);
-    const i32x12 row = both_parts(thirds);
+    for (int q = 0; q < 4; ++q) row[q] = *(const bf16x8*)(sa + k * kRowBlockBytes + at[q]);
 #pragma unroll
-    for (int j = 0; j < FN; ++j)
-      acc[0][j] = mx_mma<0, k, 2 * (k & 1)>(x[j], sc[j], row, s, acc[0][j]);
+    for (int q = 0; q < 4; ++q)
 #pragma unroll
-    for (int j = 0; j < FN; ++j)
-      acc[0][j] = mx_mma<1, k, 2 * (k & 1)>(x[j], sc[j], row, s, acc[0][j]);
+      for (int j = 0; j < FN; ++j) {
+        const int v = x[j][q];
+        acc[0][j] = MmaBf16::mma(unpack_fp4((uint32_t)v, sc[j] >> (8 * k) & 0xffu), row[q], acc[0][j]);
+      }
   };
   const std::integral_constant<int, 0> k0{};
   const std::integral_constant<int, 1> k1{};
@@ -623,7 +527,9 @@ __global__ void __launch_bounds__(64 * kStreamWaves) stream_mx(MxArgs a) {
   }
 
   if constexpr (kGateUp) {
-    store_act<1, FN>(a, acc, tr, nt * kStreamWaves + wave, lane);
+    __syncthreads();  // every wave is done with the rows
+    store_tile_lds<true, 1, 1, FN, BM, BN, BM, 32 * FN, 64 * kStreamWaves>(a, acc, tr, nt, 0, 1, wave,
+                                                                          lane, smem);
   } else {
     store_out_rows(a, acc[0], tr, (nt * kStreamWaves + wave) * 64, lane);
   }
@@ -648,17 +554,20 @@ hipError_t launch(const MxArgs& a, int64_t rows_bound, hipStream_t st) {
   return launch_wide<kGateUp>(a, rows_bound, st);
 }
 
-// K columns; `rows` rows of an expert's weights.
-MxArgs mx_args(const Shape& s, const MxIO& io, const MxRows& rows_of_a, int K, int rows) {
+// K columns of A; `rows` rows of an expert's weights, ncols columns of C.
+MxArgs mx_args(const Shape& s, const MxIO& io, const void* rows_of_a, int K, int rows, int ncols) {
   MxArgs a{};
-  a.a = rows_of_a;
+  a.A[0] = a.A[1] = (const char*)rows_of_a;
+  a.B = (const char*)io.w;
+  a.bs = (const char*)io.w_scale;
   a.off0 = io.off[0];
   a.off1 = io.off[1];
-  a.b = (const char*)io.w;
-  a.bs = (const char*)io.w_scale;
-  a.b_expert = (int64_t)rows * K / 2;
-  a.bs_expert = fp4_scale_bytes(rows, K);
   a.E = s.E;
+  a.I = s.I;
+  a.ncols = ncols;
+  a.row_bytes = (int64_t)K * 2;
+  a.b_expert_bytes = (int64_t)rows * K / 2;
+  a.bs_expert = fp4_scale_bytes(rows, K);
   a.blocks = K / kFp4BlockCols;
   a.quads = (int)fp4_scale_quads(K);
   return a;
@@ -666,19 +575,20 @@ MxArgs mx_args(const Shape& s, const MxIO& io, const MxRows& rows_of_a, int K, i
 
 }  // namespace
 
-hipError_t launch_gate_up_mx(const Shape& s, const MxIO& io, const MxRows& x, const MxRows& act,
+hipError_t launch_gate_up_mx(const Shape& s, const MxIO& io, const void* hidden_states, void* act,
                              hipStream_t st) {
-  MxArgs a = mx_args(s, io, x, s.H, 2 * s.I);
-  a.ncols = s.I;
+  MxArgs a = mx_args(s, io, hidden_states, s.H, 2 * s.I, s.I);
+  a.gather[0] = io.gather[0];
+  a.gather[1] = io.off[1] ? io.gather[1] : io.gather[0];
+  a.gather_k = s.k;
   a.up = s.I / kFp4BlockRows;
-  a.c = act;
+  a.C[0] = a.C[1] = (uint16_t*)act;
   return launch<true>(a, io.rows_bound, st);
 }
 
-hipError_t launch_down_mx(const Shape& s, const MxIO& io, const MxRows& act, const MxRows (&y)[2],
+hipError_t launch_down_mx(const Shape& s, const MxIO& io, const void* act, const ScaledRows (&y)[2],
                           hipStream_t st) {
-  MxArgs a = mx_args(s, io, act, s.I, s.H);
-  a.ncols = s.H;
+  MxArgs a = mx_args(s, io, act, s.I, s.H, s.H);
   a.y[0] = y[0];
   a.y[1] = io.off[1] ? y[1] : y[0];
   a.c_split = io.off[1] != nullptr;

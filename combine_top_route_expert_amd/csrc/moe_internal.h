@@ -240,10 +240,10 @@ hipError_t launch_gate_up_i8(const Shape& s, const GroupedIO& io, const float* a
 hipError_t launch_down_i8(const Shape& s, const GroupedIO& io, const float* a_scale,
                           const void* w_down, const float* w_scale, hipStream_t st);
 
-// ---- layer with 4-bit experts (mx_rows.hip, gemm_fp4.hip, few_rows_mx.hip) ----------
-// Rows in two 6-bit parts (blocks, mx_rows.h), or output rows in scaled fp16: [rows][cols]
-// values and mx_out_scales(cols) bytes a row, one for each 64 columns.
-struct MxRows {
+// ---- layer with 4-bit experts (gemm_fp4.hip, combine_scaled.hip, few_rows_mx.hip) ----
+// Output rows in scaled fp16: [rows][cols] values and mx_out_scales(cols) bytes a row, one for
+// each 64 columns.
+struct ScaledRows {
   char *values, *scales;
 };
 inline __host__ __device__ int64_t mx_out_scales(int64_t cols) { return 4 * ((cols + 255) / 256); }
@@ -253,15 +253,13 @@ struct MxIO {                // the rows of a chunk, or of a pair, sorted by exp
   const int32_t* gather[2];  // the chunks' slices of src_row
   const uint8_t *w, *w_scale;
 };
-// The rows of x [T][H] (bf16) in two parts.
-hipError_t launch_split_rows(const Shape& s, const MxIO& io, const void* x, const MxRows& to,
+// act: joint rows of I bf16 values.
+hipError_t launch_gate_up_mx(const Shape& s, const MxIO& io, const void* hidden_states, void* act,
                              hipStream_t st);
-hipError_t launch_gate_up_mx(const Shape& s, const MxIO& io, const MxRows& x, const MxRows& act,
-                             hipStream_t st);
-hipError_t launch_down_mx(const Shape& s, const MxIO& io, const MxRows& act, const MxRows (&y)[2],
+hipError_t launch_down_mx(const Shape& s, const MxIO& io, const void* act, const ScaledRows (&y)[2],
                           hipStream_t st);
 // out[t] = sum over kept slots of w y (fp32 in ascending slot order, rounded once).
-hipError_t launch_combine_scaled(const Shape& s, int t0, int t_mid, int t1, const MxRows (&y)[2],
+hipError_t launch_combine_scaled(const Shape& s, int t0, int t_mid, int t1, const ScaledRows (&y)[2],
                                  const int32_t* dst_row, const float* w, void* out,
                                  hipStream_t st);
 // The whole layer with 4-bit experts for a few assignments (few_rows_mx.hip): nothing is

@@ -690,23 +690,18 @@ moe_status moe_dequantize_mx(int64_t rows, int64_t cols, int32_t dtype, const ui
  * hidden_states and out are bf16 (MOE_F32 is MOE_ERR_UNSUPPORTED), weights packed
  * matrices as above, expert after expert: w_gate_up_q and its scales E matrices of
  * [2I][H], w_down_q and its scales E of [H][I].
- * The products take their activations (hidden_states and act) as the sum of two 6-bit
- * floating point numbers (E2M3), each with a power of two for 32 consecutive values:
- * off by at most 2^-8.9 of the largest of the 32, and over them closer than a rounding to
- * bf16.  Sums are fp32; y is kept to 2^-12, out rounded to bf16 once.  Up to 32 assignments
- * (T * k, of one token or not more than there are experts) take a form that rounds neither
- * hidden_states nor y, and act to 2^-16.
- * A token that holds an infinity or a NaN gives NaN in its own output row only; so may one
- * that holds a magnitude above 1.875 * 2^127.  Dropped ids as in the calls above; results do
- * not depend on N.
+ * Products take hidden_states as they are and act rounded to bf16, sums are fp32.  y is kept in
+ * fp16 with a power of two for 64 columns of a row: to 2^-11 of each value and 2^-39 of the
+ * largest of the 64; out is rounded to bf16 once.  Up to 32 assignments (T * k, of one token or not
+ * more than there are experts) take a form that keeps act to 2^-16 and y in fp32.
+ * A token that holds an infinity or a NaN, or whose act leaves the range of bf16, gives infinities
+ * and NaN in its own output row only.  Dropped ids as in the calls above; results do not depend on N.
  * Limits: H % 64 == 0 and I % 64 == 0.
  * --------------------------------------------------------------------------- */
 
 /* Bytes of workspace moe_mx_forward needs: the metadata and, for the min(N,2) * ceil(T/N) * k
- * rows of a pair, 25/16 bytes for each of H + I values, in blocks of 32 rows of which
- * every expert may leave one in part empty (up to 50 E (H + I) bytes more), and 2H bytes of y
- * with one for each 64 of H; for the form for few assignments also 4 bytes for each of their
- * I values, where that is more.  Host-only. */
+ * rows of a pair, 2I bytes of act, and 2H of y with one for each 64 of H; for the form for few
+ * assignments 4I of act, where that is more.  Host-only. */
 moe_status moe_mx_workspace_size(const moe_shape* shape, size_t* bytes);
 
 /*
