@@ -121,7 +121,9 @@ __global__ void __launch_bounds__(64 * kWaves) few_gate_up_mx(FewMxArgs a) {
     up += sums[w][1][lane];
   }
   const float act = swiglu<true>(gate, up);
-  const __bf16 hi = (__bf16)act, lo = (__bf16)(act - (float)hi);
+  const __bf16 hi = (__bf16)act;
+  // (an infinity has no rest: inf - inf would make NaN of it)
+  const __bf16 lo = __builtin_fabsf((float)hi) < INFINITY ? (__bf16)(act - (float)hi) : (__bf16)0.0f;
   __bf16* to = (__bf16*)a.out + ((int64_t)f * groups + g) * 2 * kRows + lane;
   to[0] = hi;
   to[kRows] = lo;
