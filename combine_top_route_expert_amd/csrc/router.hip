@@ -3,7 +3,9 @@
 //
 //   score = softmax(logits) or sigmoid(logits), per token
 //   key   = the logit; with a bias or a group limit: score + bias (in 64 bits)
-//   limit: only the `limit` groups with the largest sum of their two largest keys stay
+//   limit: only the `limit` groups with the largest sum of their two largest keys stay, of which
+//          a closed expert's counts as less than any number: those with two open experts before
+//          those with one, and these before those with none
 //   ids   = the k largest keys, the larger first, ties to the lower id
 //   w_j   = factor * score of id j, or factor * score / (sum of the chosen scores)
 // A logit of -inf is never chosen; slots with no expert left get id -1 and weight 0.
@@ -194,13 +196,16 @@ __global__ void __launch_bounds__(64 * kWaves) router_top_k(RouterArgs a) {
           second = fmax(second, fmin(first, v));
           first = fmax(first, v);
         }
-      const double sum = size > 1 ? first + second : first;
-      // a group's place among them: those with more, or as much and a lower number
+      // open ones of the two, and their sum
+      const int open = (first > -(double)INFINITY ? 1 : 0) + (second > -(double)INFINITY ? 1 : 0);
+      const double sum = open == 2 ? first + second : open == 1 ? first : 0.0;
+      // a group's place among them: those with more open, then more, or as much and a lower number
       int before = 0;
       for (int g = 0; g < a.G; ++g) {
         const double o = __hiloint2double(__builtin_amdgcn_readlane(__double2hiint(sum), g),
                                           __builtin_amdgcn_readlane(__double2loint(sum), g));
-        before += o > sum || (o == sum && g < lane) ? 1 : 0;
+        const int n = __builtin_amdgcn_readlane(open, g);
+        before += n > open || (n == open && (o > sum || (o == sum && g < lane))) ? 1 : 0;
       }
       kept = __ballot(lane < a.G && before < a.limit);
 #pragma unroll

@@ -588,8 +588,10 @@ typedef enum moe_score {
  *  score         a moe_score
  *  group_limit   0: none.  Else a token's experts come from the group_limit groups (of
  *                shape's num_groups groups of E / G consecutive experts) with the
- *                largest sum of their two largest keys; num_groups <= 64
- *                (MOE_ERR_UNSUPPORTED beyond)
+ *                largest sum of their two largest keys, equal sums by the lower group;
+ *                a closed expert's key counts as less than any number, so that groups with
+ *                two open experts come before those with one, and these before those with
+ *                none; num_groups <= 64 (MOE_ERR_UNSUPPORTED beyond)
  *  renormalize   nonzero: weights are divided by the sum of the token's chosen scores
  *  factor        finite: multiplies the weights
  *  top_k_index   [T][k] int32 (out), top_k_weights [T][k] float32 (out)
