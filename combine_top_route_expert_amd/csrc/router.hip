@@ -399,7 +399,9 @@ RouterArgs router_args(const Shape& s, const RouterIO& io) {
 
 }  // namespace
 
-bool router_limit_ok(const Shape& s, int limit) { return limit <= 0 || s.G <= kMaxLimitGroups; }
+bool router_limit_ok(const Shape& s, int limit) {
+  return limit <= 0 || limit >= s.G || s.G <= kMaxLimitGroups;
+}
 
 hipError_t launch_router_top_k(const Shape& s, const RouterIO& io, hipStream_t st) {
   RouterArgs a = router_args(s, io);

@@ -586,18 +586,18 @@ typedef enum moe_score {
  *  logits        [T][E] of logits_dtype (a moe_dtype; the layer's does not matter here)
  *  bias          [E] float32, nullable: added to the scores for the choice only
  *  score         a moe_score
- *  group_limit   0: none.  Else a token's experts come from the group_limit groups (of
- *                shape's num_groups groups of E / G consecutive experts) with the
+ *  group_limit   0 or num_groups: none.  Else a token's experts come from the group_limit
+ *                groups (of shape's num_groups groups of E / G consecutive experts) with the
  *                largest sum of their two largest keys, equal sums by the lower group;
  *                a closed expert's key counts as less than any number, so that groups with
  *                two open experts come before those with one, and these before those with
- *                none; num_groups <= 64 (MOE_ERR_UNSUPPORTED beyond)
+ *                none; num_groups <= 64 under a limit (MOE_ERR_UNSUPPORTED beyond)
  *  renormalize   nonzero: weights are divided by the sum of the token's chosen scores
  *  factor        finite: multiplies the weights
  *  top_k_index   [T][k] int32 (out), top_k_weights [T][k] float32 (out)
  * The k experts with the largest keys are chosen, the larger key first, equal keys by
  * the lower id.  The key is the logit; with a bias or a group limit it is score + bias,
- * evaluated in 64 bits.  A logit of -inf, and a bias that is not finite, close the expert:
+ * evaluated in 64 bits (where the sigmoids of logits above about 37 are all 1).  A logit of -inf, and a bias that is not finite, close the expert:
  * it is never chosen, and a slot for which no expert is left has id -1 (the layer drops
  * it) and weight 0.  A token with a NaN or +inf among its logits has no order: it gets
  * ids 0, 1, ... and NaN weights, so that its output row is NaN and no other one.

@@ -89,3 +89,14 @@ def test_gradient_reaches_the_experts_that_were_left():
     want = torch.zeros(1, 8, dtype=torch.float64)
     want[0, 7], want[0, 5] = p * (1 - p), -p * (1 - p)
     assert float((grad.double().cpu() - want).abs().max()) < 16 * bo.U32
+
+
+@pytest.mark.parametrize("E,G", [(4, 2), (256, 8), (6, 1), (256, 128)])
+def test_all_groups_open_is_no_limit(E, G):
+    """With group_limit = num_groups, or none, the key is the logit: it tells sigmoids apart that are the same number in 64
+    bits.  With a bias they are equal, and the lower id comes first."""
+    x = torch.zeros(1, E, device="cuda")
+    x[0, 0], x[0, 1], x[0, 3] = 40.0, 41.0, 42.0
+    for limit in (0, G):
+        assert route(x, 3, G, None, "sigmoid", limit)[0].tolist() == [[3, 1, 0]]
+        assert route(x, 3, G, torch.zeros(E, device="cuda"), "sigmoid", limit)[0].tolist() == [[0, 1, 3]]
