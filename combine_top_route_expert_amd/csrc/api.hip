@@ -1371,14 +1371,31 @@ MxPlan mx_plan(const Shape& s) {
   return p;
 }
 
+// Shapes of the layer with 4-bit experts: bf16, and no product that one launch cannot hold.
+moe_status mx_shape(const moe_shape* shape, Shape* s) {
+  const moe_status st = resolve_shape(shape, s);
+  if (st != MOE_OK) return st;
+  if (s->dtype != MOE_BF16) return MOE_ERR_UNSUPPORTED;
+  if (few_rows_mx(*s)) return few_launches_fit_mx(*s) ? MOE_OK : MOE_ERR_UNSUPPORTED;
+  for (int c = 0; c < s->N; c += 2) {
+    int t0, t1;
+    chunk_tokens(*s, c, &t0, &t1);
+    if (c + 1 < s->N) {
+      int u0;
+      chunk_tokens(*s, c + 1, &u0, &t1);
+    }
+    if (!mx_launches_fit(*s, (int64_t)(t1 - t0) * s->k)) return MOE_ERR_UNSUPPORTED;
+  }
+  return MOE_OK;
+}
+
 }  // namespace
 }  // namespace moe
 
 moe_status moe_mx_workspace_size(const moe_shape* shape, size_t* bytes) {
   Shape s;
-  const moe_status st = resolve_shape(shape, &s);
+  const moe_status st = mx_shape(shape, &s);
   if (st != MOE_OK) return st;
-  if (s.dtype != MOE_BF16) return MOE_ERR_UNSUPPORTED;
   if (!bytes) return MOE_ERR_INVALID_ARG;
   *bytes = mx_plan(s).bytes;
   return MOE_OK;
@@ -1390,9 +1407,8 @@ moe_status moe_mx_forward(const moe_shape* shape, const void* hidden_states,
                           const uint8_t* w_down_q, const uint8_t* w_down_scale, void* out,
                           int32_t* dev_error, void* ws, size_t ws_bytes, hipStream_t stream) {
   Shape s;
-  const moe_status st = resolve_shape(shape, &s);
+  const moe_status st = mx_shape(shape, &s);
   if (st != MOE_OK) return st;
-  if (s.dtype != MOE_BF16) return MOE_ERR_UNSUPPORTED;
   if (!ws || !aligned(ws, 256) || !aligned(dev_error, 4)) return MOE_ERR_INVALID_ARG;
   const MxPlan p = mx_plan(s);
   if (ws_bytes < p.bytes) return MOE_ERR_WORKSPACE_TOO_SMALL;

@@ -86,14 +86,21 @@ hipError_t launch_combine_scaled(const Shape& s, int t0, int t_mid, int t1, cons
                                  hipStream_t st) {
   if (t1 <= t0) return hipSuccess;
   const int nvec = s.H / 8;
-  const unsigned blocks = (unsigned)((t1 - t0 + kWaves - 1) / kWaves);
   const int spans = (nvec + 64 * kVecPerLane - 1) / (64 * kVecPerLane);
   const unsigned parts = t1 - t0 <= kSplitTokens ? (unsigned)std::min(spans, 256) : 1u;
-  hipLaunchKernelGGL(combine_scaled, dim3(blocks, parts), dim3(64 * kWaves), 0, st,
-                     (const u32x4*)y[0].values, (const uint8_t*)y[0].scales,
-                     (const u32x4*)y[1].values, (const uint8_t*)y[1].scales, t_mid, dst_row, w,
-                     (u32x4*)out, t0, t1, s.k, nvec, (int)mx_out_scales(s.H));
-  return hipGetLastError();
+  // (a launch has less than 2^32 threads, 64 for every token)
+  constexpr int kMost = 1 << 25;
+  for (int64_t t = t0; t < t1; t += kMost) {
+    const int end = (int)std::min<int64_t>(t + kMost, t1);
+    const unsigned blocks = (unsigned)((end - t + kWaves - 1) / kWaves);
+    hipLaunchKernelGGL(combine_scaled, dim3(blocks, parts), dim3(64 * kWaves), 0, st,
+                       (const u32x4*)y[0].values, (const uint8_t*)y[0].scales,
+                       (const u32x4*)y[1].values, (const uint8_t*)y[1].scales, t_mid, dst_row, w,
+                       (u32x4*)out, (int)t, end, s.k, nvec, (int)mx_out_scales(s.H));
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 }  // namespace moe

@@ -169,6 +169,11 @@ __global__ void __launch_bounds__(64 * kWaves) few_down_mx(FewMxArgs a) {
 //   E = 8, H = 4096, I = 2048, k = 2:  2: 67 / 24;  E = 16, H = I = 2880, k = 4:  16: 80 / 70
 bool few_rows_mx(const Shape& s) { return s.A > 0 && s.A <= 32 && (s.T == 1 || s.A <= s.E); }
 
+bool few_launches_fit_mx(const Shape& s) {
+  constexpr int64_t most = 0x7fffffff / (64 * kWaves);
+  return s.A * (s.I / kRows) <= most && (int64_t)s.T * (s.H / kRows) <= most;
+}
+
 hipError_t launch_few_mx(const Shape& s, const void* hidden_states, const int32_t* top_k_index,
                          const float* top_k_weights, const uint8_t* w_gate_up_q,
                          const uint8_t* w_gate_up_scale, const uint8_t* w_down_q,
@@ -202,8 +207,6 @@ hipError_t launch_few_mx(const Shape& s, const void* hidden_states, const int32_
   d.blocks = s.I / kFp4BlockCols;
   d.quads = (int)fp4_scale_quads(s.I);
   const int64_t gate = s.A * (s.I / kRows), down = (int64_t)s.T * (s.H / kRows);
-  if (gate > 0x7fffffff / (64 * kWaves) || down > 0x7fffffff / (64 * kWaves))
-    return hipErrorInvalidConfiguration;
   hipLaunchKernelGGL(few_gate_up_mx, dim3((unsigned)gate), dim3(64 * kWaves), 0, st, g);
   hipLaunchKernelGGL(few_down_mx, dim3((unsigned)down), dim3(64 * kWaves), 0, st, d);
   return hipGetLastError();

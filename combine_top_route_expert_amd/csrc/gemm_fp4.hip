@@ -385,17 +385,6 @@ __global__ void __launch_bounds__(64 * kWaves, 1) grouped_gemm_mx(MxArgs a) {
     run(std::integral_constant<int, 4>{});
 }
 
-template <bool kGateUp>
-hipError_t launch_wide(MxArgs a, int64_t rows_bound, hipStream_t st) {
-  constexpr int cols = kWaves * kWideFN * (kGateUp ? 16 : 32);
-  a.n_tiles = (a.ncols + cols - 1) / cols;
-  const int64_t grid = xcd_grid(m_tiles_bound(rows_bound, a.E, kWideRows), a.n_tiles);
-  if (grid <= 0) return hipSuccess;
-  if (grid > 0x7fffffff / (64 * kWaves)) return hipErrorInvalidConfiguration;
-  hipLaunchKernelGGL(grouped_gemm_mx<kGateUp>, dim3((unsigned)grid), dim3(64 * kWaves), 0, st, a);
-  return hipGetLastError();
-}
-
 // ---------------------------------------------------------------- few rows an expert
 // Products with up to 32 rows a tile, bound by streaming the weights: every wave reads its own
 // 64 weight rows (gate_up: 32 gate rows and their up rows) straight into registers, a unit of
@@ -535,23 +524,32 @@ __global__ void __launch_bounds__(64 * kStreamWaves) stream_mx(MxArgs a) {
   }
 }
 
-template <bool kGateUp>
-hipError_t launch_stream(MxArgs a, int64_t rows_bound, hipStream_t st) {
-  constexpr int cols = kStreamWaves * (kGateUp ? 32 : 64);
-  a.n_tiles = (a.ncols + cols - 1) / cols;
-  const int64_t grid = xcd_grid(m_tiles_bound(rows_bound, a.E, 32), a.n_tiles);
-  if (grid <= 0) return hipSuccess;
-  if (grid > 0x7fffffff / (64 * kStreamWaves)) return hipErrorInvalidConfiguration;
-  hipLaunchKernelGGL((stream_mx<kGateUp>), dim3((unsigned)grid), dim3(64 * kStreamWaves), 0, st,
-                     a);
-  return hipGetLastError();
+// Form, column tiles and workgroups of one product.
+struct MxLaunch {
+  bool stream;
+  int n_tiles;
+  int64_t grid;
+};
+MxLaunch mx_launch(bool gate_up, int64_t rows_bound, int E, int ncols) {
+  MxLaunch l;
+  l.stream = rows_bound <= (int64_t)kStreamRows * E;
+  const int cols = (l.stream ? kStreamWaves * 64 : kWaves * kWideFN * 32) / (gate_up ? 2 : 1);
+  l.n_tiles = (int)(((int64_t)ncols + cols - 1) / cols);
+  l.grid = xcd_grid(m_tiles_bound(rows_bound, E, l.stream ? 32 : kWideRows), l.n_tiles);
+  return l;
 }
 
 template <bool kGateUp>
-hipError_t launch(const MxArgs& a, int64_t rows_bound, hipStream_t st) {
+hipError_t launch(MxArgs a, int64_t rows_bound, hipStream_t st) {
   if (rows_bound <= 0) return hipSuccess;
-  if (rows_bound <= (int64_t)kStreamRows * a.E) return launch_stream<kGateUp>(a, rows_bound, st);
-  return launch_wide<kGateUp>(a, rows_bound, st);
+  const MxLaunch l = mx_launch(kGateUp, rows_bound, a.E, a.ncols);
+  a.n_tiles = l.n_tiles;
+  const dim3 grid((unsigned)l.grid);  // (in range: mx_launches_fit)
+  if (l.stream)
+    hipLaunchKernelGGL(stream_mx<kGateUp>, grid, dim3(64 * kStreamWaves), 0, st, a);
+  else
+    hipLaunchKernelGGL(grouped_gemm_mx<kGateUp>, grid, dim3(64 * kWaves), 0, st, a);
+  return hipGetLastError();
 }
 
 // K columns of A; `rows` rows of an expert's weights, ncols columns of C.
@@ -574,6 +572,13 @@ MxArgs mx_args(const Shape& s, const MxIO& io, const void* rows_of_a, int K, int
 }
 
 }  // namespace
+
+bool mx_launches_fit(const Shape& s, int64_t rows_bound) {
+  constexpr int threads = 64 * kWaves;
+  static_assert(kStreamWaves == kWaves, "one limit for both forms");
+  return mx_launch(true, rows_bound, s.E, s.I).grid <= 0x7fffffff / threads &&
+         mx_launch(false, rows_bound, s.E, s.H).grid <= 0x7fffffff / threads;
+}
 
 hipError_t launch_gate_up_mx(const Shape& s, const MxIO& io, const void* hidden_states, void* act,
                              hipStream_t st) {

@@ -21,6 +21,7 @@
 // of a wave's maximum, one after the other, take the time.  64 tokens, 8 of 256 experts by
 // sigmoid with a bias and a group limit: 6.4 us, a launch's latency and the rounds; 16384
 // tokens, 8 of 128 experts: 10.6 us for 5 MB.
+#include <algorithm>
 #include <type_traits>
 
 #include "wave.h"
@@ -397,6 +398,26 @@ RouterArgs router_args(const Shape& s, const RouterIO& io) {
   return a;
 }
 
+// A launch has less than 2^32 threads, 64 for every token: launch(first, tokens) for at most
+// kMostTokens of them at a time, with the arguments of the first.
+constexpr int kMostTokens = 1 << 25;
+template <class F>
+hipError_t in_launches(const RouterArgs& all, bool bf16, F launch) {
+  for (int64_t t = 0; t < all.T; t += kMostTokens) {
+    RouterArgs a = all;
+    const int64_t logits = t * all.E * (bf16 ? 2 : 4), slots = t * all.k;
+    a.T = (int)std::min<int64_t>(all.T - t, kMostTokens);
+    a.logits = (const char*)all.logits + logits;
+    a.idx = all.idx + slots;
+    if (all.w) a.w = all.w + slots;
+    if (all.grad_w) a.grad_w = all.grad_w + slots;
+    if (all.grad) a.grad = (char*)all.grad + logits;
+    const hipError_t e = launch(a, dim3((unsigned)((a.T + kWaves - 1) / kWaves)));
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
 }  // namespace
 
 bool router_limit_ok(const Shape& s, int limit) {
@@ -407,14 +428,15 @@ hipError_t launch_router_top_k(const Shape& s, const RouterIO& io, hipStream_t s
   RouterArgs a = router_args(s, io);
   if (a.limit >= a.G) a.limit = 0;  // every group stays
   const bool scored = a.bias || a.limit > 0;
-  const dim3 grid((unsigned)((s.T + kWaves - 1) / kWaves)), block(64 * kWaves);
   const size_t lds = a.limit > 0 ? sizeof(double) * kWaves * s.E : 0;
   return with_layout(s.E, io.bf16, [&](auto r, auto bf16, auto vec) {
     constexpr int R = decltype(r)::value;
     constexpr bool B = decltype(bf16)::value, V = decltype(vec)::value;
     auto go = [&](auto kernel) {
-      hipLaunchKernelGGL(kernel, grid, block, lds, st, a);
-      return hipGetLastError();
+      return in_launches(a, io.bf16, [&](const RouterArgs& part, dim3 grid) {
+        hipLaunchKernelGGL(kernel, grid, dim3(64 * kWaves), lds, st, part);
+        return hipGetLastError();
+      });
     };
     if (io.sigmoid)
       return scored ? go(router_top_k<R, B, V, true, true>) : go(router_top_k<R, B, V, true, false>);
@@ -424,13 +446,14 @@ hipError_t launch_router_top_k(const Shape& s, const RouterIO& io, hipStream_t s
 
 hipError_t launch_router_top_k_backward(const Shape& s, const RouterIO& io, hipStream_t st) {
   const RouterArgs a = router_args(s, io);
-  const dim3 grid((unsigned)((s.T + kWaves - 1) / kWaves)), block(64 * kWaves);
   return with_layout(s.E, io.bf16, [&](auto r, auto bf16, auto vec) {
     constexpr int R = decltype(r)::value;
     constexpr bool B = decltype(bf16)::value, V = decltype(vec)::value;
     auto go = [&](auto kernel) {
-      hipLaunchKernelGGL(kernel, grid, block, 0, st, a);
-      return hipGetLastError();
+      return in_launches(a, io.bf16, [&](const RouterArgs& part, dim3 grid) {
+        hipLaunchKernelGGL(kernel, grid, dim3(64 * kWaves), 0, st, part);
+        return hipGetLastError();
+      });
     };
     return io.sigmoid ? go(router_top_k_backward<R, B, V, true>)
                       : go(router_top_k_backward<R, B, V, false>);

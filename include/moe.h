@@ -698,7 +698,9 @@ moe_status moe_dequantize_mx(int64_t rows, int64_t cols, int32_t dtype, const ui
  * more than there are experts) take a form that keeps act to 2^-16 and y in fp32.
  * A token that holds an infinity or a NaN, or whose act leaves the range of bf16, gives infinities
  * and NaN in its own output row only.  Dropped ids as in the calls above; results do not depend on N.
- * Limits: H % 64 == 0 and I % 64 == 0.
+ * Limits: H % 64 == 0 and I % 64 == 0; each product of a pair has to fit one launch (2^23
+ * workgroups of 128 rows by 512 columns, or 32 by 256 for few rows an expert), else
+ * MOE_ERR_UNSUPPORTED from either call.
  * --------------------------------------------------------------------------- */
 
 /* Bytes of workspace moe_mx_forward needs: the metadata and, for the min(N,2) * ceil(T/N) * k
