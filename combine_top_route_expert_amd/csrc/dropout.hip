@@ -41,55 +41,56 @@ __device__ __forceinline__ u32x4 philox(uint64_t v, uint64_t offset, uint64_t ke
 }
 
 constexpr int kThreads = 256;
-constexpr int kGroups = 2;  // 8-element groups a thread holds at a time
+constexpr int kGroups = 2;  // 8-element groups of a thread
+// Elements of a launch (4 M threads).  A thread that took several passes over a larger tensor
+// would cost 10% of 2^29 elements' time.
+constexpr int64_t kMostElements = (int64_t)1 << 30;
 
-// n elements (a multiple of 4).  out may be x or residual: a thread reads its
-// groups before it writes them.
+// n elements (a multiple of 4) from x on, the first of them in group `first` of the tensor.  out
+// may be x or residual: a thread reads its groups before it writes them.
 template <bool kBf16, bool kResidual>
 __global__ void __launch_bounds__(kThreads)
 dropout_add(const u32x4* x, const u32x4* residual, const uint64_t* seed_offset, uint32_t least,
-            float factor, u32x4* out, int64_t n) {
+            float factor, u32x4* out, int64_t n, int64_t first) {
   constexpr int kEl = kVecEl<kBf16>, kVecs = 8 / kEl;
   const uint64_t seed = seed_offset[0], offset = seed_offset[1];
-  const int64_t groups = (n + 7) / 8, step = (int64_t)gridDim.x * kThreads * kGroups;
+  const int64_t groups = (n + 7) / 8;
   const int64_t nvec = n / kEl;  // (fp32: the last group may be half a one)
-  for (int64_t g0 = (int64_t)blockIdx.x * kThreads * kGroups + threadIdx.x; g0 < groups;
-       g0 += step) {
-    u32x4 a[kGroups][kVecs], r[kGroups][kVecs];
+  const int64_t g0 = (int64_t)blockIdx.x * kThreads * kGroups + threadIdx.x;
+  u32x4 a[kGroups][kVecs], r[kGroups][kVecs];
 #pragma unroll
-    for (int i = 0; i < kGroups; ++i)
+  for (int i = 0; i < kGroups; ++i)
 #pragma unroll
-      for (int q = 0; q < kVecs; ++q) {
-        const int64_t v = (g0 + (int64_t)i * kThreads) * kVecs + q;
-        if (v < nvec) {
-          a[i][q] = __builtin_nontemporal_load(x + v);
-          if constexpr (kResidual) r[i][q] = __builtin_nontemporal_load(residual + v);
-        }
+    for (int q = 0; q < kVecs; ++q) {
+      const int64_t v = (g0 + (int64_t)i * kThreads) * kVecs + q;
+      if (v < nvec) {
+        a[i][q] = __builtin_nontemporal_load(x + v);
+        if constexpr (kResidual) r[i][q] = __builtin_nontemporal_load(residual + v);
       }
+    }
 #pragma unroll
-    for (int i = 0; i < kGroups; ++i) {
-      const int64_t g = g0 + (int64_t)i * kThreads;
-      if (g >= groups) break;
-      const u32x4 bits = philox((uint64_t)g, offset, seed);
+  for (int i = 0; i < kGroups; ++i) {
+    const int64_t g = g0 + (int64_t)i * kThreads;
+    if (g >= groups) break;
+    const u32x4 bits = philox((uint64_t)(first + g), offset, seed);
 #pragma unroll
-      for (int q = 0; q < kVecs; ++q) {
-        const int64_t v = g * kVecs + q;
-        if (v >= nvec) break;
-        float f[kEl], base[kEl];
-        unpack<kBf16>(a[i][q], f);
-        if constexpr (kResidual) unpack<kBf16>(r[i][q], base);
+    for (int q = 0; q < kVecs; ++q) {
+      const int64_t v = g * kVecs + q;
+      if (v >= nvec) break;
+      float f[kEl], base[kEl];
+      unpack<kBf16>(a[i][q], f);
+      if constexpr (kResidual) unpack<kBf16>(r[i][q], base);
 #pragma unroll
-        for (int j = 0; j < kEl; ++j) {
-          const int e = q * kEl + j;
-          const uint32_t half = e & 1 ? bits[e / 2] >> 16 : bits[e / 2] & 0xffffu;
-          // what is dropped is not multiplied: an infinity there leaves no NaN
-          if constexpr (kResidual)
-            f[j] = half >= least ? __builtin_fmaf(f[j], factor, base[j]) : base[j];
-          else
-            f[j] = half >= least ? f[j] * factor : 0.0f;
-        }
-        __builtin_nontemporal_store(pack<kBf16>(f), out + v);
+      for (int j = 0; j < kEl; ++j) {
+        const int e = q * kEl + j;
+        const uint32_t half = e & 1 ? bits[e / 2] >> 16 : bits[e / 2] & 0xffffu;
+        // what is dropped is not multiplied: an infinity there leaves no NaN
+        if constexpr (kResidual)
+          f[j] = half >= least ? __builtin_fmaf(f[j], factor, base[j]) : base[j];
+        else
+          f[j] = half >= least ? f[j] * factor : 0.0f;
       }
+      __builtin_nontemporal_store(pack<kBf16>(f), out + v);
     }
   }
 }
@@ -103,13 +104,18 @@ hipError_t launch_dropout_add(const Shape& s, const void* x, const void* residua
   // p in 16 bits: the least half that is kept (something always is)
   const uint32_t least = (uint32_t)std::min(65535.0, __builtin_rint(p * 65536.0));
   const float factor = 65536.0f / (float)(65536u - least);
-  const int64_t groups = (n + 7) / 8;
-  const int64_t blocks = (groups + kThreads * kGroups - 1) / (kThreads * kGroups);
-  const dim3 grid((unsigned)std::min<int64_t>(blocks, 1 << 22)), block(kThreads);
   auto go = [&](auto kernel) {
-    hipLaunchKernelGGL(kernel, grid, block, 0, st, (const u32x4*)x, (const u32x4*)residual,
-                       seed_offset, least, factor, (u32x4*)out, n);
-    return hipGetLastError();
+    for (int64_t at = 0; at < n; at += kMostElements) {
+      const int64_t left = std::min(n - at, kMostElements), bytes = at * s.elem;
+      const int64_t blocks = ((left + 7) / 8 + kThreads * kGroups - 1) / (kThreads * kGroups);
+      const char* res = residual ? (const char*)residual + bytes : nullptr;
+      hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(kThreads), 0, st,
+                         (const u32x4*)((const char*)x + bytes), (const u32x4*)res, seed_offset, least,
+                         factor, (u32x4*)((char*)out + bytes), left, at / 8);
+      const hipError_t e = hipGetLastError();
+      if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
   };
   if (s.dtype == MOE_BF16)
     return residual ? go(dropout_add<true, true>) : go(dropout_add<true, false>);

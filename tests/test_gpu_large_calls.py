@@ -1,7 +1,9 @@
-"""More tokens than one launch of a kernel that takes 64 threads for each can hold."""
+"""Calls that are run in several launches: tokens of which one launch of a wave for each holds 2^25, dropout of more than 2^30
+elements."""
 import pytest
 import torch
 
+import block_oracle as bo
 import combine_top_route_expert_amd as moe
 from gpu_layer import say
 
@@ -69,3 +71,28 @@ def test_4bit_layer():
         assert bool(((out[:, c].float() - ref).abs() <= bound).all())
     first, last = out[: 1 << 20], out[-(1 << 20):]
     assert bool((first == first[:, :1]).all()) and bool((last == last[:, :1]).all())
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_dropout(dtype):
+    """The mask goes on where one launch ends: stretches on both sides of it, and the last elements, against the generator."""
+    T, H = (1 << 22) + 3, 256
+    say(f"dropout of {T} x {H} {dtype}")
+    s = moe.make_shape(T, H, 1, 1, 64, 1, 1, "bf16" if dtype is torch.bfloat16 else "f32")
+    x = torch.ones(T, H, dtype=dtype, device="cuda")
+    so = torch.tensor([99, 7], device="cuda")
+    for residual in (None, x):
+        out = torch.full_like(x, float("nan"))
+        moe.moe_dropout_add(s, x, residual, 0.25, so, out)
+        scale = 65536 / (65536 - 16384)
+        base = 0.0 if residual is None else 1.0
+        # the factor 4/3 is rounded to float32 (U of it) before its product with 1 is added to the base (one rounding)
+        half = 2.0 ** -8 if dtype is torch.bfloat16 else bo.U32
+        bound = bo.U32 * scale + half * (scale + base)
+        got = out.view(-1)
+        for first in (0, (1 << 27) - 20, 1 << 27, (1 << 27) + 3, T * H // 8 - 40):
+            want = torch.from_numpy(bo.kept_mask(320, 0.25, 99, 7, first)).cuda()
+            ref = base + scale * want.double()
+            off = (got[8 * first: 8 * first + 320].double() - ref).abs()
+            assert bool((off <= torch.where(want, bound, 0.0)).all()), first
+        del out, got
