@@ -1376,7 +1376,7 @@ moe_status mx_shape(const moe_shape* shape, Shape* s) {
   const moe_status st = resolve_shape(shape, s);
   if (st != MOE_OK) return st;
   if (s->dtype != MOE_BF16) return MOE_ERR_UNSUPPORTED;
-  if (few_rows_mx(*s)) return few_launches_fit_mx(*s) ? MOE_OK : MOE_ERR_UNSUPPORTED;
+  if (few_rows_mx(*s)) return MOE_OK;
   for (int c = 0; c < s->N; c += 2) {
     int t0, t1;
     chunk_tokens(*s, c, &t0, &t1);

@@ -27,9 +27,9 @@ namespace moe {
 
 namespace {
 
-constexpr int kUnit = 4;                        // blocks
+constexpr int kUnit = 4;   // blocks
 constexpr int kWaves = 8;  // waves of a workgroup
-constexpr int kRows = 32;                       // weight rows of a block
+constexpr int kRows = 32;  // weight rows of a block
 
 struct FewMxArgs {
   const void* x;  // gate_up: hidden states [T][H] bf16; down: act [T*k][I / 32][2][32] bf16
@@ -98,7 +98,7 @@ __global__ void __launch_bounds__(64 * kWaves) few_gate_up_mx(FewMxArgs a) {
   const int groups = a.ncols / kRows;
   const int f = blockIdx.x / groups, g = blockIdx.x % groups;
   if (blockIdx.x == 0 && wave == 0) {
-    // at most 64 assignments, one per lane
+    // at most 32 assignments, one per lane
     const int id = lane < a.rows ? a.idx[lane] : 0;
     const int dropped = __popcll(__ballot(lane < a.rows && (id < 0 || id >= a.E)));
     if (lane == 0) *a.dev_error = dropped;
@@ -162,16 +162,19 @@ __global__ void __launch_bounds__(64 * kWaves) few_down_mx(FewMxArgs a) {
 }  // namespace
 
 // At most 32 assignments, and no more than there are experts (those of one token are distinct
-// in any case): an expert that several assignments share is read for each of them.  Whole
-// layer in us, sorted streaming tiles / this form:
-//   E = 64, H = 2048, I = 1024, k = 4: 4 assignments 48 / 19, 16: 50 / 25, 32: 54 / 38, 64: 61 / 64
-//   E = 256, H = 7168, I = 2048, k = 8: 8 assignments 97 / 58, 32: 171 / 181, 64: 315 / 336
-//   E = 8, H = 4096, I = 2048, k = 2:  2: 67 / 24;  E = 16, H = I = 2880, k = 4:  16: 80 / 70
-bool few_rows_mx(const Shape& s) { return s.A > 0 && s.A <= 32 && (s.T == 1 || s.A <= s.E); }
-
-bool few_launches_fit_mx(const Shape& s) {
-  constexpr int64_t most = 0x7fffffff / (64 * kWaves);
-  return s.A * (s.I / kRows) <= most && (int64_t)s.T * (s.H / kRows) <= most;
+// in any case): an expert that several assignments share is read for each of them.  And at most
+// 512 MB of weights to read, counted for every assignment: beyond that what the sorted form's
+// launches cost is less than what its loads gain.  Whole layer in us, sorted streaming tiles / this
+// form:
+//   E = 64, H = 2048, I = 1024, k = 4 (3.3 MB an expert): 4 assignments 40 / 19, 16: 44 / 26, 32: 48 / 38
+//   E = 128, H = 4096, I = 1536, k = 8 (10 MB): 32 assignments 93 / 91
+//   E = 160, H = 5120, I = 2048, k = 8 (17 MB): 24: 113 / 107, 32: 121 / 143
+//   E = 256, H = 7168, I = 2048, k = 8 (23 MB): 8: 90 / 59, 16: 107 / 95, 24: 142 / 143, 32: 166 / 181
+//   E = 64, H = 8192, I = 4096 (53 MB): 8: 123 / 114, 12: 166 / 162
+//   E = 8, H = 4096, I = 2048, k = 2:  2: 60 / 24;  E = 16, H = I = 2880, k = 4:  16: 74 / 68, 32: 75 / 114
+bool few_rows_mx(const Shape& s) {
+  const double bytes = 3.0 * s.H * s.I * 17 / 32 * s.A;
+  return s.A > 0 && s.A <= 32 && (s.T == 1 || s.A <= s.E) && bytes <= 0x1p29;
 }
 
 hipError_t launch_few_mx(const Shape& s, const void* hidden_states, const int32_t* top_k_index,
@@ -206,6 +209,7 @@ hipError_t launch_few_mx(const Shape& s, const void* hidden_states, const int32_
   d.ncols = s.H;
   d.blocks = s.I / kFp4BlockCols;
   d.quads = (int)fp4_scale_quads(s.I);
+  // (few workgroups: at most 512 MB of weights, of which each reads a kilobyte or more)
   const int64_t gate = s.A * (s.I / kRows), down = (int64_t)s.T * (s.H / kRows);
   hipLaunchKernelGGL(few_gate_up_mx, dim3((unsigned)gate), dim3(64 * kWaves), 0, st, g);
   hipLaunchKernelGGL(few_down_mx, dim3((unsigned)down), dim3(64 * kWaves), 0, st, d);

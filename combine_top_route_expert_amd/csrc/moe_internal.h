@@ -267,7 +267,6 @@ hipError_t launch_combine_scaled(const Shape& s, int t0, int t_mid, int t1, cons
 // The whole layer with 4-bit experts for a few assignments (few_rows_mx.hip): nothing is
 // sorted, act holds row f for assignment f, four bytes a value; also counts the dropped ids.
 bool few_rows_mx(const Shape& s);
-bool few_launches_fit_mx(const Shape& s);
 hipError_t launch_few_mx(const Shape& s, const void* hidden_states, const int32_t* top_k_index,
                          const float* top_k_weights, const uint8_t* w_gate_up_q,
                          const uint8_t* w_gate_up_scale, const uint8_t* w_down_q,

@@ -695,7 +695,8 @@ moe_status moe_dequantize_mx(int64_t rows, int64_t cols, int32_t dtype, const ui
  * Products take hidden_states as they are and act rounded to bf16, sums are fp32.  y is kept in
  * fp16 with a power of two for 64 columns of a row: to 2^-11 of each value and 2^-39 of the
  * largest of the 64; out is rounded to bf16 once.  Up to 32 assignments (T * k, of one token or not
- * more than there are experts) take a form that keeps act to 2^-16 and y in fp32.
+ * more than there are experts) with up to 512 MB of weights, counted for each, take a form that
+ * keeps act to 2^-16 and y in fp32.
  * A token that holds an infinity or a NaN, or whose act leaves the range of bf16, gives infinities
  * and NaN in its own output row only.  Dropped ids as in the calls above; results do not depend on N.
  * Limits: H % 64 == 0 and I % 64 == 0; each product of a pair has to fit one launch (2^23

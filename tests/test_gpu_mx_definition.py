@@ -27,11 +27,12 @@ def _gpu():
     moe.load_library()
 
 
-def definition(c: Case, x=None):
-    """(values in float64, bound of what the library's float32 sums and roundings may be off)."""
+def definition(c: Case, x=None, few_form=None):
+    """(values in float64, bound of what the library's float32 sums and roundings may be off); few_form: whether the layer
+    takes the form for a few assignments, None for small experts."""
     s = c.shape
     x = c.x if x is None else x
-    if few(s):
+    if few(s) if few_form is None else few_form:
         return few_reference(c, x)
     ref = torch.zeros(s.T, s.H, dtype=torch.float64, device="cuda")
     err = torch.zeros_like(ref)
@@ -84,6 +85,21 @@ def test_few_assignments(T, H, E, k, I):  # noqa: E741
     c.idx[0, 0], c.idx[T - 1, k - 1] = -3, E
     within(c.forward(), *definition(c), "out")
     assert int(c.err.item()) == (1 if T * k == 1 else 2)
+
+
+@pytest.mark.parametrize("T,few_form", [(2, True), (5, True), (6, False), (8, False)])
+def test_few_assignments_of_large_experts(T, few_form):
+    """23 MB an expert: up to 512 MB, 22 assignments, unsorted; of more, whose error shows act's rounding, sorted."""
+    H, E, k, I = 7168, 32, 4, 2048  # noqa: E741
+    say(f"4-bit experts, {T * k} assignments of large experts")
+    c = Case(T, H, E, k, I, seed=T)
+    got = c.forward()
+    ref, err = definition(c, few_form=few_form)
+    within(got, ref, err, "out")
+    off = norm_error(got, ref)
+    assert off <= (TWO_ROUNDINGS if not few_form else 1.1 * 1.66e-3), off
+    assert few_form or off > 1.1 * 1.66e-3, off
+    assert int(c.err.item()) == 0
 
 
 @pytest.mark.parametrize("few_rows", [True, False])
