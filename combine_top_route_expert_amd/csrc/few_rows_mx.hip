@@ -5,8 +5,7 @@
 // A wave multiplies 32 weight rows by 256 columns at a time (a unit: four kilobytes and
 // their scales, from one or two places), all of whose loads it issues at once; the units of
 // K, and in few_down those of the slots, are dealt to the waves.  The weights are converted to
-// bf16 (exactly, unless a group's power is below 2^-126) and multiplied by matrix instructions
-// of which one row, or two, are filled: only the lanes that hold those load any of x, where
+// bf16 (exactly, subnormal ones too) and multiplied by matrix instructions of which one row, or two, are filled: only the lanes that hold those load any of x, where
 // a dot product of a lane's 32 columns needs the whole row's in every lane (with v_dot2_f32_bf16
 // 19.6 us for the token below instead of 18.9, 187 instead of 181 for four of them with 8 experts
 // of H = 7168, I = 2048; with single multiply-adds 20 and 195).  act is kept as two bf16

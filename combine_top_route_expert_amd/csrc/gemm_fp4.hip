@@ -393,7 +393,11 @@ __global__ void __launch_bounds__(64 * kWaves, 1) grouped_gemm_mx(MxArgs a) {
 // Of an H = 7168, I = 2048 layer with 64 tokens on 8 of 256 experts (2 rows each) gate_up
 // reads 3.4 GB in 571 us and down 1.7 in 302, 5.9 and 5.6 TB/s (a plain read of such weights: 6.8).
 constexpr int kStreamWaves = 4;
-// Rows an expert, on average, up to which these products are taken.
+// Rows an expert, on average (dropped ids count as rows: the host does not know them), up to which
+// these products are taken.  That layer in ms, these and the wide ones: 1 row (an expert that has
+// any) 0.44 and 0.52, 2 rows 0.89 and 0.96, 8 rows 1.08 and 1.11, 16 rows 1.12 and 1.16, 32 rows
+// 1.61 and 1.31; with H = 4096, I = 1024, 128 experts 32 rows 0.26 and 0.23; with H = 2048,
+// I = 1024, 64 experts 4 rows 0.065 and 0.061, 32 rows 0.084 and 0.073.
 constexpr int kStreamRows = 24;
 
 template <bool kGateUp>

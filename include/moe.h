@@ -676,13 +676,14 @@ moe_status moe_quantize_mx(int64_t rows, int64_t cols, int32_t dtype, const void
                             uint8_t* scale, hipStream_t stream);
 
 /* Packs a matrix that is already in 4 bits, row by row: q_rows [rows][cols/2] (even column in
- * the low half), scale_rows [rows][cols/32].  Limits as for moe_quantize_mx. */
+ * the low half), scale_rows [rows][cols/32].  Limits as for moe_quantize_mx; none of the four may
+ * overlap another. */
 moe_status moe_pack_mx(int64_t rows, int64_t cols, const uint8_t* q_rows,
                         const uint8_t* scale_rows, uint8_t* q, uint8_t* scale,
                         hipStream_t stream);
 
 /* The values of a packed matrix as x [rows][cols] of dtype: exact.  Limits as for
- * moe_quantize_mx. */
+ * moe_quantize_mx; x may not overlap q or scale. */
 moe_status moe_dequantize_mx(int64_t rows, int64_t cols, int32_t dtype, const uint8_t* q,
                               const uint8_t* scale, void* x, hipStream_t stream);
 

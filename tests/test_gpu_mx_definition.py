@@ -221,6 +221,53 @@ def test_rows_in_another_order_stay_the_same():
     assert torch.equal(c.forward(x=c.x[at].contiguous()), want[at])
 
 
+@pytest.mark.parametrize("T", [8, 60, 700])
+def test_the_smallest_weights(T):
+    """Groups with the power 2^-127: their values are subnormal numbers of bf16, and as exact as others."""
+    E, H, I = 16, 128, 64  # noqa: E741
+    c = Case(T, H, E, 2, I, 1, seed=T)
+    codes = torch.randint(0, 256, (E * 2 * I * H // 2,), generator=gen(T), device="cuda", dtype=torch.uint8)
+    c.wgu, c.wgus = codes, torch.zeros_like(c.wgus)
+    moe.moe_dequantize_mx(E * 2 * I, H, "f32", c.wgu, c.wgus, c.vgu)
+    assert 0.0 < float(c.vgu.abs().max()) <= 6 * 2.0 ** -127
+    x = (c.x.float() * 2.0 ** 125).to(BF16)
+    check(c, x)
+
+
+@pytest.mark.parametrize("T", [4, 60, 2100])
+def test_two_layers_at_once(T):
+    """Two streams, each with its own rows, workspace and output, over the same weights; eager and as two graphs."""
+    c = Case(T, 320, 8, 2, 192, 2, seed=T)
+    xs = [c.x, (c.x.float() * 2 + 1).to(BF16)]
+    want = [c.forward(x=x) for x in xs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in xs]
+    size = moe.moe_mx_workspace_size(c.shape)
+    ws = [torch.empty(size, dtype=torch.uint8, device="cuda") for _ in xs]
+    out = [torch.empty_like(w) for w in want]
+    err = [torch.empty(1, dtype=torch.int32, device="cuda") for _ in xs]
+
+    def layer(i, stream=None):
+        moe.moe_mx_forward(c.shape, xs[i], c.idx, c.w, c.wgu, c.wgus, c.wd, c.wds, out[i], ws[i], err[i], stream)
+
+    graphs = []
+    for i, side in enumerate(streams):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            layer(i)
+        graphs.append(graph)
+    for go in (lambda i: layer(i, streams[i]), lambda i: graphs[i].replay()):
+        for _ in range(4):
+            for o in out:
+                o.fill_(float("nan"))
+            torch.cuda.synchronize()
+            for i, side in enumerate(streams):
+                with torch.cuda.stream(side):
+                    go(i)
+            torch.cuda.synchronize()
+            assert torch.equal(out[0], want[0]) and torch.equal(out[1], want[1])
+
+
 def test_block_as_it_is_served():
     """Norm, router on its rows, the 4-bit layer, its output into the residual stream; eager, then captured and replayed with other
     rows and with eager work between."""
