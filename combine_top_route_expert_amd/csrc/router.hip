@@ -197,16 +197,24 @@ __global__ void __launch_bounds__(64 * kWaves) router_top_k(RouterArgs a) {
           second = fmax(second, fmin(first, v));
           first = fmax(first, v);
         }
-      // open ones of the two, and their sum
-      const int open = (first > -(double)INFINITY ? 1 : 0) + (second > -(double)INFINITY ? 1 : 0);
-      const double sum = open == 2 ? first + second : open == 1 ? first : 0.0;
-      // a group's place among them: those with more open, then more, or as much and a lower number
-      int before = 0;
-      for (int g = 0; g < a.G; ++g) {
-        const double o = __hiloint2double(__builtin_amdgcn_readlane(__double2hiint(sum), g),
-                                          __builtin_amdgcn_readlane(__double2loint(sum), g));
-        const int n = __builtin_amdgcn_readlane(open, g);
-        before += n > open || (n == open && (o > sum || (o == sum && g < lane))) ? 1 : 0;
+      double sum = size > 1 ? first + second : first;
+      int before = 0;  // groups that come before the lane's
+      // where a group has a closed expert among its two, those with more open ones come first
+      if (size > 1 && __ballot(lane < a.G && sum == -(double)INFINITY) != 0) {
+        const int open = (first > -(double)INFINITY ? 1 : 0) + (second > -(double)INFINITY ? 1 : 0);
+        if (open < 2) sum = open == 1 ? first : 0.0;
+        for (int g = 0; g < a.G; ++g) {
+          const int n = __builtin_amdgcn_readlane(open, g);
+          const double o = __hiloint2double(__builtin_amdgcn_readlane(__double2hiint(sum), g),
+                                            __builtin_amdgcn_readlane(__double2loint(sum), g));
+          before += n > open || (n == open && (o > sum || (o == sum && g < lane))) ? 1 : 0;
+        }
+      } else {  // those with more, or as much and a lower number
+        for (int g = 0; g < a.G; ++g) {
+          const double o = __hiloint2double(__builtin_amdgcn_readlane(__double2hiint(sum), g),
+                                            __builtin_amdgcn_readlane(__double2loint(sum), g));
+          before += o > sum || (o == sum && g < lane) ? 1 : 0;
+        }
       }
       kept = __ballot(lane < a.G && before < a.limit);
 #pragma unroll
