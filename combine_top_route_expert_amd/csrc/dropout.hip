@@ -11,8 +11,8 @@
 // rounded p, so that the expectation is exact.  A counter is the group's number and
 // the call's offset, so the mask depends neither on the dtype nor on the launch.
 //
-// Bound by memory: 16384 rows of 2048 without a residual 25 us, 5.4 TB/s (a copy of 2 GiB: 4.85);
-// 64 rows of 7168 with one 3.1 us, the launch.
+// Bound by memory: 16384 rows of 2048 without a residual 24 us, 5.6 TB/s (a copy of 2 GiB: 4.85);
+// 64 rows of 7168 with one 3.0 us, the launch.
 #include <algorithm>
 
 #include "row_quantizer.h"

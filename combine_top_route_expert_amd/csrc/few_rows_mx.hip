@@ -13,8 +13,8 @@
 // and out is rounded once.
 //
 // One token with 4 experts of H = 2048, I = 1024: few_gate_up 5.4 us, few_down 6.7, of which the
-// 13 MB of weights are 3: latency bounds both.  32 assignments of H = 7168, I = 2048: 99 us and
-// 68, 5.0 and 3.7 TB/s.  Workgroups of 4 waves cost 1 to 10% more.
+// 13 MB of weights are 3: latency bounds both.  16 assignments of H = 7168, I = 2048: 51 us and
+// 36, 4.9 and 3.5 TB/s.  Workgroups of 4 waves cost 1 to 10% more.
 //
 // Sums are in fp32: over a wave's units column by column (few_down: over a unit's), then over
 // the waves (few_down: the slots' units and then the waves), in that order whatever runs

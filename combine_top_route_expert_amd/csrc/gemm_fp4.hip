@@ -91,8 +91,9 @@ __device__ __forceinline__ int weight_block(const MxArgs& g, int nt, int nb, int
 // a wave's weights takes one instruction beside every matrix instruction at four row blocks, four
 // at one.
 //
-// 4096 tokens with 8 of 256 experts of H = 7168, I = 2048: gate_up 1.56 ms, its matrix pipe busy for
-// 71% of them at the 1.85 GHz that the power limit leaves; down 1.00 ms, 54%: 1.13 PFLOP/s together.
+// 4096 tokens with 8 of 256 experts of H = 7168, I = 2048: gate_up 1.56 to 1.64 ms on several cards, its
+// matrix pipe busy for 71% of them at the 1.85 GHz that the power limit leaves; down 1.00 to 1.09 ms,
+// 54%: 1.06 to 1.13 PFLOP/s together.
 // Tiles whose last row block holds a few rows, and prologues and epilogues with one workgroup on a CU,
 // take the rest.
 constexpr int kWaves = 4, kWideFN = 4;  // waves; column blocks of a wave
@@ -391,7 +392,8 @@ __global__ void __launch_bounds__(64 * kWaves, 1) grouped_gemm_mx(MxArgs a) {
 // four stages ahead, and no other wave reads them; only the rows of A, which the waves of a
 // workgroup share, go through LDS, a unit at a time in two buffers with one barrier for it.
 // Of an H = 7168, I = 2048 layer with 64 tokens on 8 of 256 experts (2 rows each) gate_up
-// reads 3.4 GB in 571 us and down 1.7 in 302, 5.9 and 5.6 TB/s (a plain read of such weights: 6.8).
+// reads 3.4 GB in 545 to 571 us and down 1.7 in 285 to 302, 6.1 and 5.9 TB/s on average (a plain read
+// of such weights: 6.8).
 constexpr int kStreamWaves = 4;
 // Rows an expert, on average (dropped ids count as rows: the host does not know them), up to which
 // these products are taken.  That layer in ms, these and the wide ones: 1 row (an expert that has

@@ -1,5 +1,6 @@
-// Tile machinery of the grouped expert GEMMs (gemm_bf16.hip, gemm_i8.hip; gemm_fp4.hip
-// has its own loop and shares the rows, the waits and the bf16 epilogue): the
+// Tile machinery of the grouped expert GEMMs (gemm_bf16.hip, gemm_i8.hip; gemm_fp4.hip has its own
+// loops and shares the rows' layout in LDS, the waits, the bf16 matrix instruction and the bf16
+// epilogue): the
 // copies of A and B stages into LDS and the K loops around the matrix
 // instruction.  Both kernels move K in stages of 128 bytes of a row (64 bf16 or
 // 128 int8 values) and feed 16 bytes of a row per lane to a 32 x 32 matrix
